@@ -26,6 +26,10 @@ LA_DTYPE_F32 = 1
 LA_GATE_LOG = 0
 LA_GATE_SOFTPLUS = 1
 LA_GATE_SIGMOID_BOUND = 2
+LA_GATE_LOGSIGMOID = 3
+LA_ACT_NONE = 0
+LA_ACT_SILU = 1
+LA_ACT_SIGMOID = 2
 
 EXPORTED_SYMBOLS = (
     "gdn_fwd",
@@ -53,6 +57,18 @@ EXPORTED_SYMBOLS = (
     "gdn_fwd_host",
     "la_gdn_fwd_host_staging_bytes",
     "la_gdn_fwd_host_plan",
+    "glr_fwd",
+    "glr_bwd",
+    "glr_decode",
+    "la_glr_checkpoint_rows",
+    "la_glr_workspace_bytes",
+    "gn_fwd",
+    "gn_bwd",
+    "la_gn_bwd_workspace_bytes",
+    "sconv_fwd",
+    "sconv_bwd",
+    "sconv_decode",
+    "la_sconv_bwd_workspace_bytes",
 )
 
 _i64 = ctypes.c_int64
@@ -190,6 +206,17 @@ def load(build_if_missing: bool = True):
         lib.la_gdn_fwd_host_plan.restype = _i32
         lib.la_gdn_fwd_host_plan.argtypes = [_vp, _i32, _i32, _i32, _i64, ctypes.POINTER(_i64), _i32,
                                              ctypes.POINTER(_i64)]
+        for name, params in (("glr_fwd", GlrFwdParams), ("glr_bwd", GlrBwdParams), ("glr_decode", GlrDecodeParams),
+                             ("gn_fwd", GnFwdParams), ("gn_bwd", GnBwdParams), ("sconv_fwd", SconvFwdParams),
+                             ("sconv_bwd", SconvBwdParams), ("sconv_decode", SconvDecodeParams)):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp]
+        for name, args in (("la_glr_checkpoint_rows", [_i64, _i32]),
+                           ("la_glr_workspace_bytes", [_i64, _i32, _i32, _i32, _i32]),
+                           ("la_gn_bwd_workspace_bytes", [_i64, _i32, _i32, _i32]),
+                           ("la_sconv_bwd_workspace_bytes", [_i64, _i32, _i32, _i32])):
+            getattr(lib, name).restype = ctypes.c_size_t
+            getattr(lib, name).argtypes = args
         lib.gdn_fwd_static_workspace.restype = ctypes.c_int
         lib.gdn_fwd_static_workspace.argtypes = [ctypes.POINTER(GdnFwdParams), _vp]
         _lib = lib
@@ -264,6 +291,95 @@ class GdnSummaryBwdParams(ctypes.Structure):
         ("status", _vp),
         ("gate_mode", _i32), ("a_log", _vp), ("dt_bias", _vp), ("gate_lower_bound", ctypes.c_float),
         ("beta_sigmoid", _i32), ("beta_bf16", _i32),
+    ]
+
+
+class GlrFwdParams(ctypes.Structure):
+    """Mirror of la_glr_fwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("g", _vp), ("g_stride_t", _i64), ("cu_seqlens", _vp),
+        ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("T", _i64), ("x_dtype", _i32), ("g_dtype", _i32),
+        ("gate_mode", _i32), ("gate_lower_bound", ctypes.c_float), ("complement_input", _i32),
+        ("initial_state", _vp), ("initial_state_dtype", _i32), ("state_indices", _vp),
+        ("state_pool_size", _i64), ("h", _vp), ("h_stride_t", _i64), ("final_state", _vp),
+        ("checkpoints", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("status", _vp),
+    ]
+
+
+class GlrBwdParams(ctypes.Structure):
+    """Mirror of la_glr_bwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("g", _vp), ("g_stride_t", _i64), ("cu_seqlens", _vp),
+        ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("T", _i64), ("x_dtype", _i32), ("g_dtype", _i32),
+        ("gate_mode", _i32), ("gate_lower_bound", ctypes.c_float), ("complement_input", _i32),
+        ("initial_state", _vp), ("initial_state_dtype", _i32), ("checkpoints", _vp), ("d_h", _vp),
+        ("d_h_stride_t", _i64), ("d_final_state", _vp), ("dx", _vp), ("dx_stride_t", _i64), ("dg", _vp),
+        ("dg_stride_t", _i64), ("d_initial_state", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t), ("status", _vp),
+    ]
+
+
+class GlrDecodeParams(ctypes.Structure):
+    """Mirror of la_glr_decode_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_n", _i64), ("g", _vp), ("g_stride_n", _i64), ("N", _i32), ("D", _i32),
+        ("x_dtype", _i32), ("g_dtype", _i32), ("gate_mode", _i32), ("gate_lower_bound", ctypes.c_float),
+        ("complement_input", _i32), ("state_pool", _vp), ("state_dtype", _i32), ("state_pool_size", _i64),
+        ("state_indices", _vp), ("h", _vp), ("h_stride_n", _i64), ("status", _vp),
+    ]
+
+
+class GnFwdParams(ctypes.Structure):
+    """Mirror of la_gn_fwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("x_stride_h", _i64), ("z", _vp), ("z_stride_t", _i64),
+        ("z_stride_h", _i64), ("weight", _vp), ("bias", _vp), ("T", _i64), ("H", _i32), ("V", _i32),
+        ("x_dtype", _i32), ("weight_dtype", _i32), ("per_head", _i32), ("center", _i32), ("activation", _i32),
+        ("eps", ctypes.c_float), ("y", _vp), ("y_stride_t", _i64), ("y_stride_h", _i64),
+    ]
+
+
+class GnBwdParams(ctypes.Structure):
+    """Mirror of la_gn_bwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("x_stride_h", _i64), ("z", _vp), ("z_stride_t", _i64),
+        ("z_stride_h", _i64), ("weight", _vp), ("bias", _vp), ("dy", _vp), ("dy_stride_t", _i64),
+        ("dy_stride_h", _i64), ("T", _i64), ("H", _i32), ("V", _i32), ("x_dtype", _i32),
+        ("weight_dtype", _i32), ("per_head", _i32), ("center", _i32), ("activation", _i32),
+        ("eps", ctypes.c_float), ("dx", _vp), ("dx_stride_t", _i64), ("dx_stride_h", _i64), ("dz", _vp),
+        ("dz_stride_t", _i64), ("dz_stride_h", _i64), ("d_weight", _vp), ("d_bias", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SconvFwdParams(ctypes.Structure):
+    """Mirror of la_sconv_fwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("weight", _vp), ("bias", _vp), ("cu_seqlens", _vp),
+        ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("W", _i32), ("T", _i64), ("x_dtype", _i32),
+        ("weight_dtype", _i32), ("activation", _i32), ("initial_state", _vp), ("state_indices", _vp),
+        ("state_pool_size", _i64), ("y", _vp), ("y_stride_t", _i64), ("final_state", _vp), ("status", _vp),
+    ]
+
+
+class SconvBwdParams(ctypes.Structure):
+    """Mirror of la_sconv_bwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("weight", _vp), ("bias", _vp), ("cu_seqlens", _vp),
+        ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("W", _i32), ("T", _i64), ("x_dtype", _i32),
+        ("weight_dtype", _i32), ("activation", _i32), ("initial_state", _vp), ("dy", _vp),
+        ("dy_stride_t", _i64), ("d_final_state", _vp), ("dx", _vp), ("dx_stride_t", _i64), ("d_weight", _vp),
+        ("d_bias", _vp), ("d_initial_state", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+        ("status", _vp),
+    ]
+
+
+class SconvDecodeParams(ctypes.Structure):
+    """Mirror of la_sconv_decode_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_n", _i64), ("weight", _vp), ("bias", _vp), ("N", _i32), ("D", _i32),
+        ("W", _i32), ("x_dtype", _i32), ("weight_dtype", _i32), ("activation", _i32), ("state_pool", _vp),
+        ("state_pool_size", _i64), ("state_indices", _vp), ("y", _vp), ("y_stride_n", _i64), ("status", _vp),
     ]
 
 

@@ -1,0 +1,161 @@
+// mixer.cuh -- what the token-mixer operators (glr.cu, gn.cu, sconv.cu) share: element access in
+// bf16 or fp32, activations, the numbering of sequence blocks, and host-side argument checks.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/liblinattn.h"
+
+namespace la {
+namespace mixer {
+
+typedef __nv_bfloat16 bf16;
+
+// ---------------------------------------------------------------- element access
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ bf16 from_f<bf16>(float x) { return __float2bfloat16_rn(x); }
+
+// An element of a bf16 or fp32 array whose type is known at run time (parameters, states).
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int is_bf16) {
+    return is_bf16 ? to_f(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, float x) {
+    if (is_bf16) static_cast<bf16*>(p)[i] = from_f<bf16>(x);
+    else static_cast<float*>(p)[i] = x;
+}
+
+// ---------------------------------------------------------------- activations
+// 1 / (1 + e^-x); e^-x may overflow to infinity, which gives the right 0.
+__device__ __forceinline__ float sigmoidf(float x) { return 1.f / (1.f + expf(-x)); }
+
+__device__ __forceinline__ float act_fwd(int kind, float p) {
+    if (kind == LA_ACT_NONE) return p;
+    const float s = sigmoidf(p);
+    return kind == LA_ACT_SIGMOID ? s : p * s;
+}
+// act(p) and act'(p).  silu' = s (1 + p (1 - s)); sigmoid' = s (1 - s).
+__device__ __forceinline__ float act_grad(int kind, float p, float& d) {
+    if (kind == LA_ACT_NONE) {
+        d = 1.f;
+        return p;
+    }
+    const float s = sigmoidf(p);
+    if (kind == LA_ACT_SIGMOID) {
+        d = s * (1.f - s);
+        return s;
+    }
+    d = s * (1.f + p * (1.f - s));
+    return p * s;
+}
+
+// ---------------------------------------------------------------- sequence blocks
+// The packed batch is cut into blocks of `B` tokens that start at each sequence's own first
+// token, so that what a block computes does not depend on the batch around its sequence.  Block
+// c of sequence i is slot cu[i] / B + i + c: these numbers are all different (a sequence of L
+// tokens from cu[i] on needs at most floor((cu[i] + L) / B) - floor(cu[i] / B) + 1 of them), there
+// are T / B + N slots, each sequence has at least one (an empty one too), and no table is needed.
+struct SeqBlock {
+    int32_t seq;    // -1: the slot holds no block
+    int64_t start;  // first token of the block
+    int32_t count;  // tokens in the block (0 only for the block of an empty sequence)
+    int64_t c;      // block number within the sequence
+    int64_t len;    // tokens in the sequence
+    int64_t first;  // first token of the sequence
+};
+
+__device__ __forceinline__ int64_t cu_load(const void* cu, int cu64, int64_t i) {
+    return cu64 ? static_cast<const int64_t*>(cu)[i] : static_cast<int64_t>(static_cast<const int32_t*>(cu)[i]);
+}
+
+__device__ __forceinline__ void raise_status(int32_t* status, int32_t code) {
+    if (status) atomicCAS(status, LA_OK, code);
+}
+
+// The block in `slot`; called by whole warps.  32-ary search over cu[i] / B + i, one round of loads
+// for up to 32 sequences, two for up to 1024.  With invalid cu_seqlens the answer is some block
+// inside [0, T), so that no access leaves the operands.
+template <int B>
+__device__ __forceinline__ SeqBlock find_block(const void* cu, int cu64, int32_t N, int64_t T, int64_t slot) {
+    const int lane = threadIdx.x & 31;
+    int32_t lo = 0, n = N;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int32_t step = (n + 31) / 32;
+        const int32_t i = lo + lane * step;
+        const bool at_or_before = lane * step < n && cu_load(cu, cu64, i) / B + i <= slot;
+        const unsigned m = __ballot_sync(0xffffffffu, at_or_before);
+        const int k = m ? 31 - __clz(m) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    SeqBlock b;
+    b.seq = -1;
+    b.start = b.c = b.len = b.first = 0;
+    b.count = 0;
+    const int64_t s0 = cu_load(cu, cu64, lo), s1 = cu_load(cu, cu64, lo + 1);
+    if (s0 < 0 || s1 < s0 || s1 > T) return b;
+    const int64_t c = slot - (s0 / B + lo);
+    if (c < 0 || (c > 0 && c * B >= s1 - s0)) return b;
+    b.seq = lo;
+    b.c = c;
+    b.first = s0;
+    b.len = s1 - s0;
+    b.start = s0 + c * B;
+    b.count = static_cast<int32_t>(min(static_cast<int64_t>(B), s1 - b.start));
+    return b;
+}
+
+// Checks entry i of cu_seqlens (0 <= i < N, with its right neighbour and the two ends).
+__device__ __forceinline__ void check_cu(const void* cu, int cu64, int32_t N, int64_t T, int64_t i, int32_t* status) {
+    const int64_t a = cu_load(cu, cu64, i), b = cu_load(cu, cu64, i + 1);
+    if (a < 0 || b < a || b > T || (i == 0 && a != 0) || (i == N - 1 && b != T)) raise_status(status, LA_ERR_BAD_SEQLENS);
+}
+
+// ---------------------------------------------------------------- host checks
+inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool known_dtype(int32_t d) { return d == LA_DTYPE_BF16 || d == LA_DTYPE_F32; }
+inline int dtype_size(int32_t d) { return d == LA_DTYPE_BF16 ? 2 : 4; }
+
+// A [rows, D] operand: non-null when it has elements, element-aligned, rows that an output does not
+// overlap.
+inline bool good_rows(const void* p, int64_t stride, int64_t rows, int64_t D, int32_t dtype, bool out) {
+    if (rows == 0 || D == 0) return true;
+    if (!p || !aligned_to(p, dtype_size(dtype))) return false;
+    if (stride < 0) return false;
+    return !out || rows == 1 || stride >= D;
+}
+// An optional contiguous operand.
+inline bool good_optional(const void* p, int32_t dtype) { return !p || aligned_to(p, dtype_size(dtype)); }
+
+inline la_status check_seqs(const void* cu, int32_t bits, int32_t N, int64_t T) {
+    if (T < 0 || N < 0) return LA_ERR_INVALID_ARG;
+    if (N == 0 && T > 0) return LA_ERR_INVALID_ARG;
+    if (T >= (int64_t(1) << 40)) return LA_ERR_UNSUPPORTED;
+    if (bits != 32 && bits != 64) return LA_ERR_INVALID_ARG;
+    if (!cu || !aligned_to(cu, bits / 8)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+inline la_status check_gate(int32_t mode, float lb) {
+    if (mode == LA_GATE_SOFTPLUS) return LA_ERR_UNSUPPORTED;
+    if (mode == LA_GATE_SIGMOID_BOUND) return (lb < 0.f && std::isfinite(lb)) ? LA_OK : LA_ERR_INVALID_ARG;
+    return (mode == LA_GATE_LOG || mode == LA_GATE_LOGSIGMOID) ? LA_OK : LA_ERR_INVALID_ARG;
+}
+
+inline la_status check_workspace(const void* p, size_t have, size_t need) {
+    if (need == 0) return LA_OK;
+    return (p && have >= need && aligned_to(p, 256)) ? LA_OK : LA_ERR_WORKSPACE;
+}
+
+inline la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
+
+}  // namespace mixer
+}  // namespace la

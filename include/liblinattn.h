@@ -71,8 +71,14 @@ typedef enum la_dtype { LA_DTYPE_BF16 = 0, LA_DTYPE_F32 = 1 } la_dtype;
  *                         softplus(x) = log(1 + e^x) (taken as x above 20).
  *   LA_GATE_SIGMOID_BOUND log decay = gate_lower_bound * sigmoid(g[t,h]), bounded
  *                         below by gate_lower_bound (< 0; PR #616 uses -5 by default).
+ *   LA_GATE_LOGSIGMOID    log decay = log(sigmoid(g)) (the glr_* entry points only).
  */
-typedef enum la_gate_mode { LA_GATE_LOG = 0, LA_GATE_SOFTPLUS = 1, LA_GATE_SIGMOID_BOUND = 2 } la_gate_mode;
+typedef enum la_gate_mode {
+    LA_GATE_LOG = 0,
+    LA_GATE_SOFTPLUS = 1,
+    LA_GATE_SIGMOID_BOUND = 2,
+    LA_GATE_LOGSIGMOID = 3
+} la_gate_mode;
 
 /* Parameters of gdn_fwd.  Strides are in elements. */
 typedef struct la_gdn_fwd_params {
@@ -559,6 +565,247 @@ size_t la_gdn_workspace_bytes(int32_t N, int32_t summary);
    la_gdn_workspace_bytes(N, 0) plus per-chunk tables and one 17408-byte record per
    (chunk, head), at most (T / 64 + N) * HV of them (0.57 GB for T = 65536, N = 8, HV = 32). */
 size_t la_gdn_fwd_split_workspace_bytes(int64_t T, int32_t N, int32_t HV);
+
+/* ===========================================================================
+ * Token-mixer operators around the recurrence: the gated linear recurrence
+ * (glr_*), the per-head group norm with an activation or gate (gn_*) and the
+ * short causal convolution (sconv_*).
+ *
+ * They follow the conventions at the top of this file, with these differences:
+ *   - Operands are bf16 or fp32 as their dtype field says (la_dtype); any
+ *     strides and element-aligned addresses are accepted (16-byte aligned rows
+ *     take wider loads).  Input strides may be 0 (a broadcast operand); output
+ *     rows must not overlap each other or an input.
+ *   - A workspace is always the caller's: LA_ERR_WORKSPACE when it is missing,
+ *     smaller than the matching la_*_workspace_bytes() or not 256-byte aligned
+ *     (a size of 0 needs none).  Its contents need no initialisation.
+ *   - The status word is written only when something is wrong; the caller
+ *     zeroes it.
+ * Sums, states and statistics are fp32; every output is rounded once.
+ * ======================================================================== */
+
+typedef enum la_activation { LA_ACT_NONE = 0, LA_ACT_SILU = 1, LA_ACT_SIGMOID = 2 } la_activation;
+
+/* Parameters of glr_fwd.  Strides are in elements. */
+typedef struct la_glr_fwd_params {
+    const void* x;    int64_t x_stride_t;     /* [T, D] */
+    const void* g;    int64_t g_stride_t;     /* [T, D]: log decay or gate logits (gate_mode) */
+    const void* cu_seqlens;                   /* [N + 1] */
+    int32_t cu_seqlens_bits;                  /* 32 or 64 */
+    int32_t N, D;
+    int64_t T;
+    int32_t x_dtype, g_dtype;                 /* la_dtype of x and h; of g */
+    int32_t gate_mode;                        /* LA_GATE_LOG, LA_GATE_SIGMOID_BOUND or LA_GATE_LOGSIGMOID */
+    float gate_lower_bound;                   /* < 0 (LA_GATE_SIGMOID_BOUND) */
+    int32_t complement_input;                 /* the input enters as (1 - a_t) x_t */
+    const void* initial_state;                /* [N, D] contiguous, or NULL (zeros) */
+    int32_t initial_state_dtype;              /* la_dtype */
+    const int32_t* state_indices;             /* [N] or NULL: initial_state is then a pool, as in gdn_fwd */
+    int64_t state_pool_size;
+    void* h;          int64_t h_stride_t;     /* [T, D] out */
+    float* final_state;                       /* [N, D] out or NULL; NULL with state_indices */
+    float* checkpoints;                       /* [la_glr_checkpoint_rows(T, N), D] out or NULL */
+    void* workspace;  size_t workspace_bytes; /* >= la_glr_workspace_bytes(T, N, D, 0, 0) */
+    int32_t* status;
+} la_glr_fwd_params;
+
+/*
+ * glr_fwd -- the gated linear recurrence: for every sequence and channel
+ *
+ *     h_t = a_t h_{t-1} + m_t x_t,   a_t = exp(log decay of g_t),   m_t = 1 or 1 - a_t,
+ *
+ * the diagonal member of the linear-attention family that gdn_fwd belongs to.
+ * The log decay is expected to be <= 0 (a sequence of growing factors may
+ * overflow).  An empty sequence's final state is its initial state (or zeros).
+ * checkpoints receives the fp32 state entering every 128-token block of every
+ * sequence, for glr_bwd: block c of sequence i is row cu_seqlens[i] / 128 + i + c
+ * (rows in between are left alone).
+ * Batch invariant: blocks start at each sequence's own first token, and the
+ * states combine in a fixed order.
+ */
+la_status glr_fwd(const la_glr_fwd_params* p, void* stream);
+
+/* Parameters of glr_bwd.  Strides are in elements. */
+typedef struct la_glr_bwd_params {
+    const void* x;    int64_t x_stride_t;
+    const void* g;    int64_t g_stride_t;
+    const void* cu_seqlens;
+    int32_t cu_seqlens_bits;
+    int32_t N, D;
+    int64_t T;
+    int32_t x_dtype, g_dtype;                 /* of x, d_h, dx; of g, dg */
+    int32_t gate_mode;
+    float gate_lower_bound;
+    int32_t complement_input;
+    const void* initial_state;                /* as the forward's, or NULL */
+    int32_t initial_state_dtype;
+    const float* checkpoints;                 /* the forward's, or NULL (recomputed) */
+    const void* d_h;  int64_t d_h_stride_t;   /* [T, D] */
+    const float* d_final_state;               /* [N, D] contiguous, or NULL (zeros) */
+    void* dx;         int64_t dx_stride_t;    /* [T, D] out */
+    void* dg;         int64_t dg_stride_t;    /* [T, D] out: gradient of g as given */
+    float* d_initial_state;                   /* [N, D] out or NULL */
+    void* workspace;  size_t workspace_bytes; /* >= la_glr_workspace_bytes(T, N, D, 1, checkpoints != NULL) */
+    int32_t* status;
+} la_glr_bwd_params;
+
+/* glr_bwd -- gradients of L = sum(d_h * h) + sum(d_final_state * final_state). */
+la_status glr_bwd(const la_glr_bwd_params* p, void* stream);
+
+/* Parameters of glr_decode.  Strides are in elements. */
+typedef struct la_glr_decode_params {
+    const void* x;    int64_t x_stride_n;     /* [N, D] */
+    const void* g;    int64_t g_stride_n;     /* [N, D] */
+    int32_t N, D;
+    int32_t x_dtype, g_dtype;
+    int32_t gate_mode;
+    float gate_lower_bound;
+    int32_t complement_input;
+    void* state_pool;                         /* [state_pool_size, D] contiguous, updated in place */
+    int32_t state_dtype;
+    int64_t state_pool_size;
+    const int32_t* state_indices;             /* [N] or NULL: sequence i uses slot i */
+    void* h;          int64_t h_stride_n;     /* [N, D] out */
+    int32_t* status;
+} la_glr_decode_params;
+
+/* glr_decode -- one glr_fwd step per sequence against a state pool (as gdn_decode). */
+la_status glr_decode(const la_glr_decode_params* p, void* stream);
+
+/* Rows of glr_fwd's checkpoints buffer: T / 128 + N (0 for invalid arguments). */
+size_t la_glr_checkpoint_rows(int64_t T, int32_t N);
+
+/* Bytes of device workspace glr_fwd (backward = 0) or glr_bwd (backward = 1) needs. */
+size_t la_glr_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t backward, int32_t checkpoints_given);
+
+/* Parameters of gn_fwd.  Strides are in elements; V is contiguous. */
+typedef struct la_gn_fwd_params {
+    const void* x;    int64_t x_stride_t, x_stride_h;   /* [T, H, V] */
+    const void* z;    int64_t z_stride_t, z_stride_h;   /* [T, H, V] gate, or NULL */
+    const void* weight;                                 /* [V], or [H, V] with per_head, contiguous */
+    const void* bias;                                   /* as weight, or NULL */
+    int64_t T;
+    int32_t H, V;
+    int32_t x_dtype, weight_dtype;                      /* of x, z, y; of weight, bias */
+    int32_t per_head;
+    int32_t center;                                     /* subtract the group's mean (0: RMS only) */
+    int32_t activation;                                 /* la_activation */
+    float eps;                                          /* > 0 */
+    void* y;          int64_t y_stride_t, y_stride_h;   /* [T, H, V] out */
+} la_gn_fwd_params;
+
+/*
+ * gn_fwd -- normalisation of every head's channels of every token (a group norm
+ * with H groups, channels last), with an activation or a gate:
+ *
+ *     n = (x - mu) / sqrt(mean((x - mu)^2) + eps),  mu = mean(x) or 0,  p = n weight + bias,
+ *     y = act(p) without z,   y = p act(z) with z.
+ *
+ * V is at most 8192 (LA_ERR_UNSUPPORTED above).
+ */
+la_status gn_fwd(const la_gn_fwd_params* p, void* stream);
+
+/* Parameters of gn_bwd.  Strides are in elements; V is contiguous. */
+typedef struct la_gn_bwd_params {
+    const void* x;    int64_t x_stride_t, x_stride_h;
+    const void* z;    int64_t z_stride_t, z_stride_h;
+    const void* weight;
+    const void* bias;
+    const void* dy;   int64_t dy_stride_t, dy_stride_h; /* [T, H, V] */
+    int64_t T;
+    int32_t H, V;
+    int32_t x_dtype, weight_dtype;                      /* of x, z, dy, dx, dz; of weight, bias and their gradients */
+    int32_t per_head;
+    int32_t center;
+    int32_t activation;
+    float eps;
+    void* dx;         int64_t dx_stride_t, dx_stride_h; /* [T, H, V] out */
+    void* dz;         int64_t dz_stride_t, dz_stride_h; /* [T, H, V] out; NULL without z */
+    void* d_weight;                                     /* as weight, out */
+    void* d_bias;                                       /* as bias, out; NULL without bias */
+    void* workspace;  size_t workspace_bytes;           /* >= la_gn_bwd_workspace_bytes(T, H, V, per_head) */
+} la_gn_bwd_params;
+
+/* gn_bwd -- gradients of L = sum(dy * y); the statistics are recomputed from x. The sums over
+ * tokens (and heads, for a shared weight) run in an order fixed by the shape. */
+la_status gn_bwd(const la_gn_bwd_params* p, void* stream);
+
+size_t la_gn_bwd_workspace_bytes(int64_t T, int32_t H, int32_t V, int32_t per_head);
+
+/* Parameters of sconv_fwd.  Strides are in elements. */
+typedef struct la_sconv_fwd_params {
+    const void* x;    int64_t x_stride_t;     /* [T, D] */
+    const void* weight;                       /* [D, W] contiguous; weight[d][W - 1] meets the current token */
+    const void* bias;                         /* [D] or NULL */
+    const void* cu_seqlens;
+    int32_t cu_seqlens_bits;
+    int32_t N, D, W;                          /* W 2, 3 or 4 */
+    int64_t T;
+    int32_t x_dtype, weight_dtype;            /* of x, y and the states; of weight and bias */
+    int32_t activation;                       /* la_activation */
+    const void* initial_state;                /* [N, W - 1, D] contiguous, oldest token first, or NULL (zeros) */
+    const int32_t* state_indices;             /* [N] or NULL: initial_state is then a pool [P, W - 1, D] */
+    int64_t state_pool_size;
+    void* y;          int64_t y_stride_t;     /* [T, D] out */
+    void* final_state;                        /* [N, W - 1, D] out or NULL; NULL with state_indices */
+    int32_t* status;
+} la_sconv_fwd_params;
+
+/*
+ * sconv_fwd -- causal depthwise convolution along each sequence with an activation:
+ *
+ *     y_t = act(bias + sum_j weight[:, j] x_{t - (W - 1) + j}),
+ *
+ * tokens before the start being the initial state's rows (zeros without one).  final_state
+ * is the last W - 1 inputs (the initial state's rows shifted along for shorter sequences),
+ * which with state_indices goes back into the sequence's slot.
+ */
+la_status sconv_fwd(const la_sconv_fwd_params* p, void* stream);
+
+/* Parameters of sconv_bwd.  Strides are in elements. */
+typedef struct la_sconv_bwd_params {
+    const void* x;    int64_t x_stride_t;
+    const void* weight;
+    const void* bias;
+    const void* cu_seqlens;
+    int32_t cu_seqlens_bits;
+    int32_t N, D, W;
+    int64_t T;
+    int32_t x_dtype, weight_dtype;
+    int32_t activation;
+    const void* initial_state;                /* as the forward's, or NULL */
+    const void* dy;   int64_t dy_stride_t;    /* [T, D] */
+    const void* d_final_state;                /* [N, W - 1, D] in x's dtype, or NULL (zeros) */
+    void* dx;         int64_t dx_stride_t;    /* [T, D] out */
+    void* d_weight;                           /* [D, W] out, in weight's dtype */
+    void* d_bias;                             /* [D] out; NULL without bias */
+    void* d_initial_state;                    /* [N, W - 1, D] out in x's dtype, or NULL */
+    void* workspace;  size_t workspace_bytes; /* >= la_sconv_bwd_workspace_bytes(T, N, D, W) */
+    int32_t* status;
+} la_sconv_bwd_params;
+
+/* sconv_bwd -- gradients of L = sum(dy * y) + sum(d_final_state * final_state). */
+la_status sconv_bwd(const la_sconv_bwd_params* p, void* stream);
+
+size_t la_sconv_bwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t W);
+
+/* Parameters of sconv_decode.  Strides are in elements. */
+typedef struct la_sconv_decode_params {
+    const void* x;    int64_t x_stride_n;     /* [N, D] */
+    const void* weight;
+    const void* bias;
+    int32_t N, D, W;
+    int32_t x_dtype, weight_dtype;
+    int32_t activation;
+    void* state_pool;                         /* [state_pool_size, W - 1, D] contiguous, in x's dtype, updated in place */
+    int64_t state_pool_size;
+    const int32_t* state_indices;             /* [N] or NULL: sequence i uses slot i */
+    void* y;          int64_t y_stride_n;     /* [N, D] out */
+    int32_t* status;
+} la_sconv_decode_params;
+
+/* sconv_decode -- one sconv_fwd step per sequence against a state pool (as gdn_decode). */
+la_status sconv_decode(const la_sconv_decode_params* p, void* stream);
 
 /*
  * Host helper: total checkpoint rows R = sum_i ceil(L_i / n) for a HOST copy of
