@@ -9,7 +9,21 @@
 //   e_t = dh_t + a_{t+1} e_{t+1},  dx_t = m_t e_t,  dl_t = e_t a_t (h_{t-1} - [m = 1 - a] x_t),
 //   dg_t = dl_t dl/dg,  d(initial) = a_1 e_1.
 //
-// The simplest form: one thread walks one channel of one sequence.
+// Every step is the affine map h -> a h + u, and maps compose, so the time axis is split.  A CTA takes
+// a block of 128 tokens x 64 channels into registers (each thread 8 tokens of 2 channels), composes
+// its warps' maps in shared memory, and needs one number per channel from the block before: the
+// state entering it.  That chain runs through a table in the workspace.  A block publishes its
+// composed map (A, B) as soon as it has it and the state leaving it once it knows the one entering;
+// a block that needs a state looks back over up to 32 predecessors, takes the nearest published
+// state and folds the maps after it in order.  The state leaving a block is always
+// fma(A, entering, B), whoever computes it, so the bits do not depend on what was published when.
+// The launch is cooperative (all CTAs resident), every CTA walks its items in ascending order and
+// items only wait for lower ones, so the lowest unfinished item never waits and the waits end; they
+// are bounded all the same.  Each operand is read once and each result written once.
+//
+// The backward runs the same chain from each sequence's end, over the gradient leaving a token,
+// c_t = a_t (dh_t + c_{t+1}); the states entering its blocks come from the forward's checkpoints (one
+// row per 128 tokens, 1.5 % of the operands' bytes), so it is one pass too.
 #include <algorithm>
 
 #include "mixer.cuh"
@@ -18,8 +32,14 @@ namespace {
 
 using namespace la::mixer;
 
-constexpr int kBlock = 128;    // tokens between saved states
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;                          // decode
+constexpr int kSpan = 8;                               // tokens of a thread
+constexpr int kWarps = 16;                             // of a CTA, one span each
+constexpr int kScanThreads = 32 * kWarps;
+constexpr int kBlock = kSpan * kWarps;                 // tokens of a block, and between saved states
+constexpr int kChannels = 64;                          // of a CTA, two a lane
+constexpr uint64_t kWaitNs = 1000000000ull;            // a bounded wait gives up after a second
+static_assert(kBlock == 128, "the checkpoint cadence of the interface");
 
 // a, m and dl/dg of one gate value.  The log sigmoid's a = s(g) and 1 - a = s(-g) come from
 // e = exp(-|g|) without cancellation; otherwise 1 - a = -expm1(l).
@@ -58,75 +78,446 @@ struct Args {
     int64_t dh_st, dx_st, dg_st;
     float* ds0;
     int32_t* status;
+    int tiles;       // channel tiles
+    int64_t items;   // (T / kBlock + N) * tiles
+    int* flags;      // per item: 1 the map is there, 2 the state leaving it too; null when no sequence has two blocks
+    float4* maps;    // [items][32]: (A, A, B, B) of a lane's two channels
+    float2* states;  // [items][32]
 };
 
-// The tokens [lo, hi) of sequence i, or false (with the status set) when cu_seqlens is invalid.
-__device__ bool sequence(const Args& a, int i, int64_t& lo, int64_t& hi) {
-    lo = cu_load(a.cu, a.cu64, i);
-    hi = cu_load(a.cu, a.cu64, i + 1);
-    if (lo < 0 || hi < lo || hi > a.T || (i == 0 && lo != 0) || (i == a.N - 1 && hi != a.T)) {
-        raise_status(a.status, LA_ERR_BAD_SEQLENS);
-        return false;
+// ---------------------------------------------------------------- asynchronous copies
+// One thread's two channels of one token (4 or 8 bytes) into its own place in shared memory.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "n"(kBytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <typename T>
+struct Pair {
+    T v[2];
+};
+
+// The channels d, d + 1 of one row; kPair: as one 2-element access (D even, everything aligned).
+template <typename T, bool kPair>
+__device__ __forceinline__ void load2(const void* base, int64_t at, int d, int D, float& v0, float& v1) {
+    const T* p = static_cast<const T*>(base) + at + d;
+    if (kPair) {
+        if (sizeof(T) == 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+            v0 = __uint_as_float(w << 16);
+            v1 = __uint_as_float(w & 0xFFFF0000u);
+        } else {
+            const float2 w = *reinterpret_cast<const float2*>(p);
+            v0 = w.x;
+            v1 = w.y;
+        }
+    } else {
+        v0 = to_f(p[0]);
+        v1 = d + 1 < D ? to_f(p[1]) : 0.f;
     }
-    return true;
+}
+template <typename T, bool kPair>
+__device__ __forceinline__ void store2(void* base, int64_t at, int d, int D, float v0, float v1) {
+    T* p = static_cast<T*>(base) + at + d;
+    if (kPair) {
+        if (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v0, v1);
+        else *reinterpret_cast<float2*>(p) = make_float2(v0, v1);
+    } else {
+        p[0] = from_f<T>(v0);
+        if (d + 1 < D) p[1] = from_f<T>(v1);
+    }
+}
+__device__ __forceinline__ void load2_any(const void* base, int64_t at, int d, int D, int is_bf16, float& v0, float& v1) {
+    v0 = d < D ? load_any(base, at + d, is_bf16) : 0.f;
+    v1 = d + 1 < D ? load_any(base, at + d + 1, is_bf16) : 0.f;
+}
+__device__ __forceinline__ void store2_any(void* base, int64_t at, int d, int D, int is_bf16, float v0, float v1) {
+    if (d < D) store_any(base, at + d, is_bf16, v0);
+    if (d + 1 < D) store_any(base, at + d + 1, is_bf16, v1);
 }
 
-template <typename X, typename G>
-__global__ void __launch_bounds__(kThreads) glr_fwd_kernel(const Args a) {
-    const int i = blockIdx.y + gridDim.y * blockIdx.z;
-    const int d = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.N || d >= a.D) return;
-    int64_t lo, hi;
-    if (!sequence(a, i, lo, hi)) return;
-    int64_t slot = i;
-    if (a.idx) {
-        slot = a.idx[i];
-        if (slot < 0 || slot >= a.pool) {
+// ---------------------------------------------------------------- items and the chain between them
+// Item j is block `slot` and channel tile j mod tiles; slots ascend in the forward and descend in the
+// backward, so that the neighbour whose state an item needs is item j - tiles.
+struct Item {
+    int32_t start, count;  // tokens of the block
+    int32_t d;             // first channel
+    int32_t order;         // place in the sequence's chain: 0 needs no neighbour
+    int32_t slot;          // block slot (the checkpoint row)
+    int32_t state;         // row of the initial state
+    bool last, dead;       // end of the chain; nothing to do (no block, or a bad state index)
+};
+
+// By a whole warp.
+template <bool kBackward>
+__device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
+    Item it;
+    const int32_t s = static_cast<int32_t>(j / a.tiles);
+    it.slot = kBackward ? static_cast<int32_t>(a.T / kBlock) + a.N - 1 - s : s;
+    it.d = static_cast<int32_t>(j - static_cast<int64_t>(s) * a.tiles) * kChannels;
+    const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, it.slot);
+    it.start = b.start;
+    it.count = b.count;
+    it.dead = b.seq < 0;
+    const int32_t blocks = max(1, (b.len + kBlock - 1) / kBlock);
+    it.order = kBackward ? blocks - 1 - b.c : b.c;
+    it.last = it.order == blocks - 1;
+    it.state = b.seq;
+    if (!kBackward && a.idx && !it.dead) {
+        it.state = a.idx[b.seq];
+        if (it.state < 0 || it.state >= a.pool) {
             raise_status(a.status, LA_ERR_BAD_STATE_INDEX);
-            return;
+            it.dead = true;
         }
     }
-    float h = a.s0 ? load_any(a.s0, slot * a.D + d, a.s0_bf16) : 0.f;
-    for (int64_t t = lo; t < hi; ++t) {
-        if (a.ckpt && (t - lo) % kBlock == 0) a.ckpt[(lo / kBlock + i + (t - lo) / kBlock) * a.D + d] = h;
-        float dec, m, slope;
-        gate(a.mode, a.lb, a.compl_in, to_f(static_cast<const G*>(a.g)[t * a.g_st + d]), dec, m, slope);
-        h = fmaf(dec, h, m * to_f(static_cast<const X*>(a.x)[t * a.x_st + d]));
-        if (a.h) static_cast<X*>(a.h)[t * a.h_st + d] = from_f<X>(h);
-    }
-    if (a.idx) store_any(const_cast<void*>(a.s0), slot * a.D + d, a.s0_bf16, h);
-    else if (a.fin) a.fin[static_cast<int64_t>(i) * a.D + d] = h;
+    if (it.dead) it.count = 0;
+    if ((threadIdx.x & 31) == 0) *to = it;
+    __syncwarp();
 }
 
-template <typename X, typename G>
-__global__ void __launch_bounds__(kThreads) glr_bwd_kernel(const Args a) {
-    const int i = blockIdx.y + gridDim.y * blockIdx.z;
-    const int d = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.N || d >= a.D) return;
-    int64_t lo, hi;
-    if (!sequence(a, i, lo, hi)) return;
-    float prev[kBlock];
-    float e = a.dfin ? a.dfin[static_cast<int64_t>(i) * a.D + d] : 0.f;  // gradient of h_t from later tokens
-    for (int64_t c = (hi - lo + kBlock - 1) / kBlock - 1; c >= 0; --c) {
-        const int64_t t0 = lo + c * kBlock;
-        const int n = static_cast<int>(min(static_cast<int64_t>(kBlock), hi - t0));
-        float dec, m, slope, h = a.ckpt[(lo / kBlock + i + c) * a.D + d];
-        for (int k = 0; k < n; ++k) {
-            prev[k] = h;
-            gate(a.mode, a.lb, a.compl_in, to_f(static_cast<const G*>(a.g)[(t0 + k) * a.g_st + d]), dec, m, slope);
-            h = fmaf(dec, h, m * to_f(static_cast<const X*>(a.x)[(t0 + k) * a.x_st + d]));
+__device__ __forceinline__ int load_flag(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// Called by a whole warp after its lanes stored what the flag announces.
+__device__ __forceinline__ void publish(int* p, int v) {
+    __threadfence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// The state entering item j, by one warp: the nearest published state among up to 32 predecessors,
+// with the maps published after it folded in order.  A wait over a second gives up (status).
+__device__ __forceinline__ float2 look_back(const Args& a, int64_t j, int32_t order) {
+    const int lane = threadIdx.x & 31;
+    const int n = min(order, 32);
+    uint64_t t0 = 0;
+    int k = -1;
+    for (int spin = 0; k < 0; ++spin) {
+        const int f = lane < n ? load_flag(a.flags + (j - (lane + 1) * static_cast<int64_t>(a.tiles))) : 0;
+        const unsigned state = __ballot_sync(0xffffffffu, f == 2), some = __ballot_sync(0xffffffffu, f != 0);
+        if (state) {
+            const int first = __ffs(state) - 1;
+            const unsigned before = (1u << first) - 1u;
+            if ((some & before) == before) k = first;
         }
-        for (int k = n - 1; k >= 0; --k) {
-            const int64_t t = t0 + k;
-            const float x = to_f(static_cast<const X*>(a.x)[t * a.x_st + d]);
-            gate(a.mode, a.lb, a.compl_in, to_f(static_cast<const G*>(a.g)[t * a.g_st + d]), dec, m, slope);
-            e += to_f(static_cast<const X*>(a.dh)[t * a.dh_st + d]);
-            static_cast<X*>(a.dx)[t * a.dx_st + d] = from_f<X>(m * e);
-            e *= dec;
-            static_cast<G*>(a.dg)[t * a.dg_st + d] = from_f<G>(e * (a.compl_in ? prev[k] - x : prev[k]) * slope);
+        if (k < 0 && (spin & 255) == 255) {
+            uint64_t now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (!t0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > kWaitNs)) {
+                raise_status(a.status, LA_ERR_TIMEOUT);
+                return make_float2(0.f, 0.f);
+            }
         }
     }
-    if (a.ds0) a.ds0[static_cast<int64_t>(i) * a.D + d] = e;
+    __threadfence();
+    __syncwarp();
+    float2 h = __ldcg(a.states + (j - (k + 1) * static_cast<int64_t>(a.tiles)) * 32 + lane);
+#pragma unroll 4
+    for (int i = k - 1; i >= 0; --i) {
+        const float4 m = __ldcg(a.maps + (j - (i + 1) * static_cast<int64_t>(a.tiles)) * 32 + lane);
+        h.x = fmaf(m.x, h.x, m.z);
+        h.y = fmaf(m.y, h.y, m.w);
+    }
+    return h;
+}
+
+// One warp: publishes the item's map, finds the entering state (`start` when the chain begins here),
+// publishes the leaving one.
+__device__ __forceinline__ void chain(const Args& a, int64_t j, const Item& it, float4 map, float2& in, float2& out) {
+    const int lane = threadIdx.x & 31;
+    if (it.dead) {
+        if (a.flags) publish(a.flags + j, 2);
+        return;
+    }
+    if (it.order > 0) {
+        if (!it.last) {
+            __stcg(a.maps + j * 32 + lane, map);
+            publish(a.flags + j, 1);
+        }
+        in = look_back(a, j, it.order);
+    }
+    out = make_float2(fmaf(map.x, in.x, map.z), fmaf(map.y, in.y, map.w));
+    if (a.flags && !it.last) {
+        __stcg(a.states + j * 32 + lane, out);
+        publish(a.flags + j, 2);
+    }
+}
+
+__device__ __forceinline__ void check_boundaries(const Args& a) {
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kScanThreads) + threadIdx.x; i < a.N;
+         i += static_cast<int64_t>(gridDim.x) * kScanThreads)
+        check_cu(a.cu, a.cu64, a.N, a.T, i, a.status);
+}
+
+// Shared memory: one staging place per thread, token and operand, then the warps' maps.
+template <typename X, typename G, int kX>
+constexpr size_t stage_bytes() { return static_cast<size_t>(kScanThreads) * kSpan * (kX * sizeof(Pair<X>) + sizeof(Pair<G>)); }
+
+template <typename X, typename G, bool kPair>
+__global__ void __launch_bounds__(kScanThreads, 2) glr_fwd_kernel(const Args a) {
+    extern __shared__ __align__(16) uint8_t stage[];
+    __shared__ float4 maps[kWarps][32];
+    __shared__ float2 enter[kWarps][32];
+    Pair<X>* sx = reinterpret_cast<Pair<X>*>(stage) + threadIdx.x;
+    Pair<G>* sg = reinterpret_cast<Pair<G>*>(stage + static_cast<size_t>(kScanThreads) * kSpan * sizeof(Pair<X>)) + threadIdx.x;
+    __shared__ Item items[2];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    check_boundaries(a);
+
+    auto fetch = [&](const Item& it) {
+        const int d = it.d + 2 * lane, n = d < a.D ? it.count - w * kSpan : 0;
+        const int64_t t = it.start + w * kSpan;
+#pragma unroll
+        for (int k = 0; k < kSpan; ++k)
+            if (k < n) {
+                copy_async<sizeof(Pair<X>)>(sx + k * kScanThreads, static_cast<const X*>(a.x) + (t + k) * a.x_st + d);
+                copy_async<sizeof(Pair<G>)>(sg + k * kScanThreads, static_cast<const G*>(a.g) + (t + k) * a.g_st + d);
+            }
+        copies_commit();
+    };
+
+    int64_t j = blockIdx.x;
+    if (w == 0) locate<false>(a, j, &items[0]);
+    __syncthreads();
+    if (kPair) fetch(items[0]);
+    for (int at = 0;; at ^= 1) {
+        const Item& it = items[at];
+        const int64_t jn = j + gridDim.x;
+        // the next item, while this one's operands arrive; nobody reads its place any more
+        if (w == kWarps - 1 && jn < a.items) locate<false>(a, jn, &items[at ^ 1]);
+        const int ch = it.d + 2 * lane;  // this lane's first channel
+        const int n = ch < a.D ? it.count - w * kSpan : 0;
+        const int64_t t = it.start + w * kSpan;
+        float dec[kSpan][2], u[kSpan][2];
+        if (kPair) copies_wait();
+        float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kSpan; ++k) {
+            dec[k][0] = dec[k][1] = 1.f;
+            u[k][0] = u[k][1] = 0.f;
+            if (k < n) {
+                float x0, x1, g0, g1, m0, m1, slope;
+                if (kPair) {
+                    load2<X, true>(sx + k * kScanThreads, 0, 0, 2, x0, x1);
+                    load2<G, true>(sg + k * kScanThreads, 0, 0, 2, g0, g1);
+                } else {
+                    load2<X, false>(a.x, (t + k) * a.x_st, ch, a.D, x0, x1);
+                    load2<G, false>(a.g, (t + k) * a.g_st, ch, a.D, g0, g1);
+                }
+                gate(a.mode, a.lb, a.compl_in, g0, dec[k][0], m0, slope);
+                gate(a.mode, a.lb, a.compl_in, g1, dec[k][1], m1, slope);
+                u[k][0] = m0 * x0;
+                u[k][1] = m1 * x1;
+                map.z = fmaf(dec[k][0], map.z, u[k][0]);
+                map.w = fmaf(dec[k][1], map.w, u[k][1]);
+                map.x *= dec[k][0];
+                map.y *= dec[k][1];
+            }
+        }
+        maps[w][lane] = map;
+        __syncthreads();
+        if (kPair && jn < a.items) fetch(items[at ^ 1]);
+        if (w == 0) {
+            float2 in = make_float2(0.f, 0.f), out = in;
+            if (it.order == 0 && !it.dead && a.s0) load2_any(a.s0, it.state * static_cast<int64_t>(a.D), ch, a.D, a.s0_bf16, in.x, in.y);
+            map = maps[0][lane];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) {
+                const float4 q = maps[i][lane];
+                map.z = fmaf(q.x, map.z, q.z);
+                map.w = fmaf(q.y, map.w, q.w);
+                map.x *= q.x;
+                map.y *= q.y;
+            }
+            chain(a, j, it, map, in, out);
+            if (!it.dead) {
+                if (a.ckpt && it.count > 0) store2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), ch, a.D, 0, in.x, in.y);
+                if (it.last) {
+                    if (a.idx) store2_any(const_cast<void*>(a.s0), it.state * static_cast<int64_t>(a.D), ch, a.D, a.s0_bf16, out.x, out.y);
+                    else if (a.fin) store2_any(a.fin, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, out.x, out.y);
+                }
+            }
+            enter[0][lane] = in;
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) {
+                const float4 q = maps[i - 1][lane];
+                in.x = fmaf(q.x, in.x, q.z);
+                in.y = fmaf(q.y, in.y, q.w);
+                enter[i][lane] = in;
+            }
+        }
+        __syncthreads();
+        if (a.h) {
+            float2 h = enter[w][lane];
+#pragma unroll
+            for (int k = 0; k < kSpan; ++k)
+                if (k < n) {
+                    h.x = fmaf(dec[k][0], h.x, u[k][0]);
+                    h.y = fmaf(dec[k][1], h.y, u[k][1]);
+                    store2<X, kPair>(a.h, (t + k) * a.h_st, ch, a.D, h.x, h.y);
+                }
+        }
+        if (jn >= a.items) break;
+        j = jn;
+    }
+}
+
+// kPlain: log decay without the complement, where m = dl/dg = 1.
+template <typename X, typename G, bool kPair, bool kPlain>
+__global__ void __launch_bounds__(kScanThreads, 1) glr_bwd_kernel(const Args a) {
+    extern __shared__ __align__(16) uint8_t stage[];
+    __shared__ float4 maps[kWarps][32];   // (a, a, u, u) of the states
+    __shared__ float2 grads[kWarps][32];  // the constant part of the gradients' map
+    __shared__ float2 enter[kWarps][32], leave[kWarps][32];
+    constexpr size_t kPlane = static_cast<size_t>(kScanThreads) * kSpan;
+    Pair<X>* sx = reinterpret_cast<Pair<X>*>(stage) + threadIdx.x;
+    Pair<X>* sd = sx + kPlane;
+    Pair<G>* sg = reinterpret_cast<Pair<G>*>(stage + 2 * kPlane * sizeof(Pair<X>)) + threadIdx.x;
+    __shared__ Item items[2];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    check_boundaries(a);
+
+    auto fetch = [&](const Item& it) {
+        const int d = it.d + 2 * lane, n = d < a.D ? it.count - w * kSpan : 0;
+        const int64_t t = it.start + w * kSpan;
+#pragma unroll
+        for (int k = 0; k < kSpan; ++k)
+            if (k < n) {
+                copy_async<sizeof(Pair<X>)>(sx + k * kScanThreads, static_cast<const X*>(a.x) + (t + k) * a.x_st + d);
+                copy_async<sizeof(Pair<X>)>(sd + k * kScanThreads, static_cast<const X*>(a.dh) + (t + k) * a.dh_st + d);
+                copy_async<sizeof(Pair<G>)>(sg + k * kScanThreads, static_cast<const G*>(a.g) + (t + k) * a.g_st + d);
+            }
+        copies_commit();
+    };
+
+    int64_t j = blockIdx.x;
+    if (w == 0) locate<true>(a, j, &items[0]);
+    __syncthreads();
+    if (kPair) fetch(items[0]);
+    for (int at = 0;; at ^= 1) {
+        const Item& it = items[at];
+        const int64_t jn = j + gridDim.x;
+        // the next item, while this one's operands arrive; nobody reads its place any more
+        if (w == kWarps - 1 && jn < a.items) locate<true>(a, jn, &items[at ^ 1]);
+        const int ch = it.d + 2 * lane;  // this lane's first channel
+        const int n = ch < a.D ? it.count - w * kSpan : 0;
+        const int64_t t = it.start + w * kSpan;
+        float dec[kSpan][2], u[kSpan][2], d[kSpan][2], x[kSpan][2], m[kSpan][2], slope[kSpan][2];
+        if (kPair) copies_wait();
+        float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kSpan; ++k) {
+            dec[k][0] = dec[k][1] = 1.f;
+            u[k][0] = u[k][1] = d[k][0] = d[k][1] = 0.f;
+            if (k < n) {
+                float g0, g1;
+                if (kPair) {
+                    load2<X, true>(sx + k * kScanThreads, 0, 0, 2, x[k][0], x[k][1]);
+                    load2<X, true>(sd + k * kScanThreads, 0, 0, 2, d[k][0], d[k][1]);
+                    load2<G, true>(sg + k * kScanThreads, 0, 0, 2, g0, g1);
+                } else {
+                    load2<X, false>(a.x, (t + k) * a.x_st, ch, a.D, x[k][0], x[k][1]);
+                    load2<X, false>(a.dh, (t + k) * a.dh_st, ch, a.D, d[k][0], d[k][1]);
+                    load2<G, false>(a.g, (t + k) * a.g_st, ch, a.D, g0, g1);
+                }
+                if (kPlain) {
+                    dec[k][0] = expf(g0);
+                    dec[k][1] = expf(g1);
+                    u[k][0] = x[k][0];
+                    u[k][1] = x[k][1];
+                } else {
+                    gate(a.mode, a.lb, a.compl_in, g0, dec[k][0], m[k][0], slope[k][0]);
+                    gate(a.mode, a.lb, a.compl_in, g1, dec[k][1], m[k][1], slope[k][1]);
+                    u[k][0] = m[k][0] * x[k][0];
+                    u[k][1] = m[k][1] * x[k][1];
+                }
+                map.z = fmaf(dec[k][0], map.z, u[k][0]);
+                map.w = fmaf(dec[k][1], map.w, u[k][1]);
+                map.x *= dec[k][0];
+                map.y *= dec[k][1];
+            }
+        }
+        float2 c = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = kSpan - 1; k >= 0; --k) {
+            c.x = dec[k][0] * (d[k][0] + c.x);
+            c.y = dec[k][1] * (d[k][1] + c.y);
+        }
+        maps[w][lane] = map;
+        grads[w][lane] = c;
+        __syncthreads();
+        if (kPair && jn < a.items) fetch(items[at ^ 1]);
+        if (w == 0) {
+            float2 in = make_float2(0.f, 0.f), out = in;
+            if (it.order == 0 && !it.dead && a.dfin) load2_any(a.dfin, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, in.x, in.y);
+            map = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = kWarps - 1; i >= 0; --i) {
+                const float4 q = maps[i][lane];
+                const float2 e = grads[i][lane];
+                map.z = fmaf(q.x, map.z, e.x);
+                map.w = fmaf(q.y, map.w, e.y);
+                map.x *= q.x;
+                map.y *= q.y;
+            }
+            chain(a, j, it, map, in, out);
+            if (it.last && !it.dead && a.ds0) store2_any(a.ds0, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, out.x, out.y);
+#pragma unroll
+            for (int i = kWarps - 1; i >= 0; --i) {
+                leave[i][lane] = in;
+                const float4 q = maps[i][lane];
+                const float2 e = grads[i][lane];
+                in.x = fmaf(q.x, in.x, e.x);
+                in.y = fmaf(q.y, in.y, e.y);
+            }
+        } else if (w == 1) {
+            float2 h = make_float2(0.f, 0.f);
+            if (it.count > 0) load2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), ch, a.D, 0, h.x, h.y);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                enter[i][lane] = h;
+                const float4 q = maps[i][lane];
+                h.x = fmaf(q.x, h.x, q.z);
+                h.y = fmaf(q.y, h.y, q.w);
+            }
+        }
+        __syncthreads();
+        float2 h = enter[w][lane];
+#pragma unroll
+        for (int k = 0; k < kSpan; ++k) {  // u becomes h_{t-1}
+            const float u0 = u[k][0], u1 = u[k][1];
+            u[k][0] = h.x;
+            u[k][1] = h.y;
+            h.x = fmaf(dec[k][0], h.x, u0);
+            h.y = fmaf(dec[k][1], h.y, u1);
+        }
+        float2 e = leave[w][lane];
+#pragma unroll
+        for (int k = kSpan - 1; k >= 0; --k) {
+            if (k >= n) continue;
+            e.x += d[k][0];
+            e.y += d[k][1];
+            if (kPlain) store2<X, kPair>(a.dx, (t + k) * a.dx_st, ch, a.D, e.x, e.y);
+            else store2<X, kPair>(a.dx, (t + k) * a.dx_st, ch, a.D, m[k][0] * e.x, m[k][1] * e.y);
+            e.x *= dec[k][0];
+            e.y *= dec[k][1];
+            if (kPlain) {
+                store2<G, kPair>(a.dg, (t + k) * a.dg_st, ch, a.D, e.x * u[k][0], e.y * u[k][1]);
+            } else {
+                const float p0 = a.compl_in ? u[k][0] - x[k][0] : u[k][0], p1 = a.compl_in ? u[k][1] - x[k][1] : u[k][1];
+                store2<G, kPair>(a.dg, (t + k) * a.dg_st, ch, a.D, e.x * p0 * slope[k][0], e.y * p1 * slope[k][1]);
+            }
+        }
+        if (jn >= a.items) break;
+        j = jn;
+    }
 }
 
 template <typename X, typename G>
@@ -149,22 +540,82 @@ __global__ void __launch_bounds__(kThreads) glr_decode_kernel(const Args a) {
     static_cast<X*>(a.h)[i * a.h_st + d] = from_f<X>(h);
 }
 
-enum Which { kFwd, kBwd, kDecode };
-
-template <typename X, typename G>
-la_status launch(const Args& a, Which w, cudaStream_t s) {
-    if (a.N == 0 || a.D == 0) return LA_OK;
-    const unsigned ny = std::min(a.N, 65535), nz = (a.N + ny - 1) / ny;
-    const dim3 grid((a.D + kThreads - 1) / kThreads, ny, nz);
-    if (w == kFwd) glr_fwd_kernel<X, G><<<grid, kThreads, 0, s>>>(a);
-    else if (w == kBwd) glr_bwd_kernel<X, G><<<grid, kThreads, 0, s>>>(a);
-    else glr_decode_kernel<X, G><<<grid, kThreads, 0, s>>>(a);
-    return launched();
+template <typename K>
+la_status launch_scan(K kernel, size_t smem, Args& a, cudaStream_t s) {
+    int dev = 0, sms = 0, per_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kScanThreads, smem) != cudaSuccess || per_sm < 1) {
+        (void)cudaGetLastError();
+        return LA_ERR_CUDA;
+    }
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.items, static_cast<int64_t>(sms) * per_sm));
+    void* args[] = {&a};
+    if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kScanThreads), args, smem, s) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LA_ERR_CUDA;
+    }
+    return LA_OK;
 }
 
-la_status dispatch(const Args& a, int32_t xd, int32_t gd, Which w, cudaStream_t s) {
-    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? launch<bf16, bf16>(a, w, s) : launch<bf16, float>(a, w, s);
-    return gd == LA_DTYPE_BF16 ? launch<float, bf16>(a, w, s) : launch<float, float>(a, w, s);
+// Whether every row of the operand starts on a boundary of two of its elements.
+bool pairs(const void* p, int64_t stride, int64_t T, int32_t dtype) {
+    return aligned_to(p, 2 * dtype_size(dtype)) && (T == 1 || stride % 2 == 0);
+}
+
+enum Which { kFwd, kBwd };
+
+template <typename X, typename G>
+la_status scan(Args& a, Which w, bool pair, cudaStream_t s) {
+    if (w == kFwd) {
+        const size_t smem = pair ? stage_bytes<X, G, 1>() : 0;
+        return pair ? launch_scan(glr_fwd_kernel<X, G, true>, smem, a, s) : launch_scan(glr_fwd_kernel<X, G, false>, smem, a, s);
+    }
+    const size_t smem = pair ? stage_bytes<X, G, 2>() : 0;
+    const bool plain = a.mode == LA_GATE_LOG && !a.compl_in;
+    if (pair) return plain ? launch_scan(glr_bwd_kernel<X, G, true, true>, smem, a, s) : launch_scan(glr_bwd_kernel<X, G, true, false>, smem, a, s);
+    return plain ? launch_scan(glr_bwd_kernel<X, G, false, true>, smem, a, s) : launch_scan(glr_bwd_kernel<X, G, false, false>, smem, a, s);
+}
+
+// The chain's table: flags, maps and states of every item.  None when no sequence can have two blocks.
+struct Table {
+    size_t maps, states, total;
+};
+Table table(int64_t T, int32_t N, int32_t D) {
+    Table t = {0, 0, 0};
+    if (T <= kBlock) return t;
+    const size_t items = static_cast<size_t>(T / kBlock + N) * ((D + kChannels - 1) / kChannels);
+    t.maps = (items * sizeof(int) + 255) & ~size_t(255);
+    t.states = t.maps + items * 32 * sizeof(float4);
+    t.total = t.states + items * 32 * sizeof(float2);
+    return t;
+}
+
+la_status run_scan(Args& a, int32_t xd, int32_t gd, Which w, void* ws, cudaStream_t s) {
+    if (a.N == 0) return LA_OK;
+    a.tiles = (a.D + kChannels - 1) / kChannels;
+    a.items = (a.T / kBlock + a.N) * a.tiles;
+    if (a.items >= (int64_t(1) << 31)) return LA_ERR_UNSUPPORTED;
+    const Table t = table(a.T, a.N, a.D);
+    if (t.total) {
+        uint8_t* p = static_cast<uint8_t*>(ws);
+        a.flags = reinterpret_cast<int*>(p);
+        a.maps = reinterpret_cast<float4*>(p + t.maps);
+        a.states = reinterpret_cast<float2*>(p + t.states);
+        if (cudaMemsetAsync(a.flags, 0, static_cast<size_t>(a.items) * sizeof(int), s) != cudaSuccess) return LA_ERR_CUDA;
+    }
+    bool pair = a.D % 2 == 0 && pairs(a.x, a.x_st, a.T, xd) && pairs(a.g, a.g_st, a.T, gd);
+    if (w == kFwd) pair = pair && (!a.h || pairs(a.h, a.h_st, a.T, xd));
+    else pair = pair && pairs(a.dh, a.dh_st, a.T, xd) && pairs(a.dx, a.dx_st, a.T, xd) && pairs(a.dg, a.dg_st, a.T, gd);
+    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? scan<bf16, bf16>(a, w, pair, s) : scan<bf16, float>(a, w, pair, s);
+    return gd == LA_DTYPE_BF16 ? scan<float, bf16>(a, w, pair, s) : scan<float, float>(a, w, pair, s);
+}
+
+template <typename X, typename G>
+la_status launch_decode(const Args& a, cudaStream_t s) {
+    const unsigned ny = std::min(a.N, 65535), nz = (a.N + ny - 1) / ny;
+    glr_decode_kernel<X, G><<<dim3((a.D + kThreads - 1) / kThreads, ny, nz), kThreads, 0, s>>>(a);
+    return launched();
 }
 
 }  // namespace
@@ -176,8 +627,9 @@ size_t la_glr_checkpoint_rows(int64_t T, int32_t N) {
 }
 
 size_t la_glr_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t backward, int32_t checkpoints_given) {
-    if (T < 0 || N < 0 || D < 0 || !backward || checkpoints_given) return 0;
-    return (la_glr_checkpoint_rows(T, N) * D * 4 + 255) & ~size_t(255);
+    if (T < 0 || N < 0 || D <= 0) return 0;
+    const size_t states = backward && !checkpoints_given ? (la_glr_checkpoint_rows(T, N) * D * 4 + 255) & ~size_t(255) : 0;
+    return states + table(T, N, D).total;
 }
 
 la_status glr_fwd(const la_glr_fwd_params* p, void* stream) {
@@ -204,7 +656,7 @@ la_status glr_fwd(const la_glr_fwd_params* p, void* stream) {
     a.idx = p->state_indices; a.pool = p->state_pool_size;
     a.h = p->h; a.h_st = p->h_stride_t; a.fin = p->final_state; a.ckpt = p->checkpoints;
     a.status = p->status;
-    return dispatch(a, p->x_dtype, p->g_dtype, kFwd, static_cast<cudaStream_t>(stream));
+    return run_scan(a, p->x_dtype, p->g_dtype, kFwd, p->workspace, static_cast<cudaStream_t>(stream));
 }
 
 la_status glr_bwd(const la_glr_bwd_params* p, void* stream) {
@@ -234,11 +686,12 @@ la_status glr_bwd(const la_glr_bwd_params* p, void* stream) {
     a.status = p->status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.ckpt = const_cast<float*>(p->checkpoints);
-    if (!a.ckpt) {  // the forward again, for the states entering every block
-        a.ckpt = static_cast<float*>(p->workspace);
-        if ((st = dispatch(a, p->x_dtype, p->g_dtype, kFwd, s)) != LA_OK) return st;
+    if (!a.ckpt && a.N > 0) {  // the forward again, for the states entering every block, which come after the table
+        Args f = a;
+        f.ckpt = a.ckpt = reinterpret_cast<float*>(static_cast<uint8_t*>(p->workspace) + ((table(a.T, a.N, a.D).total + 255) & ~size_t(255)));
+        if ((st = run_scan(f, p->x_dtype, p->g_dtype, kFwd, p->workspace, s)) != LA_OK) return st;
     }
-    return dispatch(a, p->x_dtype, p->g_dtype, kBwd, s);
+    return run_scan(a, p->x_dtype, p->g_dtype, kBwd, p->workspace, s);
 }
 
 la_status glr_decode(const la_glr_decode_params* p, void* stream) {
@@ -260,7 +713,10 @@ la_status glr_decode(const la_glr_decode_params* p, void* stream) {
     a.idx = p->state_indices; a.pool = p->state_pool_size;
     a.h = p->h; a.h_st = p->h_stride_n;
     a.status = p->status;
-    return dispatch(a, p->x_dtype, p->g_dtype, kDecode, static_cast<cudaStream_t>(stream));
+    if (a.N == 0) return LA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p->x_dtype == LA_DTYPE_BF16) return p->g_dtype == LA_DTYPE_BF16 ? launch_decode<bf16, bf16>(a, s) : launch_decode<bf16, float>(a, s);
+    return p->g_dtype == LA_DTYPE_BF16 ? launch_decode<float, bf16>(a, s) : launch_decode<float, float>(a, s);
 }
 
 }  // extern "C"

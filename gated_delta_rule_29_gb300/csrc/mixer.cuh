@@ -65,11 +65,11 @@ __device__ __forceinline__ float act_grad(int kind, float p, float& d) {
 // are T / B + N slots, each sequence has at least one (an empty one too), and no table is needed.
 struct SeqBlock {
     int32_t seq;    // -1: the slot holds no block
-    int64_t start;  // first token of the block
+    int32_t start;  // first token of the block
     int32_t count;  // tokens in the block (0 only for the block of an empty sequence)
-    int64_t c;      // block number within the sequence
-    int64_t len;    // tokens in the sequence
-    int64_t first;  // first token of the sequence
+    int32_t c;      // block number within the sequence
+    int32_t len;    // tokens in the sequence
+    int32_t first;  // first token of the sequence
 };
 
 __device__ __forceinline__ int64_t cu_load(const void* cu, int cu64, int64_t i) {
@@ -105,11 +105,11 @@ __device__ __forceinline__ SeqBlock find_block(const void* cu, int cu64, int32_t
     const int64_t c = slot - (s0 / B + lo);
     if (c < 0 || (c > 0 && c * B >= s1 - s0)) return b;
     b.seq = lo;
-    b.c = c;
-    b.first = s0;
-    b.len = s1 - s0;
-    b.start = s0 + c * B;
-    b.count = static_cast<int32_t>(min(static_cast<int64_t>(B), s1 - b.start));
+    b.c = static_cast<int32_t>(c);
+    b.first = static_cast<int32_t>(s0);
+    b.len = static_cast<int32_t>(s1 - s0);
+    b.start = static_cast<int32_t>(s0 + c * B);
+    b.count = min(B, b.first + b.len - b.start);
     return b;
 }
 
@@ -138,7 +138,7 @@ inline bool good_optional(const void* p, int32_t dtype) { return !p || aligned_t
 inline la_status check_seqs(const void* cu, int32_t bits, int32_t N, int64_t T) {
     if (T < 0 || N < 0) return LA_ERR_INVALID_ARG;
     if (N == 0 && T > 0) return LA_ERR_INVALID_ARG;
-    if (T >= (int64_t(1) << 40)) return LA_ERR_UNSUPPORTED;
+    if (T >= (int64_t(1) << 31) - 1024) return LA_ERR_UNSUPPORTED;  // tokens are numbered in 32 bits
     if (bits != 32 && bits != 64) return LA_ERR_INVALID_ARG;
     if (!cu || !aligned_to(cu, bits / 8)) return LA_ERR_INVALID_ARG;
     return LA_OK;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a) {
     for (int j = 0; j < W; ++j) w[j] = load_any(a.w, static_cast<int64_t>(d) * W + j, a.w_bf16);
     const float bias = a.b ? load_any(a.b, d, a.w_bf16) : 0.f;
     const int k0 = warp * kSpan, k1 = min(k0 + kSpan, b.count);
-    const int64_t p0 = b.c * kBlock;
+    const int64_t p0 = static_cast<int64_t>(b.c) * kBlock;
     if (k0 < k1) {
 #pragma unroll
         for (int j = 1; j < W; ++j) win[j] = input_at<X, W>(a, b.first, slot, p0 + k0 - W + j, d);
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a) {
             float p = bias;
 #pragma unroll
             for (int j = 0; j < W; ++j) p = fmaf(w[j], win[j], p);
-            static_cast<X*>(a.y)[(b.start + k) * a.y_st + d] = from_f<X>(act_fwd(a.act, p));
+            static_cast<X*>(a.y)[(static_cast<int64_t>(b.start) + k) * a.y_st + d] = from_f<X>(act_fwd(a.act, p));
         }
     }
     // The sequence's last W - 1 inputs.  With a pool they replace the rows that the sequence started
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j] = 0.f;
     const int k0 = warp * kSpan, k1 = min(k0 + kSpan, b.count);
-    const int64_t p0 = b.c * kBlock;
+    const int64_t p0 = static_cast<int64_t>(b.c) * kBlock;
     if (b.seq >= 0 && d < a.D && k0 < k1) {
         float w[W], win[W], dp[W];
 #pragma unroll
