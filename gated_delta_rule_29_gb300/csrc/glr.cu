@@ -78,11 +78,10 @@ struct Args {
     int64_t dh_st, dx_st, dg_st;
     float* ds0;
     int32_t* status;
-    int tiles;       // channel tiles
-    int64_t items;   // (T / kBlock + N) * tiles
-    int* flags;      // per item: 1 the map is there, 2 the state leaving it too; null when no sequence has two blocks
-    float4* maps;    // [items][32]: (A, A, B, B) of a lane's two channels
-    float2* states;  // [items][32]
+    int tiles;         // channel tiles
+    int64_t items;     // (T / kBlock + N) * tiles
+    ulonglong2* maps;  // [items][32]: (A, B) of a lane's two channels; null when no sequence has two blocks
+    uint2* states;     // [items][32]: the states leaving the item
 };
 
 // ---------------------------------------------------------------- asynchronous copies
@@ -179,75 +178,113 @@ __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
     __syncwarp();
 }
 
-__device__ __forceinline__ int load_flag(const int* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+// The chain's words carry their own readiness, so that neither side needs a fence: a map (A, B) is one
+// 64-bit word and a state one 32-bit word, each written by a single store (16-byte and 8-byte vectors
+// hold a lane's two channels, every element of its own).  The table starts as all ones, a NaN that
+// `settled` keeps out of what is published.
+constexpr uint32_t kUnset = 0xFFFFFFFFu;
+__device__ __forceinline__ float settled(float x) { return __float_as_uint(x) == kUnset ? __uint_as_float(0x7FC00000u) : x; }
+
+__device__ __forceinline__ uint2 load_state(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
     return v;
 }
-// Called by a whole warp after its lanes stored what the flag announces.
-__device__ __forceinline__ void publish(int* p, int v) {
-    __threadfence();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ ulonglong2 load_map(const ulonglong2* p) {
+    ulonglong2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void publish_state(uint2* p, float2 v) {
+    asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(__float_as_uint(settled(v.x))),
+                 "r"(__float_as_uint(settled(v.y)))
+                 : "memory");
+}
+__device__ __forceinline__ unsigned long long word(float a, float b) {
+    return static_cast<unsigned long long>(__float_as_uint(settled(a))) |
+           (static_cast<unsigned long long>(__float_as_uint(b)) << 32);
+}
+__device__ __forceinline__ void publish_map(ulonglong2* p, float4 m) {
+    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word(m.x, m.z)), "l"(word(m.y, m.w)) : "memory");
 }
 
-// The state entering item j, by one warp: the nearest published state among up to 32 predecessors,
-// with the maps published after it folded in order.  A wait over a second gives up (status).
+// The state entering item j for this lane's two channels: the nearest published state among up to
+// kWindow predecessors that only published maps lie after, with those maps folded in order.  The
+// window's words are read together.  A wait over a second gives up (status).
+constexpr int kWindow = 32, kBatch = 4;
 __device__ __forceinline__ float2 look_back(const Args& a, int64_t j, int32_t order) {
     const int lane = threadIdx.x & 31;
-    const int n = min(order, 32);
+    const int n = min(order, kWindow);
+    const int64_t stride = static_cast<int64_t>(a.tiles) * 32;
+    const uint2* states = a.states + (j - a.tiles) * 32 + lane;      // the predecessor's, and back from it
+    const ulonglong2* maps = a.maps + (j - a.tiles) * 32 + lane;
     uint64_t t0 = 0;
-    int k = -1;
-    for (int spin = 0; k < 0; ++spin) {
-        const int f = lane < n ? load_flag(a.flags + (j - (lane + 1) * static_cast<int64_t>(a.tiles))) : 0;
-        const unsigned state = __ballot_sync(0xffffffffu, f == 2), some = __ballot_sync(0xffffffffu, f != 0);
-        if (state) {
-            const int first = __ffs(state) - 1;
-            const unsigned before = (1u << first) - 1u;
-            if ((some & before) == before) k = first;
+    float2 h = make_float2(0.f, 0.f);
+    int k = 0, found = -1;  // the nearest k predecessors have published maps, but no state when last looked at
+    for (int spin = 0; found < 0; ++spin) {
+        uint2 s[kBatch];
+        ulonglong2 m[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int q = min(k + i, n - 1);
+            s[i] = load_state(states - q * stride);
+            m[i] = load_map(maps - q * stride);
         }
-        if (k < 0 && (spin & 255) == 255) {
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (!open || k >= n) continue;
+            if (s[i].x != kUnset && s[i].y != kUnset) {
+                h = make_float2(__uint_as_float(s[i].x), __uint_as_float(s[i].y));
+                found = k;
+                open = false;
+            } else if (static_cast<uint32_t>(m[i].x) != kUnset && static_cast<uint32_t>(m[i].y) != kUnset && k + 1 < n) {
+                ++k;
+            } else {
+                open = false;
+                k = 0;  // look again from the nearest
+            }
+        }
+        if (found < 0 && (spin & 255) == 255) {
             uint64_t now;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
             if (!t0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > kWaitNs)) {
+            if (now - t0 > kWaitNs) {
                 raise_status(a.status, LA_ERR_TIMEOUT);
-                return make_float2(0.f, 0.f);
+                return h;
             }
         }
     }
-    __threadfence();
-    __syncwarp();
-    float2 h = __ldcg(a.states + (j - (k + 1) * static_cast<int64_t>(a.tiles)) * 32 + lane);
-#pragma unroll 4
-    for (int i = k - 1; i >= 0; --i) {
-        const float4 m = __ldcg(a.maps + (j - (i + 1) * static_cast<int64_t>(a.tiles)) * 32 + lane);
-        h.x = fmaf(m.x, h.x, m.z);
-        h.y = fmaf(m.y, h.y, m.w);
+    for (int i = found - 1; i >= 0; i -= kBatch) {
+        ulonglong2 m[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) m[q] = load_map(maps - max(i - q, 0) * stride);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            if (i - q >= 0) {
+                h.x = fmaf(__uint_as_float(static_cast<uint32_t>(m[q].x)), h.x, __uint_as_float(static_cast<uint32_t>(m[q].x >> 32)));
+                h.y = fmaf(__uint_as_float(static_cast<uint32_t>(m[q].y)), h.y, __uint_as_float(static_cast<uint32_t>(m[q].y >> 32)));
+            }
     }
     return h;
 }
 
-// One warp: publishes the item's map, finds the entering state (`start` when the chain begins here),
-// publishes the leaving one.
+// One warp: publishes the item's map, finds the entering state (`in` where the chain begins), publishes
+// the leaving one.
 __device__ __forceinline__ void chain(const Args& a, int64_t j, const Item& it, float4 map, float2& in, float2& out) {
     const int lane = threadIdx.x & 31;
     if (it.dead) {
-        if (a.flags) publish(a.flags + j, 2);
+        if (a.states) publish_state(a.states + j * 32 + lane, make_float2(0.f, 0.f));
         return;
     }
+    map.x = settled(map.x);
+    map.y = settled(map.y);
     if (it.order > 0) {
-        if (!it.last) {
-            __stcg(a.maps + j * 32 + lane, map);
-            publish(a.flags + j, 1);
-        }
+        if (!it.last) publish_map(a.maps + j * 32 + lane, map);
         in = look_back(a, j, it.order);
     }
     out = make_float2(fmaf(map.x, in.x, map.z), fmaf(map.y, in.y, map.w));
-    if (a.flags && !it.last) {
-        __stcg(a.states + j * 32 + lane, out);
-        publish(a.flags + j, 2);
-    }
+    if (a.states && !it.last) publish_state(a.states + j * 32 + lane, out);
 }
 
 __device__ __forceinline__ void check_boundaries(const Args& a) {
@@ -577,32 +614,22 @@ la_status scan(Args& a, Which w, bool pair, cudaStream_t s) {
     return plain ? launch_scan(glr_bwd_kernel<X, G, false, true>, smem, a, s) : launch_scan(glr_bwd_kernel<X, G, false, false>, smem, a, s);
 }
 
-// The chain's table: flags, maps and states of every item.  None when no sequence can have two blocks.
-struct Table {
-    size_t maps, states, total;
-};
-Table table(int64_t T, int32_t N, int32_t D) {
-    Table t = {0, 0, 0};
-    if (T <= kBlock) return t;
-    const size_t items = static_cast<size_t>(T / kBlock + N) * ((D + kChannels - 1) / kChannels);
-    t.maps = (items * sizeof(int) + 255) & ~size_t(255);
-    t.states = t.maps + items * 32 * sizeof(float4);
-    t.total = t.states + items * 32 * sizeof(float2);
-    return t;
+// The chain's table: maps and states of every item.  None when no sequence can have two blocks.
+size_t map_bytes(int64_t T, int32_t N, int32_t D) {
+    if (T <= kBlock) return 0;
+    return static_cast<size_t>(T / kBlock + N) * ((D + kChannels - 1) / kChannels) * 32 * sizeof(ulonglong2);
 }
+size_t table_bytes(int64_t T, int32_t N, int32_t D) { return map_bytes(T, N, D) / 2 * 3; }  // a state is half a map
 
 la_status run_scan(Args& a, int32_t xd, int32_t gd, Which w, void* ws, cudaStream_t s) {
     if (a.N == 0) return LA_OK;
     a.tiles = (a.D + kChannels - 1) / kChannels;
     a.items = (a.T / kBlock + a.N) * a.tiles;
     if (a.items >= (int64_t(1) << 31)) return LA_ERR_UNSUPPORTED;
-    const Table t = table(a.T, a.N, a.D);
-    if (t.total) {
-        uint8_t* p = static_cast<uint8_t*>(ws);
-        a.flags = reinterpret_cast<int*>(p);
-        a.maps = reinterpret_cast<float4*>(p + t.maps);
-        a.states = reinterpret_cast<float2*>(p + t.states);
-        if (cudaMemsetAsync(a.flags, 0, static_cast<size_t>(a.items) * sizeof(int), s) != cudaSuccess) return LA_ERR_CUDA;
+    if (const size_t maps = map_bytes(a.T, a.N, a.D)) {
+        a.maps = static_cast<ulonglong2*>(ws);
+        a.states = reinterpret_cast<uint2*>(static_cast<uint8_t*>(ws) + maps);
+        if (cudaMemsetAsync(ws, 0xFF, table_bytes(a.T, a.N, a.D), s) != cudaSuccess) return LA_ERR_CUDA;
     }
     bool pair = a.D % 2 == 0 && pairs(a.x, a.x_st, a.T, xd) && pairs(a.g, a.g_st, a.T, gd);
     if (w == kFwd) pair = pair && (!a.h || pairs(a.h, a.h_st, a.T, xd));
@@ -629,7 +656,7 @@ size_t la_glr_checkpoint_rows(int64_t T, int32_t N) {
 size_t la_glr_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t backward, int32_t checkpoints_given) {
     if (T < 0 || N < 0 || D <= 0) return 0;
     const size_t states = backward && !checkpoints_given ? (la_glr_checkpoint_rows(T, N) * D * 4 + 255) & ~size_t(255) : 0;
-    return states + table(T, N, D).total;
+    return states + table_bytes(T, N, D);
 }
 
 la_status glr_fwd(const la_glr_fwd_params* p, void* stream) {
@@ -688,7 +715,7 @@ la_status glr_bwd(const la_glr_bwd_params* p, void* stream) {
     a.ckpt = const_cast<float*>(p->checkpoints);
     if (!a.ckpt && a.N > 0) {  // the forward again, for the states entering every block, which come after the table
         Args f = a;
-        f.ckpt = a.ckpt = reinterpret_cast<float*>(static_cast<uint8_t*>(p->workspace) + ((table(a.T, a.N, a.D).total + 255) & ~size_t(255)));
+        f.ckpt = a.ckpt = reinterpret_cast<float*>(static_cast<uint8_t*>(p->workspace) + table_bytes(a.T, a.N, a.D));
         if ((st = run_scan(f, p->x_dtype, p->g_dtype, kFwd, p->workspace, s)) != LA_OK) return st;
     }
     return run_scan(a, p->x_dtype, p->g_dtype, kBwd, p->workspace, s);
