@@ -10,16 +10,19 @@
 //   dg_t = dl_t dl/dg,  d(initial) = a_1 e_1.
 //
 // Every step is the affine map h -> a h + u, and maps compose, so the time axis is split.  A CTA takes
-// a block of 128 tokens x 64 channels into registers (each thread 8 tokens of 2 channels), composes
-// its warps' maps in shared memory, and needs one number per channel from the block before: the
-// state entering it.  That chain runs through a table in the workspace.  A block publishes its
-// composed map (A, B) as soon as it has it and the state leaving it once it knows the one entering;
-// a block that needs a state looks back over up to 32 predecessors, takes the nearest published
-// state and folds the maps after it in order.  The state leaving a block is always
-// fma(A, entering, B), whoever computes it, so the bits do not depend on what was published when.
-// The launch is cooperative (all CTAs resident), every CTA walks its items in ascending order and
-// items only wait for lower ones, so the lowest unfinished item never waits and the waits end; they
-// are bounded all the same.  Each operand is read once and each result written once.
+// a block of 128 tokens x 64 channels into shared memory, each warp its own 16 tokens by TMA, each
+// thread 8 tokens of 4 channels.  First pass: the block's composed map.  Then one number per channel
+// from the block before, the state entering it.  Second pass: the block again from shared memory (the
+// gate is cheaper to evaluate twice than to keep), results over the inputs, stored by TMA.
+//
+// The entering states run through a table in the workspace.  A block publishes its composed map (A, B)
+// as soon as it has it and the state leaving it once it knows the one entering; a block that needs a
+// state looks back over up to 32 predecessors, takes the nearest published state and folds the maps
+// after it in order.  The state leaving a block is always fma(A, entering, B), whoever computes it, so
+// the bits do not depend on what was published when.  The launch is cooperative (all CTAs resident),
+// every CTA walks its items in ascending order and items only wait for lower ones, so the lowest
+// unfinished item never waits and the waits end; they are bounded all the same.  Each operand is read
+// once and each result written once.
 //
 // The backward runs the same chain from each sequence's end, over the gradient leaving a token,
 // c_t = a_t (dh_t + c_{t+1}); the states entering its blocks come from the forward's checkpoints (one
@@ -30,36 +33,74 @@
 
 namespace {
 
+using namespace la;
 using namespace la::mixer;
 
-constexpr int kThreads = 128;                          // decode
-constexpr int kSpan = 8;                               // tokens of a thread
-constexpr int kWarps = 16;                             // of a CTA, one span each
+constexpr int kThreads = 128;                    // decode
+constexpr int kWarps = 8;                        // of a scan CTA
 constexpr int kScanThreads = 32 * kWarps;
-constexpr int kBlock = kSpan * kWarps;                 // tokens of a block, and between saved states
-constexpr int kChannels = 64;                          // of a CTA, two a lane
-constexpr uint64_t kWaitNs = 1000000000ull;            // a bounded wait gives up after a second
+constexpr int kSpan = 8;                         // tokens of a thread
+constexpr int kWarpRows = 2 * kSpan;             // tokens of a warp: its halves take one span each
+constexpr int kBlock = kWarpRows * kWarps;       // tokens of a block, and between saved states
+constexpr int kChannels = 64;                    // of a CTA, four a lane
+constexpr uint64_t kWaitNs = 1000000000ull;      // a bounded wait gives up after a second
 static_assert(kBlock == 128, "the checkpoint cadence of the interface");
 
-// a, m and dl/dg of one gate value.  The log sigmoid's a = s(g) and 1 - a = s(-g) come from
-// e = exp(-|g|) without cancellation; otherwise 1 - a = -expm1(l).
-__device__ __forceinline__ void gate(int mode, float lb, bool compl_in, float g, float& a, float& m, float& slope) {
-    if (mode == LA_GATE_LOGSIGMOID) {
-        const float e = expf(-fabsf(g)), big = 1.f / (1.f + e), small = e * big;
-        a = g >= 0.f ? big : small;
-        slope = g >= 0.f ? small : big;
-        m = compl_in ? slope : 1.f;
-        return;
-    }
+// e^l as 2^(l log2 e): the product's rounding is off by |l| 2^-24 of the result, which is small where
+// the result is not; results below 2^-126 are zero.
+__device__ __forceinline__ float exp_fast(float l) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l * 1.4426950408889634f));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 - e^l given e^l: the Taylor series (to l^7 / 7!, 2e-7 of it at 1/2) where the difference would cancel.
+__device__ __forceinline__ float one_minus_exp(float l, float e) {
+    float p = fmaf(l, 1.f / 7.f, 1.f);
+    p = fmaf(l * (1.f / 6.f), p, 1.f);
+    p = fmaf(l * (1.f / 5.f), p, 1.f);
+    p = fmaf(l * (1.f / 4.f), p, 1.f);
+    p = fmaf(l * (1.f / 3.f), p, 1.f);
+    p = fmaf(l * (1.f / 2.f), p, 1.f);
+    return fabsf(l) < 0.5f ? -l * p : 1.f - e;
+}
+
+// a, m and dl/dg of one gate value.  s(g) and 1 - s(g) come from e = exp(-|g|) without cancellation.
+template <int kMode, bool kComplement>
+__device__ __forceinline__ void gate(float lb, float g, float& a, float& m, float& slope) {
     float l = g;
     slope = 1.f;
-    if (mode == LA_GATE_SIGMOID_BOUND) {
-        const float e = expf(-fabsf(g)), big = 1.f / (1.f + e), small = e * big;
-        l = lb * (g >= 0.f ? big : small);
-        slope = l * (g >= 0.f ? small : big);
+    if (kMode != LA_GATE_LOG) {
+        const float e = exp_fast(-fabsf(g)), big = rcp_fast(1.f + e), small = e * big;
+        const float s = g >= 0.f ? big : small, rest = g >= 0.f ? small : big;
+        if (kMode == LA_GATE_LOGSIGMOID) {
+            a = s;
+            slope = rest;
+            m = kComplement ? rest : 1.f;
+            return;
+        }
+        l = lb * s;
+        slope = l * rest;
     }
-    a = expf(l);
-    m = compl_in ? -expm1f(l) : 1.f;
+    a = exp_fast(l);
+    m = kComplement ? one_minus_exp(l, a) : 1.f;
+}
+
+// Calls f with the gate's mode and complement as constants.
+template <int kMode, bool kComplement>
+struct Gate {
+    static constexpr int mode = kMode;
+    static constexpr bool complement = kComplement;
+};
+template <typename F>
+__device__ __forceinline__ void with_gate(int mode, int complement, F f) {
+    if (mode == LA_GATE_LOG) complement ? f(Gate<LA_GATE_LOG, true>()) : f(Gate<LA_GATE_LOG, false>());
+    else if (mode == LA_GATE_LOGSIGMOID) complement ? f(Gate<LA_GATE_LOGSIGMOID, true>()) : f(Gate<LA_GATE_LOGSIGMOID, false>());
+    else complement ? f(Gate<LA_GATE_SIGMOID_BOUND, true>()) : f(Gate<LA_GATE_SIGMOID_BOUND, false>());
 }
 
 struct Args {
@@ -82,54 +123,70 @@ struct Args {
     int64_t items;     // (T / kBlock + N) * tiles
     ulonglong2* maps;  // [items][32]: (A, B) of a lane's two channels; null when no sequence has two blocks
     uint2* states;     // [items][32]: the states leaving the item
+    int tma;           // every operand can move by TMA
 };
 
-// ---------------------------------------------------------------- asynchronous copies
-// One thread's two channels of one token (4 or 8 bytes) into its own place in shared memory.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "n"(kBytes)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
+// ---------------------------------------------------------------- a thread's four channels of one row in shared memory
 template <typename T>
-struct Pair {
-    T v[2];
-};
+__device__ __forceinline__ void get4(const T* p, float (&v)[4]) {
+    if (sizeof(T) == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        v[0] = __uint_as_float(w.x << 16);
+        v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16);
+        v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        v[0] = w.x;
+        v[1] = w.y;
+        v[2] = w.z;
+        v[3] = w.w;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put4(T* p, const float (&v)[4]) {
+    if (sizeof(T) == 2) {
+        __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+// Two of the four channels (p points at the first of the pair).
+template <typename T>
+__device__ __forceinline__ float2 get2(const T* p) {
+    if (sizeof(T) == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    return *reinterpret_cast<const float2*>(p);
+}
+template <typename T>
+__device__ __forceinline__ void put2(T* p, float x, float y) {
+    if (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+    else *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
 
-// The channels d, d + 1 of one row; kPair: as one 2-element access (D even, everything aligned).
-template <typename T, bool kPair>
-__device__ __forceinline__ void load2(const void* base, int64_t at, int d, int D, float& v0, float& v1) {
-    const T* p = static_cast<const T*>(base) + at + d;
-    if (kPair) {
-        if (sizeof(T) == 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-            v0 = __uint_as_float(w << 16);
-            v1 = __uint_as_float(w & 0xFFFF0000u);
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(p);
-            v0 = w.x;
-            v1 = w.y;
-        }
-    } else {
-        v0 = to_f(p[0]);
-        v1 = d + 1 < D ? to_f(p[1]) : 0.f;
-    }
+// ---------------------------------------------------------------- a warp's rows between global and shared memory
+// Without TMA: lane by lane, rows [0, n) of the warp, channels below D.
+template <typename T>
+__device__ __forceinline__ void rows_in(T* s, const void* base, int64_t stride, int64_t token, int n, int d, int D) {
+    const int lane = threadIdx.x & 31;
+    const T* p = static_cast<const T*>(base) + token * stride + d;
+    for (int r = 0; r < n; ++r)
+#pragma unroll
+        for (int c = 0; c < kChannels; c += 32) s[r * kChannels + c + lane] = d + c + lane < D ? p[r * stride + c + lane] : from_f<T>(0.f);
 }
-template <typename T, bool kPair>
-__device__ __forceinline__ void store2(void* base, int64_t at, int d, int D, float v0, float v1) {
-    T* p = static_cast<T*>(base) + at + d;
-    if (kPair) {
-        if (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v0, v1);
-        else *reinterpret_cast<float2*>(p) = make_float2(v0, v1);
-    } else {
-        p[0] = from_f<T>(v0);
-        if (d + 1 < D) p[1] = from_f<T>(v1);
-    }
+template <typename T>
+__device__ __forceinline__ void rows_out(const T* s, void* base, int64_t stride, int64_t token, int n, int d, int D) {
+    const int lane = threadIdx.x & 31;
+    T* p = static_cast<T*>(base) + token * stride + d;
+    for (int r = 0; r < n; ++r)
+#pragma unroll
+        for (int c = 0; c < kChannels; c += 32)
+            if (d + c + lane < D) p[r * stride + c + lane] = s[r * kChannels + c + lane];
 }
+
 __device__ __forceinline__ void load2_any(const void* base, int64_t at, int d, int D, int is_bf16, float& v0, float& v1) {
     v0 = d < D ? load_any(base, at + d, is_bf16) : 0.f;
     v1 = d + 1 < D ? load_any(base, at + d + 1, is_bf16) : 0.f;
@@ -293,268 +350,385 @@ __device__ __forceinline__ void check_boundaries(const Args& a) {
         check_cu(a.cu, a.cu64, a.N, a.T, i, a.status);
 }
 
-// Shared memory: one staging place per thread, token and operand, then the warps' maps.
-template <typename X, typename G, int kX>
-constexpr size_t stage_bytes() { return static_cast<size_t>(kScanThreads) * kSpan * (kX * sizeof(Pair<X>) + sizeof(Pair<G>)); }
+struct Maps {
+    CUtensorMap x, g, dh, out, dg;  // out: h, or dx in the backward
+};
 
-template <typename X, typename G, bool kPair>
-__global__ void __launch_bounds__(kScanThreads, 2) glr_fwd_kernel(const Args a) {
-    extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ float4 maps[kWarps][32];
-    __shared__ float2 enter[kWarps][32];
-    Pair<X>* sx = reinterpret_cast<Pair<X>*>(stage) + threadIdx.x;
-    Pair<G>* sg = reinterpret_cast<Pair<G>*>(stage + static_cast<size_t>(kScanThreads) * kSpan * sizeof(Pair<X>)) + threadIdx.x;
-    __shared__ Item items[2];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// What both directions keep beside the staged rows.
+struct Shared {
+    float a[kWarps][kChannels], u[kWarps][kChannels], c[kWarps][kChannels];  // each warp's map (c: the gradients')
+    float in[kChannels], h0[kChannels];
+    uint64_t bar[kWarps];
+    Item items[2];
+};
+
+template <typename X, typename G, int kX>
+constexpr size_t stage_bytes() { return static_cast<size_t>(kBlock) * kChannels * (kX * sizeof(X) + sizeof(G)); }
+
+// CTAs of an SM: as many as the staged rows leave room for.
+template <typename X, typename G>
+constexpr int fwd_ctas() { return sizeof(X) + sizeof(G) == 4 ? 5 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
+template <typename X, typename G>
+constexpr int bwd_ctas() { return sizeof(X) + sizeof(G) == 8 ? 2 : 3; }
+
+template <typename X, typename G>
+__global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t stage[];
+    __shared__ Shared sh;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = lane >> 4, c4 = (lane & 15) * 4;
+    X* wx = reinterpret_cast<X*>(stage) + w * kWarpRows * kChannels;                       // the warp's rows
+    G* wg = reinterpret_cast<G*>(stage + sizeof(X) * kBlock * kChannels) + w * kWarpRows * kChannels;
+    X* sx = wx + half * kSpan * kChannels + c4;                                            // the thread's
+    G* sg = wg + half * kSpan * kChannels + c4;
+    if (lane == 0) mbar_init(&sh.bar[w], 1);
+    fence_mbar_init();
     check_boundaries(a);
 
+    // The warp's rows of an item on their way into shared memory; false when it has none.
     auto fetch = [&](const Item& it) {
-        const int d = it.d + 2 * lane, n = d < a.D ? it.count - w * kSpan : 0;
-        const int64_t t = it.start + w * kSpan;
-#pragma unroll
-        for (int k = 0; k < kSpan; ++k)
-            if (k < n) {
-                copy_async<sizeof(Pair<X>)>(sx + k * kScanThreads, static_cast<const X*>(a.x) + (t + k) * a.x_st + d);
-                copy_async<sizeof(Pair<G>)>(sg + k * kScanThreads, static_cast<const G*>(a.g) + (t + k) * a.g_st + d);
+        const int n = min(it.count - w * kWarpRows, kWarpRows), token = it.start + w * kWarpRows;
+        if (n <= 0) return;
+        if (a.tma) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.bar[w], kWarpRows * kChannels * (sizeof(X) + sizeof(G)));
+                tile_load(wx, &maps.x, &sh.bar[w], it.d, token);
+                tile_load(wg, &maps.g, &sh.bar[w], it.d, token);
             }
-        copies_commit();
+        } else {
+            rows_in(wx, a.x, a.x_st, token, n, it.d, a.D);
+            rows_in(wg, a.g, a.g_st, token, n, it.d, a.D);
+        }
     };
 
     int64_t j = blockIdx.x;
-    if (w == 0) locate<false>(a, j, &items[0]);
+    uint32_t parity = 0;
+    if (w == 0) locate<false>(a, j, &sh.items[0]);
     __syncthreads();
-    if (kPair) fetch(items[0]);
+    fetch(sh.items[0]);
     for (int at = 0;; at ^= 1) {
-        const Item& it = items[at];
+        const Item& it = sh.items[at];
         const int64_t jn = j + gridDim.x;
-        // the next item, while this one's operands arrive; nobody reads its place any more
-        if (w == kWarps - 1 && jn < a.items) locate<false>(a, jn, &items[at ^ 1]);
-        const int ch = it.d + 2 * lane;  // this lane's first channel
-        const int n = ch < a.D ? it.count - w * kSpan : 0;
-        const int64_t t = it.start + w * kSpan;
-        float dec[kSpan][2], u[kSpan][2];
-        if (kPair) copies_wait();
-        float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kSpan; ++k) {
-            dec[k][0] = dec[k][1] = 1.f;
-            u[k][0] = u[k][1] = 0.f;
-            if (k < n) {
-                float x0, x1, g0, g1, m0, m1, slope;
-                if (kPair) {
-                    load2<X, true>(sx + k * kScanThreads, 0, 0, 2, x0, x1);
-                    load2<G, true>(sg + k * kScanThreads, 0, 0, 2, g0, g1);
-                } else {
-                    load2<X, false>(a.x, (t + k) * a.x_st, ch, a.D, x0, x1);
-                    load2<G, false>(a.g, (t + k) * a.g_st, ch, a.D, g0, g1);
-                }
-                gate(a.mode, a.lb, a.compl_in, g0, dec[k][0], m0, slope);
-                gate(a.mode, a.lb, a.compl_in, g1, dec[k][1], m1, slope);
-                u[k][0] = m0 * x0;
-                u[k][1] = m1 * x1;
-                map.z = fmaf(dec[k][0], map.z, u[k][0]);
-                map.w = fmaf(dec[k][1], map.w, u[k][1]);
-                map.x *= dec[k][0];
-                map.y *= dec[k][1];
-            }
+        const int rows = min(it.count - w * kWarpRows, kWarpRows);  // of the warp
+        const int n = rows - half * kSpan;                          // of the thread (may exceed kSpan)
+        float2 in = make_float2(0.f, 0.f);
+        if (w == 0 && it.order == 0 && !it.dead && a.s0)
+            load2_any(a.s0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, in.x, in.y);
+        __syncwarp();
+        if (a.tma && rows > 0) {
+            if (!mbar_wait(&sh.bar[w], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            parity ^= 1;
         }
-        maps[w][lane] = map;
-        __syncthreads();
-        if (kPair && jn < a.items) fetch(items[at ^ 1]);
-        if (w == 0) {
-            float2 in = make_float2(0.f, 0.f), out = in;
-            if (it.order == 0 && !it.dead && a.s0) load2_any(a.s0, it.state * static_cast<int64_t>(a.D), ch, a.D, a.s0_bf16, in.x, in.y);
-            map = maps[0][lane];
-#pragma unroll
-            for (int i = 1; i < kWarps; ++i) {
-                const float4 q = maps[i][lane];
-                map.z = fmaf(q.x, map.z, q.z);
-                map.w = fmaf(q.y, map.w, q.w);
-                map.x *= q.x;
-                map.y *= q.y;
-            }
-            chain(a, j, it, map, in, out);
-            if (!it.dead) {
-                if (a.ckpt && it.count > 0) store2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), ch, a.D, 0, in.x, in.y);
-                if (it.last) {
-                    if (a.idx) store2_any(const_cast<void*>(a.s0), it.state * static_cast<int64_t>(a.D), ch, a.D, a.s0_bf16, out.x, out.y);
-                    else if (a.fin) store2_any(a.fin, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, out.x, out.y);
-                }
-            }
-            enter[0][lane] = in;
-#pragma unroll
-            for (int i = 1; i < kWarps; ++i) {
-                const float4 q = maps[i - 1][lane];
-                in.x = fmaf(q.x, in.x, q.z);
-                in.y = fmaf(q.y, in.y, q.w);
-                enter[i][lane] = in;
-            }
-        }
-        __syncthreads();
-        if (a.h) {
-            float2 h = enter[w][lane];
+        // the map of the thread's span
+        float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
+        with_gate(a.mode, a.compl_in, [&](auto gt) {
 #pragma unroll
             for (int k = 0; k < kSpan; ++k)
                 if (k < n) {
-                    h.x = fmaf(dec[k][0], h.x, u[k][0]);
-                    h.y = fmaf(dec[k][1], h.y, u[k][1]);
-                    store2<X, kPair>(a.h, (t + k) * a.h_st, ch, a.D, h.x, h.y);
+                    float x[4], g[4];
+                    get4(sx + k * kChannels, x);
+                    get4(sg + k * kChannels, g);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float dec, m, slope;
+                        gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, g[i], dec, m, slope);
+                        cu[i] = fmaf(dec, cu[i], decltype(gt)::complement ? m * x[i] : x[i]);
+                        ca[i] *= dec;
+                    }
                 }
+        });
+        // the other half's: the lower one's map enters the upper one, both make the warp's
+        float oa[4], ou[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            oa[i] = __shfl_xor_sync(0xffffffffu, ca[i], 16);
+            ou[i] = __shfl_xor_sync(0xffffffffu, cu[i], 16);
+        }
+        if (half == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sh.a[w][c4 + i] = ca[i] * oa[i];
+                sh.u[w][c4 + i] = fmaf(oa[i], cu[i], ou[i]);
+            }
+        }
+        __syncthreads();
+        if (w == kWarps - 1 && jn < a.items) locate<false>(a, jn, &sh.items[at ^ 1]);
+        if (w == 0) {
+            float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 qa = *reinterpret_cast<const float2*>(&sh.a[i][2 * lane]), qu = *reinterpret_cast<const float2*>(&sh.u[i][2 * lane]);
+                map.z = fmaf(qa.x, map.z, qu.x);
+                map.w = fmaf(qa.y, map.w, qu.y);
+                map.x *= qa.x;
+                map.y *= qa.y;
+            }
+            float2 out;
+            chain(a, j, it, map, in, out);
+            *reinterpret_cast<float2*>(&sh.in[2 * lane]) = in;
+            if (!it.dead) {
+                if (a.ckpt && it.count > 0) store2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
+                if (it.last) {
+                    if (a.idx) store2_any(const_cast<void*>(a.s0), it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, out.x, out.y);
+                    else if (a.fin) store2_any(a.fin, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, out.x, out.y);
+                }
+            }
+        }
+        // while the chain goes on: the map of the rows before this warp's (the thread's, in the upper half)
+        float pa[4] = {1.f, 1.f, 1.f, 1.f}, pu[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < w; ++i) {
+            float qa[4], qu[4];
+            get4(&sh.a[i][c4], qa);
+            get4(&sh.u[i][c4], qu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pu[e] = fmaf(qa[e], pu[e], qu[e]);
+                pa[e] *= qa[e];
+            }
+        }
+        if (half == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pu[e] = fmaf(oa[e], pu[e], ou[e]);
+                pa[e] *= oa[e];
+            }
+        }
+        __syncthreads();
+        if (a.h && rows > 0) {
+            float h[4];
+            get4(&sh.in[c4], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = fmaf(pa[e], h[e], pu[e]);
+            with_gate(a.mode, a.compl_in, [&](auto gt) {
+#pragma unroll
+                for (int k = 0; k < kSpan; ++k)
+                    if (k < n) {
+                        float x[4], g[4];
+                        get4(sx + k * kChannels, x);
+                        get4(sg + k * kChannels, g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float dec, m, slope;
+                            gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, g[i], dec, m, slope);
+                            h[i] = fmaf(dec, h[i], decltype(gt)::complement ? m * x[i] : x[i]);
+                        }
+                        put4(sx + k * kChannels, h);
+                    }
+            });
+            // whole tiles by TMA; the last rows of a sequence one by one
+            if (a.tma && rows == kWarpRows) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tile_store(&maps.out, wx, it.d, it.start + w * kWarpRows);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
+            } else {
+                __syncwarp();
+                rows_out(wx, a.h, a.h_st, it.start + w * kWarpRows, rows, it.d, a.D);
+            }
         }
         if (jn >= a.items) break;
+        fence_proxy_async_smem();  // the rows were written here, and are about to be by TMA
+        __syncwarp();
+        fetch(sh.items[at ^ 1]);
         j = jn;
     }
+    if (lane == 0) bulk_wait_all();
 }
 
-// kPlain: log decay without the complement, where m = dl/dg = 1.
-template <typename X, typename G, bool kPair, bool kPlain>
-__global__ void __launch_bounds__(kScanThreads, 1) glr_bwd_kernel(const Args a) {
-    extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ float4 maps[kWarps][32];   // (a, a, u, u) of the states
-    __shared__ float2 grads[kWarps][32];  // the constant part of the gradients' map
-    __shared__ float2 enter[kWarps][32], leave[kWarps][32];
-    constexpr size_t kPlane = static_cast<size_t>(kScanThreads) * kSpan;
-    Pair<X>* sx = reinterpret_cast<Pair<X>*>(stage) + threadIdx.x;
-    Pair<X>* sd = sx + kPlane;
-    Pair<G>* sg = reinterpret_cast<Pair<G>*>(stage + 2 * kPlane * sizeof(Pair<X>)) + threadIdx.x;
-    __shared__ Item items[2];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+template <typename X, typename G>
+__global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t stage[];
+    __shared__ Shared sh;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = lane >> 4, c4 = (lane & 15) * 4;
+    constexpr int kPlane = kBlock * kChannels;
+    X* wx = reinterpret_cast<X*>(stage) + w * kWarpRows * kChannels;
+    X* wd = wx + kPlane;
+    G* wg = reinterpret_cast<G*>(stage + 2 * sizeof(X) * kPlane) + w * kWarpRows * kChannels;
+    const int mine = half * kSpan * kChannels + c4;  // the thread's first element of the warp's rows
+    if (lane == 0) mbar_init(&sh.bar[w], 1);
+    fence_mbar_init();
     check_boundaries(a);
 
     auto fetch = [&](const Item& it) {
-        const int d = it.d + 2 * lane, n = d < a.D ? it.count - w * kSpan : 0;
-        const int64_t t = it.start + w * kSpan;
-#pragma unroll
-        for (int k = 0; k < kSpan; ++k)
-            if (k < n) {
-                copy_async<sizeof(Pair<X>)>(sx + k * kScanThreads, static_cast<const X*>(a.x) + (t + k) * a.x_st + d);
-                copy_async<sizeof(Pair<X>)>(sd + k * kScanThreads, static_cast<const X*>(a.dh) + (t + k) * a.dh_st + d);
-                copy_async<sizeof(Pair<G>)>(sg + k * kScanThreads, static_cast<const G*>(a.g) + (t + k) * a.g_st + d);
+        const int n = min(it.count - w * kWarpRows, kWarpRows), token = it.start + w * kWarpRows;
+        if (n <= 0) return;
+        if (a.tma) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.bar[w], kWarpRows * kChannels * (2 * sizeof(X) + sizeof(G)));
+                tile_load(wx, &maps.x, &sh.bar[w], it.d, token);
+                tile_load(wd, &maps.dh, &sh.bar[w], it.d, token);
+                tile_load(wg, &maps.g, &sh.bar[w], it.d, token);
             }
-        copies_commit();
+        } else {
+            rows_in(wx, a.x, a.x_st, token, n, it.d, a.D);
+            rows_in(wd, a.dh, a.dh_st, token, n, it.d, a.D);
+            rows_in(wg, a.g, a.g_st, token, n, it.d, a.D);
+        }
     };
 
     int64_t j = blockIdx.x;
-    if (w == 0) locate<true>(a, j, &items[0]);
+    uint32_t parity = 0;
+    if (w == 0) locate<true>(a, j, &sh.items[0]);
     __syncthreads();
-    if (kPair) fetch(items[0]);
+    fetch(sh.items[0]);
     for (int at = 0;; at ^= 1) {
-        const Item& it = items[at];
+        const Item& it = sh.items[at];
         const int64_t jn = j + gridDim.x;
-        // the next item, while this one's operands arrive; nobody reads its place any more
-        if (w == kWarps - 1 && jn < a.items) locate<true>(a, jn, &items[at ^ 1]);
-        const int ch = it.d + 2 * lane;  // this lane's first channel
-        const int n = ch < a.D ? it.count - w * kSpan : 0;
-        const int64_t t = it.start + w * kSpan;
-        float dec[kSpan][2], u[kSpan][2], d[kSpan][2], x[kSpan][2], m[kSpan][2], slope[kSpan][2];
-        if (kPair) copies_wait();
-        float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
+        const int rows = min(it.count - w * kWarpRows, kWarpRows);
+        const int n = rows - half * kSpan;
+        float2 in = make_float2(0.f, 0.f);
+        if (w == 0 && it.order == 0 && !it.dead && a.dfin)
+            load2_any(a.dfin, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
+        if (w == 1 && it.count > 0) load2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
+        __syncwarp();
+        if (a.tma && rows > 0) {
+            if (!mbar_wait(&sh.bar[w], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            parity ^= 1;
+        }
+        // the maps of the thread's span, h -> ca h + cu forwards and c -> ca c + cc backwards
+        float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f};
+        with_gate(a.mode, a.compl_in, [&](auto gt) {
 #pragma unroll
-        for (int k = 0; k < kSpan; ++k) {
-            dec[k][0] = dec[k][1] = 1.f;
-            u[k][0] = u[k][1] = d[k][0] = d[k][1] = 0.f;
-            if (k < n) {
-                float g0, g1;
-                if (kPair) {
-                    load2<X, true>(sx + k * kScanThreads, 0, 0, 2, x[k][0], x[k][1]);
-                    load2<X, true>(sd + k * kScanThreads, 0, 0, 2, d[k][0], d[k][1]);
-                    load2<G, true>(sg + k * kScanThreads, 0, 0, 2, g0, g1);
-                } else {
-                    load2<X, false>(a.x, (t + k) * a.x_st, ch, a.D, x[k][0], x[k][1]);
-                    load2<X, false>(a.dh, (t + k) * a.dh_st, ch, a.D, d[k][0], d[k][1]);
-                    load2<G, false>(a.g, (t + k) * a.g_st, ch, a.D, g0, g1);
+            for (int k = 0; k < kSpan; ++k)
+                if (k < n) {
+                    float x[4], g[4], d[4];
+                    get4(wx + mine + k * kChannels, x);
+                    get4(wg + mine + k * kChannels, g);
+                    get4(wd + mine + k * kChannels, d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float dec, m, slope;
+                        gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, g[i], dec, m, slope);
+                        cu[i] = fmaf(dec, cu[i], decltype(gt)::complement ? m * x[i] : x[i]);
+                        ca[i] *= dec;
+                        cc[i] = fmaf(ca[i], d[i], cc[i]);
+                    }
                 }
-                if (kPlain) {
-                    dec[k][0] = expf(g0);
-                    dec[k][1] = expf(g1);
-                    u[k][0] = x[k][0];
-                    u[k][1] = x[k][1];
-                } else {
-                    gate(a.mode, a.lb, a.compl_in, g0, dec[k][0], m[k][0], slope[k][0]);
-                    gate(a.mode, a.lb, a.compl_in, g1, dec[k][1], m[k][1], slope[k][1]);
-                    u[k][0] = m[k][0] * x[k][0];
-                    u[k][1] = m[k][1] * x[k][1];
-                }
-                map.z = fmaf(dec[k][0], map.z, u[k][0]);
-                map.w = fmaf(dec[k][1], map.w, u[k][1]);
-                map.x *= dec[k][0];
-                map.y *= dec[k][1];
+        });
+        float oa[4], ou[4], oc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            oa[i] = __shfl_xor_sync(0xffffffffu, ca[i], 16);
+            ou[i] = __shfl_xor_sync(0xffffffffu, cu[i], 16);
+            oc[i] = __shfl_xor_sync(0xffffffffu, cc[i], 16);
+        }
+        if (half == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sh.a[w][c4 + i] = ca[i] * oa[i];
+                sh.u[w][c4 + i] = fmaf(oa[i], cu[i], ou[i]);
+                sh.c[w][c4 + i] = fmaf(ca[i], oc[i], cc[i]);
             }
         }
-        float2 c = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = kSpan - 1; k >= 0; --k) {
-            c.x = dec[k][0] * (d[k][0] + c.x);
-            c.y = dec[k][1] * (d[k][1] + c.y);
-        }
-        maps[w][lane] = map;
-        grads[w][lane] = c;
+        if (w == 1) *reinterpret_cast<float2*>(&sh.h0[2 * lane]) = in;
         __syncthreads();
-        if (kPair && jn < a.items) fetch(items[at ^ 1]);
+        if (w == kWarps - 1 && jn < a.items) locate<true>(a, jn, &sh.items[at ^ 1]);
         if (w == 0) {
-            float2 in = make_float2(0.f, 0.f), out = in;
-            if (it.order == 0 && !it.dead && a.dfin) load2_any(a.dfin, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, in.x, in.y);
-            map = make_float4(1.f, 1.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = kWarps - 1; i >= 0; --i) {
-                const float4 q = maps[i][lane];
-                const float2 e = grads[i][lane];
-                map.z = fmaf(q.x, map.z, e.x);
-                map.w = fmaf(q.y, map.w, e.y);
-                map.x *= q.x;
-                map.y *= q.y;
-            }
-            chain(a, j, it, map, in, out);
-            if (it.last && !it.dead && a.ds0) store2_any(a.ds0, it.state * static_cast<int64_t>(a.D), ch, a.D, 0, out.x, out.y);
-#pragma unroll
-            for (int i = kWarps - 1; i >= 0; --i) {
-                leave[i][lane] = in;
-                const float4 q = maps[i][lane];
-                const float2 e = grads[i][lane];
-                in.x = fmaf(q.x, in.x, e.x);
-                in.y = fmaf(q.y, in.y, e.y);
-            }
-        } else if (w == 1) {
-            float2 h = make_float2(0.f, 0.f);
-            if (it.count > 0) load2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), ch, a.D, 0, h.x, h.y);
+            float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-                enter[i][lane] = h;
-                const float4 q = maps[i][lane];
-                h.x = fmaf(q.x, h.x, q.z);
-                h.y = fmaf(q.y, h.y, q.w);
+                const float2 qa = *reinterpret_cast<const float2*>(&sh.a[i][2 * lane]), qc = *reinterpret_cast<const float2*>(&sh.c[i][2 * lane]);
+                map.z = fmaf(map.x, qc.x, map.z);
+                map.w = fmaf(map.y, qc.y, map.w);
+                map.x *= qa.x;
+                map.y *= qa.y;
+            }
+            float2 out;
+            chain(a, j, it, map, in, out);
+            *reinterpret_cast<float2*>(&sh.in[2 * lane]) = in;
+            if (it.last && !it.dead && a.ds0)
+                store2_any(a.ds0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, out.x, out.y);
+        }
+        // while the chain goes on: the state entering the thread's span, and the gradients' map after it
+        float h[4], pa[4] = {1.f, 1.f, 1.f, 1.f}, pc[4] = {0.f, 0.f, 0.f, 0.f};
+        get4(&sh.h0[c4], h);
+        for (int i = 0; i < w; ++i) {
+            float qa[4], qu[4];
+            get4(&sh.a[i][c4], qa);
+            get4(&sh.u[i][c4], qu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = fmaf(qa[e], h[e], qu[e]);
+        }
+        if (half == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = fmaf(oa[e], h[e], ou[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pa[e] = oa[e];
+                pc[e] = oc[e];
+            }
+        }
+        for (int i = w + 1; i < kWarps; ++i) {
+            float qa[4], qc[4];
+            get4(&sh.a[i][c4], qa);
+            get4(&sh.c[i][c4], qc);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pc[e] = fmaf(pa[e], qc[e], pc[e]);
+                pa[e] *= qa[e];
             }
         }
         __syncthreads();
-        float2 h = enter[w][lane];
+        if (rows > 0) {
+            with_gate(a.mode, a.compl_in, [&](auto gt) {
+                constexpr bool kCompl = decltype(gt)::complement, kSlope = decltype(gt)::mode != LA_GATE_LOG;
+#pragma unroll 1
+                for (int p = 0; p < 4; p += 2) {  // two channels at a time: what a span keeps has to fit the registers
+                    float dec[kSpan][2], prev[kSpan][2], m[kSpan][2], slope[kSpan][2];
+                    float2 e = *reinterpret_cast<const float2*>(&sh.in[c4 + p]);
+                    e.x = fmaf(p ? pa[2] : pa[0], e.x, p ? pc[2] : pc[0]);
+                    e.y = fmaf(p ? pa[3] : pa[1], e.y, p ? pc[3] : pc[1]);
+                    float h0 = p ? h[2] : h[0], h1 = p ? h[3] : h[1];
 #pragma unroll
-        for (int k = 0; k < kSpan; ++k) {  // u becomes h_{t-1}
-            const float u0 = u[k][0], u1 = u[k][1];
-            u[k][0] = h.x;
-            u[k][1] = h.y;
-            h.x = fmaf(dec[k][0], h.x, u0);
-            h.y = fmaf(dec[k][1], h.y, u1);
-        }
-        float2 e = leave[w][lane];
+                    for (int k = 0; k < kSpan; ++k)
+                        if (k < n) {
+                            const float2 x = get2(wx + mine + k * kChannels + p), g = get2(wg + mine + k * kChannels + p);
+                            gate<decltype(gt)::mode, kCompl>(a.lb, g.x, dec[k][0], m[k][0], slope[k][0]);
+                            gate<decltype(gt)::mode, kCompl>(a.lb, g.y, dec[k][1], m[k][1], slope[k][1]);
+                            prev[k][0] = kCompl ? h0 - x.x : h0;
+                            prev[k][1] = kCompl ? h1 - x.y : h1;
+                            h0 = fmaf(dec[k][0], h0, kCompl ? m[k][0] * x.x : x.x);
+                            h1 = fmaf(dec[k][1], h1, kCompl ? m[k][1] * x.y : x.y);
+                        }
 #pragma unroll
-        for (int k = kSpan - 1; k >= 0; --k) {
-            if (k >= n) continue;
-            e.x += d[k][0];
-            e.y += d[k][1];
-            if (kPlain) store2<X, kPair>(a.dx, (t + k) * a.dx_st, ch, a.D, e.x, e.y);
-            else store2<X, kPair>(a.dx, (t + k) * a.dx_st, ch, a.D, m[k][0] * e.x, m[k][1] * e.y);
-            e.x *= dec[k][0];
-            e.y *= dec[k][1];
-            if (kPlain) {
-                store2<G, kPair>(a.dg, (t + k) * a.dg_st, ch, a.D, e.x * u[k][0], e.y * u[k][1]);
+                    for (int k = kSpan - 1; k >= 0; --k)
+                        if (k < n) {
+                            const float2 d = get2(wd + mine + k * kChannels + p);
+                            e.x += d.x;
+                            e.y += d.y;
+                            put2(wx + mine + k * kChannels + p, kCompl ? m[k][0] * e.x : e.x, kCompl ? m[k][1] * e.y : e.y);
+                            e.x *= dec[k][0];
+                            e.y *= dec[k][1];
+                            const float g0 = e.x * prev[k][0], g1 = e.y * prev[k][1];
+                            put2(wg + mine + k * kChannels + p, kSlope ? g0 * slope[k][0] : g0, kSlope ? g1 * slope[k][1] : g1);
+                        }
+                }
+            });
+            if (a.tma && rows == kWarpRows) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tile_store(&maps.out, wx, it.d, it.start + w * kWarpRows);
+                    tile_store(&maps.dg, wg, it.d, it.start + w * kWarpRows);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
             } else {
-                const float p0 = a.compl_in ? u[k][0] - x[k][0] : u[k][0], p1 = a.compl_in ? u[k][1] - x[k][1] : u[k][1];
-                store2<G, kPair>(a.dg, (t + k) * a.dg_st, ch, a.D, e.x * p0 * slope[k][0], e.y * p1 * slope[k][1]);
+                __syncwarp();
+                rows_out(wx, a.dx, a.dx_st, it.start + w * kWarpRows, rows, it.d, a.D);
+                rows_out(wg, a.dg, a.dg_st, it.start + w * kWarpRows, rows, it.d, a.D);
             }
         }
         if (jn >= a.items) break;
+        fence_proxy_async_smem();  // the rows were written here, and are about to be by TMA
+        __syncwarp();
+        fetch(sh.items[at ^ 1]);
         j = jn;
     }
+    if (lane == 0) bulk_wait_all();
 }
 
 template <typename X, typename G>
@@ -571,14 +745,15 @@ __global__ void __launch_bounds__(kThreads) glr_decode_kernel(const Args a) {
         }
     }
     float dec, m, slope;
-    gate(a.mode, a.lb, a.compl_in, to_f(static_cast<const G*>(a.g)[i * a.g_st + d]), dec, m, slope);
+    const float g = to_f(static_cast<const G*>(a.g)[i * a.g_st + d]);
+    with_gate(a.mode, a.compl_in, [&](auto gt) { gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, g, dec, m, slope); });
     const float h = fmaf(dec, load_any(a.s0, slot * a.D + d, a.s0_bf16), m * to_f(static_cast<const X*>(a.x)[i * a.x_st + d]));
     store_any(const_cast<void*>(a.s0), slot * a.D + d, a.s0_bf16, h);
     static_cast<X*>(a.h)[i * a.h_st + d] = from_f<X>(h);
 }
 
 template <typename K>
-la_status launch_scan(K kernel, size_t smem, Args& a, cudaStream_t s) {
+la_status launch_scan(K kernel, size_t smem, Args& a, Maps& maps, cudaStream_t s) {
     int dev = 0, sms = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
@@ -587,7 +762,7 @@ la_status launch_scan(K kernel, size_t smem, Args& a, cudaStream_t s) {
         return LA_ERR_CUDA;
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.items, static_cast<int64_t>(sms) * per_sm));
-    void* args[] = {&a};
+    void* args[] = {&a, &maps};
     if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kScanThreads), args, smem, s) != cudaSuccess) {
         (void)cudaGetLastError();
         return LA_ERR_CUDA;
@@ -595,23 +770,12 @@ la_status launch_scan(K kernel, size_t smem, Args& a, cudaStream_t s) {
     return LA_OK;
 }
 
-// Whether every row of the operand starts on a boundary of two of its elements.
-bool pairs(const void* p, int64_t stride, int64_t T, int32_t dtype) {
-    return aligned_to(p, 2 * dtype_size(dtype)) && (T == 1 || stride % 2 == 0);
-}
-
 enum Which { kFwd, kBwd };
 
 template <typename X, typename G>
-la_status scan(Args& a, Which w, bool pair, cudaStream_t s) {
-    if (w == kFwd) {
-        const size_t smem = pair ? stage_bytes<X, G, 1>() : 0;
-        return pair ? launch_scan(glr_fwd_kernel<X, G, true>, smem, a, s) : launch_scan(glr_fwd_kernel<X, G, false>, smem, a, s);
-    }
-    const size_t smem = pair ? stage_bytes<X, G, 2>() : 0;
-    const bool plain = a.mode == LA_GATE_LOG && !a.compl_in;
-    if (pair) return plain ? launch_scan(glr_bwd_kernel<X, G, true, true>, smem, a, s) : launch_scan(glr_bwd_kernel<X, G, true, false>, smem, a, s);
-    return plain ? launch_scan(glr_bwd_kernel<X, G, false, true>, smem, a, s) : launch_scan(glr_bwd_kernel<X, G, false, false>, smem, a, s);
+la_status scan(Args& a, Maps& maps, Which w, cudaStream_t s) {
+    return w == kFwd ? launch_scan(glr_fwd_kernel<X, G>, stage_bytes<X, G, 1>(), a, maps, s)
+                     : launch_scan(glr_bwd_kernel<X, G>, stage_bytes<X, G, 2>(), a, maps, s);
 }
 
 // The chain's table: maps and states of every item.  None when no sequence can have two blocks.
@@ -631,11 +795,15 @@ la_status run_scan(Args& a, int32_t xd, int32_t gd, Which w, void* ws, cudaStrea
         a.states = reinterpret_cast<uint2*>(static_cast<uint8_t*>(ws) + maps);
         if (cudaMemsetAsync(ws, 0xFF, table_bytes(a.T, a.N, a.D), s) != cudaSuccess) return LA_ERR_CUDA;
     }
-    bool pair = a.D % 2 == 0 && pairs(a.x, a.x_st, a.T, xd) && pairs(a.g, a.g_st, a.T, gd);
-    if (w == kFwd) pair = pair && (!a.h || pairs(a.h, a.h_st, a.T, xd));
-    else pair = pair && pairs(a.dh, a.dh_st, a.T, xd) && pairs(a.dx, a.dx_st, a.T, xd) && pairs(a.dg, a.dg_st, a.T, gd);
-    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? scan<bf16, bf16>(a, w, pair, s) : scan<bf16, float>(a, w, pair, s);
-    return gd == LA_DTYPE_BF16 ? scan<float, bf16>(a, w, pair, s) : scan<float, float>(a, w, pair, s);
+    Maps maps = {};
+    auto tile = [&](CUtensorMap* m, const void* p, int64_t stride, int32_t dtype) {
+        return tileable(p, stride, a.T, a.D, dtype) && tile_map(m, p, stride, a.T, a.D, dtype, kChannels, kWarpRows);
+    };
+    a.tma = tile(&maps.x, a.x, a.x_st, xd) && tile(&maps.g, a.g, a.g_st, gd);
+    if (w == kFwd) a.tma = a.tma && (!a.h || tile(&maps.out, a.h, a.h_st, xd));
+    else a.tma = a.tma && tile(&maps.dh, a.dh, a.dh_st, xd) && tile(&maps.out, a.dx, a.dx_st, xd) && tile(&maps.dg, a.dg, a.dg_st, gd);
+    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? scan<bf16, bf16>(a, maps, w, s) : scan<bf16, float>(a, maps, w, s);
+    return gd == LA_DTYPE_BF16 ? scan<float, bf16>(a, maps, w, s) : scan<float, float>(a, maps, w, s);
 }
 
 template <typename X, typename G>

@@ -1,6 +1,7 @@
 // mixer.cuh -- what the token-mixer operators (glr.cu, gn.cu, sconv.cu) share: element access in
 // bf16 or fp32, activations, the numbering of sequence blocks, and host-side argument checks.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -8,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/liblinattn.h"
+#include "ptx.cuh"
 
 namespace la {
 namespace mixer {
@@ -119,10 +121,51 @@ __device__ __forceinline__ void check_cu(const void* cu, int cu64, int32_t N, in
     if (a < 0 || b < a || b > T || (i == 0 && a != 0) || (i == N - 1 && b != T)) raise_status(status, LA_ERR_BAD_SEQLENS);
 }
 
+// ---------------------------------------------------------------- tiles of a [T, D] operand by TMA
+__device__ __forceinline__ void tile_load(void* dst, const CUtensorMap* map, uint64_t* bar, int channel, int token) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(channel), "r"(token), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tile_store(const CUtensorMap* map, const void* src, int channel, int token) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(channel),
+                 "r"(token), "r"(smem_u32(src))
+                 : "memory");
+}
+
+// Tiles of `rows` tokens x `channels` channels of a [T, D] operand, rows packed in shared memory.
+inline bool tile_map(CUtensorMap* m, const void* p, int64_t stride, int64_t T, int64_t D, int32_t dtype, int channels, int rows) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Encode>(f) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t es = dtype == LA_DTYPE_BF16 ? 2 : 4;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(T == 1 ? (D * es + 15) / 16 * 16 : stride * es)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(channels), static_cast<cuuint32_t>(rows)};
+    const cuuint32_t ones[2] = {1, 1};
+    return encode(m, dtype == LA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                  const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- host checks
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool known_dtype(int32_t d) { return d == LA_DTYPE_BF16 || d == LA_DTYPE_F32; }
 inline int dtype_size(int32_t d) { return d == LA_DTYPE_BF16 ? 2 : 4; }
+// Whether TMA can move tiles of a [T, D] operand: rows on 16-byte boundaries that do not overlap.
+inline bool tileable(const void* p, int64_t stride, int64_t T, int64_t D, int32_t dtype) {
+    return T > 0 && aligned_to(p, 16) && (T == 1 || (stride >= D && stride * dtype_size(dtype) % 16 == 0));
+}
 
 // A [rows, D] operand: non-null when it has elements, element-aligned, rows that an output does not
 // overlap.
