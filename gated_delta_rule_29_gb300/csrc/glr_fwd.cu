@@ -1,0 +1,194 @@
+// glr_fwd.cu -- the forward scan of the gated linear recurrence (glr.cuh has the method).
+#include "glr.cuh"
+
+namespace la {
+namespace glr {
+namespace {
+
+// CTAs of an SM: as many as the staged rows leave room for.
+template <typename X, typename G>
+constexpr int fwd_ctas() { return sizeof(X) + sizeof(G) == 4 ? 5 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
+template <typename X, typename G, int kMode, bool kCompl>
+__global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t stage[];
+    __shared__ Shared sh;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = lane >> 4, c4 = (lane & 15) * 4;
+    X* wx = reinterpret_cast<X*>(stage) + w * kWarpRows * kChannels;                       // the warp's rows
+    G* wg = reinterpret_cast<G*>(stage + sizeof(X) * kBlock * kChannels) + w * kWarpRows * kChannels;
+    X* sx = wx + half * kSpan * kChannels + c4;                                            // the thread's
+    G* sg = wg + half * kSpan * kChannels + c4;
+    if (lane == 0) mbar_init(&sh.bar[w], 1);
+    fence_mbar_init();
+    check_boundaries(a);
+
+    // The warp's rows of an item on their way into shared memory; false when it has none.
+    auto fetch = [&](const Item& it) {
+        const int n = min(it.count - w * kWarpRows, kWarpRows), token = it.start + w * kWarpRows;
+        if (n <= 0) return;
+        if (a.tma) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.bar[w], kWarpRows * kChannels * (sizeof(X) + sizeof(G)));
+                tile_load(wx, &maps.x, &sh.bar[w], it.d, token);
+                tile_load(wg, &maps.g, &sh.bar[w], it.d, token);
+            }
+        } else {
+            rows_in(wx, a.x, a.x_st, token, n, it.d, a.D);
+            rows_in(wg, a.g, a.g_st, token, n, it.d, a.D);
+        }
+    };
+
+    int64_t j = blockIdx.x;
+    uint32_t parity = 0;
+    if (w == 0) locate<false>(a, j, &sh.items[0]);
+    __syncthreads();
+    fetch(sh.items[0]);
+    for (int at = 0;; at ^= 1) {
+        const Item& it = sh.items[at];
+        const int64_t jn = j + gridDim.x;
+        const int rows = min(it.count - w * kWarpRows, kWarpRows);  // of the warp
+        const int n = rows - half * kSpan;                          // of the thread (may exceed kSpan)
+        float2 in = make_float2(0.f, 0.f);
+        if (w == 0 && it.order == 0 && !it.dead && a.s0)
+            load2_any(a.s0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, in.x, in.y);
+        __syncwarp();
+        if (a.tma && rows > 0) {
+            if (!mbar_wait(&sh.bar[w], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            parity ^= 1;
+        }
+        // the map of the thread's span
+        float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+#pragma unroll
+            for (int k = 0; k < kSpan; ++k)
+                if (k < n) {
+                    float x[4], g[4];
+                    get4(sx + k * kChannels, x);
+                    get4(sg + k * kChannels, g);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float dec, m, slope;
+                        gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
+                        cu[i] = fmaf(dec, cu[i], kCompl ? m * x[i] : x[i]);
+                        ca[i] *= dec;
+                    }
+                }
+        }
+        // the other half's: the lower one's map enters the upper one, both make the warp's
+        float oa[4], ou[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            oa[i] = __shfl_xor_sync(0xffffffffu, ca[i], 16);
+            ou[i] = __shfl_xor_sync(0xffffffffu, cu[i], 16);
+        }
+        if (half == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sh.a[w][c4 + i] = ca[i] * oa[i];
+                sh.u[w][c4 + i] = fmaf(oa[i], cu[i], ou[i]);
+            }
+        }
+        __syncthreads();
+        if (w == kWarps - 1 && jn < a.items) locate<false>(a, jn, &sh.items[at ^ 1]);
+        if (w == 0) {
+            float4 map = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 qa = *reinterpret_cast<const float2*>(&sh.a[i][2 * lane]), qu = *reinterpret_cast<const float2*>(&sh.u[i][2 * lane]);
+                map.z = fmaf(qa.x, map.z, qu.x);
+                map.w = fmaf(qa.y, map.w, qu.y);
+                map.x *= qa.x;
+                map.y *= qa.y;
+            }
+            float2 out;
+            chain(a, j, it, map, in, out);
+            *reinterpret_cast<float2*>(&sh.in[2 * lane]) = in;
+            if (!it.dead) {
+                if (a.ckpt && it.count > 0) store2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
+                if (it.last) {
+                    if (a.idx) store2_any(const_cast<void*>(a.s0), it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, out.x, out.y);
+                    else if (a.fin) store2_any(a.fin, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, out.x, out.y);
+                }
+            }
+        }
+        // while the chain goes on: the map of the rows before this warp's (the thread's, in the upper half)
+        float pa[4] = {1.f, 1.f, 1.f, 1.f}, pu[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < w; ++i) {
+            float qa[4], qu[4];
+            get4(&sh.a[i][c4], qa);
+            get4(&sh.u[i][c4], qu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pu[e] = fmaf(qa[e], pu[e], qu[e]);
+                pa[e] *= qa[e];
+            }
+        }
+        if (half == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pu[e] = fmaf(oa[e], pu[e], ou[e]);
+                pa[e] *= oa[e];
+            }
+        }
+        __syncthreads();
+        if (a.h && rows > 0) {
+            float h[4];
+            get4(&sh.in[c4], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = fmaf(pa[e], h[e], pu[e]);
+            {
+#pragma unroll
+                for (int k = 0; k < kSpan; ++k)
+                    if (k < n) {
+                        float x[4], g[4];
+                        get4(sx + k * kChannels, x);
+                        get4(sg + k * kChannels, g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float dec, m, slope;
+                            gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
+                            h[i] = fmaf(dec, h[i], kCompl ? m * x[i] : x[i]);
+                        }
+                        put4(sx + k * kChannels, h);
+                    }
+            }
+            // whole tiles by TMA; the last rows of a sequence one by one
+            if (a.tma && rows == kWarpRows) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tile_store(&maps.out, wx, it.d, it.start + w * kWarpRows);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
+            } else {
+                __syncwarp();
+                rows_out(wx, a.h, a.h_st, it.start + w * kWarpRows, rows, it.d, a.D);
+            }
+        }
+        if (jn >= a.items) break;
+        fence_proxy_async_smem();  // the rows were written here, and are about to be by TMA
+        __syncwarp();
+        fetch(sh.items[at ^ 1]);
+        j = jn;
+    }
+    if (lane == 0) bulk_wait_all();
+}
+
+template <typename X, typename G>
+la_status by_gate(Args& a, Maps& maps, cudaStream_t s) {
+    la_status st = LA_ERR_INVALID_ARG;
+    with_gate(a.mode, a.compl_in, [&](auto gt) {
+        st = launch_scan<glr_fwd_kernel<X, G, decltype(gt)::mode, decltype(gt)::complement>>(stage_bytes<X, G, 1>(), a, maps, s);
+    });
+    return st;
+}
+
+}  // namespace
+
+la_status run_fwd(Args& a, Maps& maps, int32_t xd, int32_t gd, cudaStream_t s) {
+    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? by_gate<bf16, bf16>(a, maps, s) : by_gate<bf16, float>(a, maps, s);
+    return gd == LA_DTYPE_BF16 ? by_gate<float, bf16>(a, maps, s) : by_gate<float, float>(a, maps, s);
+}
+
+}  // namespace glr
+}  // namespace la
