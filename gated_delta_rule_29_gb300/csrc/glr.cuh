@@ -47,18 +47,6 @@ constexpr int kChannels = 64;                    // of a CTA, four a lane
 constexpr uint64_t kWaitNs = 1000000000ull;      // a bounded wait gives up after a second
 static_assert(kBlock == 128, "the checkpoint cadence of the interface");
 
-// e^l as 2^(l log2 e): the product's rounding is off by |l| 2^-24 of the result, which is small where
-// the result is not; results below 2^-126 are zero.
-__device__ __forceinline__ float exp_fast(float l) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l * 1.4426950408889634f));
-    return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 1 - e^l given e^l: the Taylor series (to l^7 / 7!, 2e-7 of it at 1/2) where the difference would cancel.
 __device__ __forceinline__ float one_minus_exp(float l, float e) {
     float p = fmaf(l, 1.f / 7.f, 1.f);

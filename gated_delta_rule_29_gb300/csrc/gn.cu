@@ -8,12 +8,13 @@
 //   dp = dy act'(p)  or  dy act(z),   dz = dy p act'(z),   dw = sum dp n,   db = sum dp,
 //   dn = dp w,   dx = r (dn - [centred] mean(dn) - n mean(dn n)).
 //
-// A row is held in the registers of the lanes that share it (a power of two of lanes up to a warp,
-// or a whole CTA for long rows), so every operand is read once and every result written once;
-// the mean and the variance are two passes over those registers.  The backward recomputes the
-// statistics (they are free beside the row's bytes) and each group of lanes keeps to one head, so
-// that its weight-gradient sums stay in registers over all its rows; the partial sums of all
-// groups are added by a second kernel in a fixed order.
+// A row is held in the registers of the lanes that share it (a power of two of lanes up to a warp, or a
+// whole CTA for long rows), so every operand is read once and every result written once, 16 bytes a
+// lane where the rows' alignment allows; the mean and the variance are two passes over those registers.
+// A group of lanes keeps to one head and steps over the tokens, so that the weights stay in registers.
+// The backward recomputes the statistics (they are free beside the row's bytes) and keeps the weight
+// gradients' sums in registers over all its rows; a CTA adds its groups' sums and a second kernel the
+// CTAs', both in a fixed order.
 #include <algorithm>
 
 #include "mixer.cuh"
@@ -28,12 +29,12 @@ constexpr int kMaxV = 8192;
 struct Args {
     const void *x, *z, *w, *b, *dy;
     int64_t x_st, x_sh, z_st, z_sh, dy_st, dy_sh, y_st, y_sh, dz_st, dz_sh;
-    int64_t rows, units;  // rows T H; groups of lanes that take part (a multiple of H in the backward)
+    int64_t T;
     int H, V, per_head, center, act, w_bf16;
     int lanes;            // lanes that share a row: 1..32 or kThreads
     float eps;
     void *y, *dz;         // y: the result, or dx in the backward
-    float *pw, *pb;       // partial sums [units][V]
+    float *pw, *pb;       // partial sums [CTAs][V]
 };
 
 // Sum over the `lanes` lanes that share a row; kBlock: over the CTA (red has one float per warp).
@@ -52,186 +53,321 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float* red) {
     return v;
 }
 
-// Element k of a lane is channel lane + k * lanes.
-template <typename X, int NE, bool kBlock>
-__device__ __forceinline__ void load_row(float (&v)[NE], const void* base, int64_t at, int lane, int lanes, int V) {
-#pragma unroll
-    for (int k = 0; k < NE; ++k) {
-        const int c = lane + k * lanes;
-        v[k] = c < V ? to_f(static_cast<const X*>(base)[at + c]) : 0.f;
+// The rows of a group of lanes: head h, tokens t0, t0 + step, ...  With weights of their own every CTA
+// keeps to one head (the CTAs' sums are then the heads'); with shared weights neighbouring groups take
+// neighbouring rows, and the groups beyond the last multiple of H have none (t0 = T).
+struct Walk {
+    int h;
+    int64_t t0, step;
+};
+__device__ __forceinline__ Walk walk(const Args& a) {
+    Walk r;
+    const int per_cta = kThreads / a.lanes, u = threadIdx.x / a.lanes;
+    if (a.per_head) {
+        r.h = blockIdx.x % a.H;
+        r.t0 = static_cast<int64_t>(blockIdx.x / a.H) * per_cta + u;
+        r.step = static_cast<int64_t>(gridDim.x / a.H) * per_cta;
+    } else {
+        const int64_t unit = static_cast<int64_t>(blockIdx.x) * per_cta + u;
+        r.step = static_cast<int64_t>(gridDim.x) * per_cta / a.H;
+        r.t0 = unit / a.H;
+        r.h = static_cast<int>(unit - r.t0 * a.H);
+        if (r.t0 >= r.step) r.t0 = a.T;
     }
-}
-
-// x becomes n; returns r.
-template <int NE, bool kBlock>
-__device__ __forceinline__ float normalise(float (&x)[NE], const Args& a, int lane, float* red) {
-    float s = 0.f;
-    if (a.center) {
-#pragma unroll
-        for (int k = 0; k < NE; ++k) s += x[k];
-        const float mu = row_sum<kBlock>(s, a.lanes, red) / a.V;
-#pragma unroll
-        for (int k = 0; k < NE; ++k)
-            if (lane + k * a.lanes < a.V) x[k] -= mu;
-        s = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < NE; ++k) s = fmaf(x[k], x[k], s);
-    const float r = 1.f / sqrtf(row_sum<kBlock>(s, a.lanes, red) / a.V + a.eps);
-#pragma unroll
-    for (int k = 0; k < NE; ++k) x[k] *= r;
     return r;
 }
 
-template <typename X, int NE, bool kBlock>
+// Vector k of a lane starts at channel (lane + k * lanes) * kVec.
+#define LA_EACH_VECTOR(k, c)                                                        \
+    _Pragma("unroll") for (int k = 0; k < NV; ++k) if (const int c = (lane + k * a.lanes) * kVec; c < a.V)
+
+template <typename X, int kVec, int NV>
+__device__ __forceinline__ void load_row(Packed<X, kVec> (&v)[NV], const void* base, int64_t at, bool live, int lane, const Args& a) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (lane + k * a.lanes) * kVec;
+        if (live && c < a.V) v[k].load(static_cast<const X*>(base) + at + c);
+        else v[k].zero();
+    }
+}
+
+// n from a row; returns r.  Places beyond V stay 0.
+template <typename X, int kVec, int NV, bool kBlock>
+__device__ __forceinline__ float normalise(const Packed<X, kVec> (&raw)[NV], float (&x)[NV][kVec], const Args& a, float inv_v, int lane, float* red) {
+    float s = 0.f, mu = 0.f;
+    if (a.center) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s += raw[k].get(i);
+        mu = row_sum<kBlock>(s, a.lanes, red) * inv_v;
+        s = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const bool in = (lane + k * a.lanes) * kVec < a.V;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            x[k][i] = in ? raw[k].get(i) - mu : 0.f;
+            s = fmaf(x[k][i], x[k][i], s);
+        }
+    }
+    const float r = 1.f / sqrtf(row_sum<kBlock>(s, a.lanes, red) * inv_v + a.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[k][i] *= r;
+    return r;
+}
+
+template <int kVec, int NV>
+__device__ __forceinline__ void load_weights(float (&w)[NV][kVec], const void* p, int h, int lane, float missing, const Args& a) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (lane + k * a.lanes) * kVec;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            w[k][i] = p && c < a.V ? load_any(p, (a.per_head ? static_cast<int64_t>(h) * a.V : 0) + c + i, a.w_bf16) : missing;
+    }
+}
+
+template <typename X, int kVec, int NV, bool kBlock>
 __global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const Args a) {
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
-    const int64_t unit = blockIdx.x * static_cast<int64_t>(kThreads / a.lanes) + threadIdx.x / a.lanes;
-    // every lane of a warp runs the same number of rounds: the shuffles need them all
-    const int64_t rounds = (a.rows + a.units - 1) / a.units;
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t row = min(unit + k * a.units, a.rows - 1);
-        const bool live = unit + k * a.units < a.rows;
-        const int64_t t = row / a.H;
-        const int h = static_cast<int>(row % a.H);
-        float x[NE];
-        load_row<X, NE, kBlock>(x, a.x, t * a.x_st + h * a.x_sh, lane, a.lanes, a.V);
-        normalise<NE, kBlock>(x, a, lane, red);
-        const int64_t wo = a.per_head ? static_cast<int64_t>(h) * a.V : 0;
+    const Walk r = walk(a);
+    const int64_t rounds = (a.T + r.step - 1) / r.step;  // the same for every lane of a warp: the shuffles need them all
+    const float inv_v = 1.f / a.V;
+    float w[NV][kVec], b[NV][kVec];
+    load_weights<kVec, NV>(w, a.w, r.h, lane, 0.f, a);
+    load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
+    Packed<X, kVec> raw[NV], z[NV], next[NV], next_z[NV];
+    auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], int64_t t) {
+        load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
+        if (a.z) load_row<X, kVec, NV>(g, a.z, t * a.z_st + r.h * a.z_sh, t < a.T, lane, a);
+    };
+    // short rows: the next one is on its way while this one is worked on
+    constexpr bool kAhead = NV * kVec <= 8;
+    int64_t t = r.t0;
+    if (kAhead) load(next, next_z, t);
+    for (int64_t n = 0; n < rounds; ++n, t += r.step) {
+        const bool live = t < a.T;
+        if (kAhead) {
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const int c = lane + e * a.lanes;
-            if (c >= a.V || !live) continue;
-            float p = x[e] * load_any(a.w, wo + c, a.w_bf16);
-            if (a.b) p += load_any(a.b, wo + c, a.w_bf16);
-            const float y = a.z ? p * act_fwd(a.act, to_f(static_cast<const X*>(a.z)[t * a.z_st + h * a.z_sh + c]))
-                                : act_fwd(a.act, p);
-            static_cast<X*>(a.y)[t * a.y_st + h * a.y_sh + c] = from_f<X>(y);
+            for (int k = 0; k < NV; ++k) {
+                raw[k] = next[k];
+                z[k] = next_z[k];
+            }
+            load(next, next_z, t + r.step);
+        } else {
+            load(raw, z, t);
+        }
+        float x[NV][kVec];
+        normalise<X, kVec, NV, kBlock>(raw, x, a, inv_v, lane, red);
+        if (!live) continue;
+        X* to = static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh;
+        LA_EACH_VECTOR(k, c) {
+            float y[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float p = fmaf(x[k][i], w[k][i], b[k][i]);
+                y[i] = a.z ? p * act_fwd(a.act, z[k].get(i)) : act_fwd(a.act, p);
+            }
+            store_packed<X, kVec>(to + c, y);
         }
     }
 }
 
-template <typename X, int NE, bool kBlock>
+template <typename X, int kVec, int NV, bool kBlock>
 __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const Args a) {
+    extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
-    const int64_t unit = blockIdx.x * static_cast<int64_t>(kThreads / a.lanes) + threadIdx.x / a.lanes;
-    const int64_t rounds = (a.rows + a.units - 1) / a.units;
-    const int64_t wo = a.per_head ? (unit % a.H) * a.V : 0;
-    float w[NE], b[NE], dw[NE], db[NE];
+    const Walk r = walk(a);
+    const int64_t rounds = (a.T + r.step - 1) / r.step;
+    const float inv_v = 1.f / a.V;
+    float w[NV][kVec], b[NV][kVec], dw[NV][kVec] = {}, db[NV][kVec] = {};
+    load_weights<kVec, NV>(w, a.w, r.h, lane, 0.f, a);
+    load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
+    Packed<X, kVec> raw[NV], z[NV], dy[NV], next[NV], next_z[NV], next_dy[NV];
+    auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], Packed<X, kVec> (&d)[NV], int64_t t) {
+        load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
+        load_row<X, kVec, NV>(d, a.dy, t * a.dy_st + r.h * a.dy_sh, t < a.T, lane, a);
+        if (a.z) load_row<X, kVec, NV>(g, a.z, t * a.z_st + r.h * a.z_sh, t < a.T, lane, a);
+    };
+    constexpr bool kAhead = NV * kVec <= 8;
+    int64_t t = r.t0;
+    if (kAhead) load(next, next_z, next_dy, t);
+    for (int64_t round = 0; round < rounds; ++round, t += r.step) {
+        const bool live = t < a.T;
+        if (kAhead) {
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-        const int c = lane + e * a.lanes;
-        dw[e] = db[e] = 0.f;
-        w[e] = c < a.V ? load_any(a.w, wo + c, a.w_bf16) : 0.f;
-        b[e] = c < a.V && a.b ? load_any(a.b, wo + c, a.w_bf16) : 0.f;
-    }
-    for (int64_t k = 0; k < rounds; ++k) {
-        const bool live = unit < a.units && unit + k * a.units < a.rows;
-        const int64_t row = live ? unit + k * a.units : 0;
-        const int64_t t = row / a.H;
-        const int h = static_cast<int>(row % a.H);
-        float n[NE], g[NE];
-        load_row<X, NE, kBlock>(n, a.x, t * a.x_st + h * a.x_sh, lane, a.lanes, a.V);
-        load_row<X, NE, kBlock>(g, a.dy, t * a.dy_st + h * a.dy_sh, lane, a.lanes, a.V);
-        const float r = normalise<NE, kBlock>(n, a, lane, red);
+            for (int k = 0; k < NV; ++k) {
+                raw[k] = next[k];
+                z[k] = next_z[k];
+                dy[k] = next_dy[k];
+            }
+            load(next, next_z, next_dy, t + r.step);
+        } else {
+            load(raw, z, dy, t);
+        }
+        float n[NV][kVec], g[NV][kVec];
+        const float rs = normalise<X, kVec, NV, kBlock>(raw, n, a, inv_v, lane, red);
         float sg = 0.f, sgn = 0.f;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const int c = lane + e * a.lanes;
-            if (c >= a.V) continue;
-            const float p = fmaf(n[e], w[e], b[e]);
-            float d;
-            if (a.z) {
-                const float f = act_grad(a.act, to_f(static_cast<const X*>(a.z)[t * a.z_st + h * a.z_sh + c]), d);
-                if (live) static_cast<X*>(a.dz)[t * a.dz_st + h * a.dz_sh + c] = from_f<X>(g[e] * p * d);
-                g[e] *= f;
-            } else {
-                act_grad(a.act, p, d);
-                g[e] *= d;
-            }
-            if (live) {
-                dw[e] = fmaf(g[e], n[e], dw[e]);
-                db[e] += g[e];
-            }
-            g[e] *= w[e];
-            sg += g[e];
-            sgn = fmaf(g[e], n[e], sgn);
-        }
-        const float mg = a.center ? row_sum<kBlock>(sg, a.lanes, red) / a.V : 0.f;
-        const float mgn = row_sum<kBlock>(sgn, a.lanes, red) / a.V;
+        for (int k = 0; k < NV; ++k) {
+            float dz[kVec];
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const int c = lane + e * a.lanes;
-            if (c < a.V && live)
-                static_cast<X*>(a.y)[t * a.y_st + h * a.y_sh + c] = from_f<X>(r * (g[e] - mg - n[e] * mgn));
+            for (int i = 0; i < kVec; ++i) {
+                const float p = fmaf(n[k][i], w[k][i], b[k][i]);
+                float d, v = dy[k].get(i);  // 0 beyond V and where not live, and so is all that follows from it
+                if (a.z) {
+                    const float f = act_grad(a.act, z[k].get(i), d);
+                    dz[i] = v * p * d;
+                    v *= f;
+                } else {
+                    act_grad(a.act, p, d);
+                    v *= d;
+                }
+                dw[k][i] = fmaf(v, n[k][i], dw[k][i]);
+                db[k][i] += v;
+                v *= w[k][i];
+                g[k][i] = v;
+                sg += v;
+                sgn = fmaf(v, n[k][i], sgn);
+            }
+            const int c = (lane + k * a.lanes) * kVec;
+            if (a.z && live && c < a.V) store_packed<X, kVec>(static_cast<X*>(a.dz) + t * a.dz_st + r.h * a.dz_sh + c, dz);
+        }
+        const float mg = a.center ? row_sum<kBlock>(sg, a.lanes, red) * inv_v : 0.f;
+        const float mgn = row_sum<kBlock>(sgn, a.lanes, red) * inv_v;
+        if (!live) continue;
+        X* to = static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh;
+        LA_EACH_VECTOR(k, c) {
+            float dx[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) dx[i] = rs * (g[k][i] - mg - n[k][i] * mgn);
+            store_packed<X, kVec>(to + c, dx);
         }
     }
-    if (unit >= a.units) return;
+    // the CTA's sums, group by group
+    const int groups = kThreads / a.lanes, u = threadIdx.x / a.lanes;
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-        const int c = lane + e * a.lanes;
-        if (c >= a.V) continue;
-        a.pw[unit * a.V + c] = dw[e];
-        if (a.pb) a.pb[unit * a.V + c] = db[e];
+    for (int which = 0; which < 2; ++which) {
+        float* out = which ? a.pb : a.pw;
+        if (!out) continue;
+        __syncthreads();
+        LA_EACH_VECTOR(k, c) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) sums[u * a.V + c + i] = which ? db[k][i] : dw[k][i];
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.V; c += kThreads) {
+            float s = 0.f;
+            for (int q = 0; q < groups; ++q) s += sums[q * a.V + c];
+            out[static_cast<int64_t>(blockIdx.x) * a.V + c] = s;
+        }
     }
 }
 
-// out[c] = sum of the partial sums of column c: rows c / V, + heads, + 2 heads, ... (per head), or
-// all rows (shared).  A CTA takes 32 columns; its warps take every eighth row, in order.
-__global__ void __launch_bounds__(256) gn_sum_kernel(const float* pw, const float* pb, int64_t units, int V, int heads,
-                                                     void* dw, void* db, int w_bf16) {
-    __shared__ float part[8][33];
+// out[c] = the sum over the CTAs' partial sums of column c: rows c / V, + heads, + 2 heads, ... (per
+// head), or all rows (shared).  A CTA takes 32 columns; its 32 warps take every 32nd row, in order.
+__global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const float* pb, int64_t rows, int V, int heads,
+                                                      void* dw, void* db, int w_bf16) {
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t c = blockIdx.x * 32ll + lane;
     const float* p = blockIdx.y ? pb : pw;
     float s = 0.f;
-    if (c < static_cast<int64_t>(V) * heads)
-        for (int64_t u = c / V + static_cast<int64_t>(w) * heads; u < units; u += 8ll * heads) s += p[u * V + c % V];
+    if (c < static_cast<int64_t>(V) * heads) {
+        const int64_t step = 32ll * heads;
+#pragma unroll 8
+        for (int64_t u = c / V + static_cast<int64_t>(w) * heads; u < rows; u += step) s += p[u * V + c % V];
+    }
     part[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < static_cast<int64_t>(V) * heads) {
-        for (int i = 1; i < 8; ++i) s += part[i][lane];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) s += part[i][lane];
         store_any(blockIdx.y ? db : dw, c, w_bf16, s);
     }
 }
 
-// Lanes that share a row of n elements when each holds at most `most`.
-int row_lanes(int n, int most) {
-    int l = 1;
-    while (l < 32 && l * 4 < n) l *= 2;
-    return l * most >= n ? l : kThreads;
-}
-
+// ---------------------------------------------------------------- shapes
+// How a row is spread over lanes: vectors of 16 bytes, of 8 (bf16), or single elements; as few lanes as
+// hold it at one vector each, up to a warp, then more vectors a lane up to kPerLane elements, then the
+// whole CTA.
 constexpr int kPerLane = 32;
 
-int64_t bwd_units(int64_t rows, int H, int V) {
-    const int per_cta = kThreads / row_lanes(V, kPerLane);
-    int64_t u = std::max<int64_t>(1, std::min<int64_t>(rows / 16, 152 * 8 * static_cast<int64_t>(per_cta)));
-    return (u + H - 1) / H * H;
+struct Shape {
+    int vec, lanes, nv;
+};
+Shape shape(int V, int vec) {
+    Shape s = {vec, 1, 1};
+    const int n = V / vec;
+    while (s.lanes < 32 && s.lanes < n) s.lanes *= 2;
+    if (n > 32 * (kPerLane / vec)) s.lanes = kThreads;
+    s.nv = (n + s.lanes - 1) / s.lanes;
+    return s;
 }
 
-template <typename X, int NE, bool kBlock>
-la_status launch(Args& a, bool bwd, cudaStream_t s) {
-    const int64_t per_cta = kThreads / a.lanes;
+// CTAs of the backward: a few waves' worth, with at least kMinRows rows for a group of lanes, and a
+// multiple of the heads where each CTA keeps to one.  By V alone, not by the alignment, so that the
+// workspace's size follows from the shape.
+constexpr int kMaxCtas = 152 * 6, kMinRows = 8;
+int64_t bwd_ctas(int64_t T, int H, int V, int per_head) {
+    const int64_t rows = T * H, most = rows / kMinRows;
+    // groups of a CTA at single elements a lane, the fewest there can be
+    const int64_t groups = kThreads / shape(V, 1).lanes;
+    int64_t n = std::max<int64_t>(1, std::min<int64_t>(kMaxCtas, most / groups));
+    if (per_head) n = (n + H - 1) / H * H;
+    else n = std::max(n, (H + groups - 1) / groups);
+    return n;
+}
+
+template <typename X, int kVec, int NV, bool kBlock>
+la_status launch(const Args& a, bool bwd, cudaStream_t s) {
+    const int groups = kThreads / a.lanes;
     if (bwd) {
-        const int64_t grid = (a.units + per_cta - 1) / per_cta;
-        gn_bwd_kernel<X, NE, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+        const size_t smem = static_cast<size_t>(groups) * a.V * sizeof(float);
+        const unsigned grid = static_cast<unsigned>(bwd_ctas(a.T, a.H, a.V, a.per_head));
+        gn_bwd_kernel<X, kVec, NV, kBlock><<<grid, kThreads, smem, s>>>(a);
     } else {
-        const int64_t grid = std::min<int64_t>((a.rows + per_cta - 1) / per_cta, 152 * 64);
-        a.units = grid * per_cta;
-        gn_fwd_kernel<X, NE, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 16);
+        if (a.per_head) grid = (grid + a.H - 1) / a.H * a.H;
+        else grid = std::max<int64_t>(grid, (a.H + groups - 1) / groups);
+        gn_fwd_kernel<X, kVec, NV, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
     }
     return launched();
 }
 
+// nv rounded up to what is compiled.
+template <typename X, int kVec>
+la_status by_row(Args& a, bool bwd, cudaStream_t s) {
+    const Shape r = shape(a.V, kVec);
+    constexpr int kMost = kPerLane / kVec;
+    a.lanes = r.lanes;
+    if (r.lanes == kThreads) return launch<X, kVec, kMost, true>(a, bwd, s);
+    if (r.nv == 1) return launch<X, kVec, 1, false>(a, bwd, s);
+    if (r.nv <= kMost / 4) return launch<X, kVec, (kMost / 4 > 1 ? kMost / 4 : 2), false>(a, bwd, s);
+    return launch<X, kVec, kMost, false>(a, bwd, s);
+}
+
 template <typename X>
 la_status dispatch(Args& a, bool bwd, cudaStream_t s) {
-    a.lanes = row_lanes(a.V, kPerLane);
-    if (a.lanes == kThreads) return launch<X, kPerLane, true>(a, bwd, s);
-    if (a.lanes * 4 >= a.V) return launch<X, 4, false>(a, bwd, s);
-    return launch<X, kPerLane, false>(a, bwd, s);
+    auto fits = [&](int bytes) {
+        const int n = bytes / static_cast<int>(sizeof(X));
+        if (a.V % n) return false;
+        auto ok = [&](const void* p, int64_t st, int64_t sh) {
+            return !p || (aligned_to(p, bytes) && (a.T == 1 || st % n == 0) && (a.H == 1 || sh % n == 0));
+        };
+        return ok(a.x, a.x_st, a.x_sh) && ok(a.z, a.z_st, a.z_sh) && ok(a.dy, a.dy_st, a.dy_sh) && ok(a.y, a.y_st, a.y_sh) &&
+               ok(a.dz, a.dz_st, a.dz_sh);
+    };
+    constexpr int kWide = 16 / static_cast<int>(sizeof(X));
+    if (fits(16)) return by_row<X, kWide>(a, bwd, s);
+    if (sizeof(X) == 2 && fits(8)) return by_row<X, 4>(a, bwd, s);
+    return by_row<X, 1>(a, bwd, s);
 }
 
 bool good_thd(const void* p, int64_t st, int64_t sh, int64_t T, int H, int V, int32_t dtype, bool out) {
@@ -258,7 +394,7 @@ extern "C" {
 
 size_t la_gn_bwd_workspace_bytes(int64_t T, int32_t H, int32_t V, int32_t per_head) {
     if (T < 0 || H <= 0 || V <= 0 || V > kMaxV) return 0;
-    return static_cast<size_t>(bwd_units(T * H, H, V)) * V * 2 * 4 + 256;
+    return (static_cast<size_t>(bwd_ctas(T, H, V, per_head != 0)) * V * 2 * 4 + 255) & ~size_t(255);
 }
 
 la_status gn_fwd(const la_gn_fwd_params* p, void* stream) {
@@ -274,7 +410,7 @@ la_status gn_fwd(const la_gn_fwd_params* p, void* stream) {
     a.x = p->x; a.x_st = p->x_stride_t; a.x_sh = p->x_stride_h;
     a.z = p->z; a.z_st = p->z_stride_t; a.z_sh = p->z_stride_h;
     a.w = p->weight; a.b = p->bias; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
-    a.rows = p->T * p->H; a.H = p->H; a.V = p->V;
+    a.T = p->T; a.H = p->H; a.V = p->V;
     a.per_head = p->per_head != 0; a.center = p->center != 0; a.act = p->activation; a.eps = p->eps;
     a.y = p->y; a.y_st = p->y_stride_t; a.y_sh = p->y_stride_h;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -302,24 +438,23 @@ la_status gn_bwd(const la_gn_bwd_params* p, void* stream) {
     a.z = p->z; a.z_st = p->z_stride_t; a.z_sh = p->z_stride_h;
     a.dy = p->dy; a.dy_st = p->dy_stride_t; a.dy_sh = p->dy_stride_h;
     a.w = p->weight; a.b = p->bias; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
-    a.rows = p->T * p->H; a.H = p->H; a.V = p->V;
+    a.T = p->T; a.H = p->H; a.V = p->V;
     a.per_head = p->per_head != 0; a.center = p->center != 0; a.act = p->activation; a.eps = p->eps;
     a.y = p->dx; a.y_st = p->dx_stride_t; a.y_sh = p->dx_stride_h;
     a.dz = p->dz; a.dz_st = p->dz_stride_t; a.dz_sh = p->dz_stride_h;
-    a.units = bwd_units(a.rows, a.H, a.V);
+    int64_t ctas = bwd_ctas(a.T, a.H, a.V, a.per_head);
     a.pw = static_cast<float*>(p->workspace);
-    a.pb = p->bias ? a.pw + a.units * a.V : nullptr;
+    a.pb = p->bias ? a.pw + ctas * a.V : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int64_t units = a.units;
     if (p->T > 0) {
         st = p->x_dtype == LA_DTYPE_BF16 ? dispatch<bf16>(a, true, s) : dispatch<float>(a, true, s);
         if (st != LA_OK) return st;
     } else {
-        units = 0;  // no rows: the sums are zero
+        ctas = 0;  // no rows: the sums are zero
     }
     const int heads = a.per_head ? a.H : 1;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.V) * heads + 31) / 32), a.pb ? 2 : 1);
-    gn_sum_kernel<<<grid, 256, 0, s>>>(a.pw, a.pb, units, a.V, heads, p->d_weight, p->d_bias, a.w_bf16);
+    gn_sum_kernel<<<grid, 1024, 0, s>>>(a.pw, a.pb, ctas, a.V, heads, p->d_weight, p->d_bias, a.w_bf16);
     return launched();
 }
 

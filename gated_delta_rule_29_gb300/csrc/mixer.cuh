@@ -35,9 +35,63 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, float
     else static_cast<float*>(p)[i] = x;
 }
 
-// ---------------------------------------------------------------- activations
+// kVec consecutive elements as one access of kVec * sizeof(T) <= 16 bytes (aligned to that).
+template <typename T, int kVec>
+struct Packed {
+    static constexpr int kWords = (kVec * static_cast<int>(sizeof(T)) + 3) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* p) {
+        if (kVec * sizeof(T) == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+        else if (kVec * sizeof(T) == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+        else if (kVec * sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+        else w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+template <typename T, int kVec>
+__device__ __forceinline__ void store_packed(T* p, const float (&v)[kVec]) {
+    if (sizeof(T) == 4) {
+        if (kVec == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[kVec > 1 ? 1 : 0], v[kVec > 2 ? 2 : 0], v[kVec > 3 ? 3 : 0]);
+        else
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) p[i] = from_f<T>(v[i]);
+    } else if (kVec == 1) {
+        p[0] = from_f<T>(v[0]);
+    } else {
+        uint32_t w[kVec / 2 > 0 ? kVec / 2 : 1];
+#pragma unroll
+        for (int i = 0; i + 1 < kVec; i += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+            w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if (kVec == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[kVec > 2 ? 1 : 0], w[kVec > 4 ? 2 : 0], w[kVec > 6 ? 3 : 0]);
+        else if (kVec == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[kVec > 2 ? 1 : 0]);
+        else *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+}
+
+// ---------------------------------------------------------------- exponentials and activations
+// e^l as 2^(l log2 e): the product's rounding is off by |l| 2^-24 of the result, which is small where
+// the result is not; results below 2^-126 are zero.
+__device__ __forceinline__ float exp_fast(float l) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l * 1.4426950408889634f));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 1 / (1 + e^-x); e^-x may overflow to infinity, which gives the right 0.
-__device__ __forceinline__ float sigmoidf(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoidf(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 
 __device__ __forceinline__ float act_fwd(int kind, float p) {
     if (kind == LA_ACT_NONE) return p;
