@@ -6,22 +6,28 @@
 //   dp_t = dy_t act'(p_t),  dx_t = sum_j w_j dp_{t + (W - 1) - j} (+ the final state's gradient),
 //   dw_j = sum_t dp_t x_{t - (W - 1) + j},  db = sum_t dp_t.
 //
-// A thread walks 16 consecutive tokens of its channels (four, where rows allow 4-element accesses) with
-// the W - 1 tokens before them in registers; the eight warps of a CTA take the eight spans of a 128-token
-// block.  A span's loads are issued in groups ahead of its arithmetic.  The backward recomputes p, looks
-// W - 1 tokens past its span, and leaves one partial sum of dw and db per block (20 bytes a channel for
-// 128 tokens at W = 4), which a second kernel adds in order.
+// The sums over the tokens apart, every token needs its W - 1 neighbours only.  A CTA takes blocks of 128
+// tokens x 64 channels (with their W - 1 rows before, and after in the backward) into shared memory by TMA,
+// the next block on its way while this one is worked on; each warp walks 32 tokens, each lane two channels
+// with the window in registers.  A CTA keeps to one channel tile: the taps stay in registers, and in the
+// backward (which recomputes p) so do the sums of dw and db over all its blocks, which a second kernel adds
+// over the CTAs in order.  Rows that TMA cannot move go through the same shared memory with plain loads.
+// Memory bound by its bytes (2 rows forward, 3 backward), close behind comes the arithmetic: about 16
+// instructions an element forward and 33 backward at W = 4 with the activation's two special functions.
 #include <algorithm>
 
 #include "mixer.cuh"
 
 namespace {
 
+using namespace la;
 using namespace la::mixer;
 
-constexpr int kThreads = 256, kDecodeThreads = 128;
-constexpr int kBlock = 128;
-constexpr int kSpan = kBlock / (kThreads / 32);
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kDecodeThreads = 128;
+constexpr int kBlock = 128, kSpan = kBlock / kWarps;  // tokens of a block, and of a warp
+constexpr int kChannels = 64;                          // of a CTA, two a lane
+constexpr int kSms = 152;
+constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct Args {
     const void *x, *w, *b, *cu, *s0, *dy, *dfin;
@@ -30,8 +36,11 @@ struct Args {
     const int32_t* idx;
     int64_t pool;
     void *y, *fin, *dx, *ds0;
-    float* part;  // [slots][W + 1][D]: dw_0 .. dw_{W-1}, db
+    float* part;     // [columns][W + 1][D]: dw_0 .. dw_{W-1}, db
     int32_t* status;
+    int tiles, columns;  // channel tiles; CTAs of a tile
+    int64_t slots;
+    int tma, pair;   // inputs can move by TMA; results can be stored in pairs
 };
 
 // The state slot of sequence i, or false when its index is outside the pool.
@@ -44,244 +53,322 @@ __device__ __forceinline__ bool state_slot(const Args& a, int i, int64_t& slot) 
     return false;
 }
 
-// The input at place pos < 0 or < len of a sequence: a token, or a row of the state before it.
-template <typename X, int kVec, int W>
-__device__ __forceinline__ void input_at(Packed<X, kVec>& v, const Args& a, int64_t first, int64_t slot, int64_t pos, int d) {
-    if (pos >= 0) v.load(static_cast<const X*>(a.x) + (first + pos) * a.x_st + d);
-    else if (a.s0) v.load(static_cast<const X*>(a.s0) + (slot * (W - 1) + (W - 1) + pos) * a.D + d);
-    else v.zero();
+// Channels d, d + 1 of one row, below D.
+template <typename T>
+__device__ __forceinline__ float2 row2(const void* base, int64_t at, int d, int D) {
+    const T* p = static_cast<const T*>(base) + at;
+    return make_float2(d < D ? to_f(p[d]) : 0.f, d + 1 < D ? to_f(p[d + 1]) : 0.f);
 }
-
-template <int kVec, int W>
-__device__ __forceinline__ void load_taps(float (&w)[W][kVec], float (&bias)[kVec], const Args& a, int d) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = load_any(a.w, static_cast<int64_t>(d + i) * W + j, a.w_bf16);
-        bias[i] = a.b ? load_any(a.b, d + i, a.w_bf16) : 0.f;
+template <typename T>
+__device__ __forceinline__ void put_row2(void* base, int64_t at, int d, int D, int pair, float2 v) {
+    T* p = static_cast<T*>(base) + at + d;
+    if (pair) {
+        const float x[2] = {v.x, v.y};
+        if (d < D) {
+            if (sizeof(T) == 4) *reinterpret_cast<float2*>(p) = v;
+            else store_packed<T, 2>(p, x);
+        }
+        return;
     }
+    if (d < D) p[0] = from_f<T>(v.x);
+    if (d + 1 < D) p[1] = from_f<T>(v.y);
+}
+template <typename T>
+__device__ __forceinline__ float2 staged2(const T* p) {
+    if (sizeof(T) == 4) return *reinterpret_cast<const float2*>(p);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+
+// The input at place pos of the sequence that starts at `first`: a token, or a row of the state before it.
+template <typename X, int W>
+__device__ __forceinline__ float2 input_at(const Args& a, int64_t first, int64_t slot, int64_t pos, int d) {
+    if (pos >= 0) return row2<X>(a.x, (first + pos) * a.x_st, d, a.D);
+    return a.s0 ? row2<X>(a.s0, (slot * (W - 1) + (W - 1) + pos) * a.D, d, a.D) : make_float2(0.f, 0.f);
 }
 
-__device__ __forceinline__ void check_boundaries(const Args& a, int64_t slot) {
-    if (blockIdx.x == 0)
-        for (int64_t i = slot * kThreads + threadIdx.x; i < a.N && i < (slot + 1) * kThreads; i += kThreads)
+template <int W>
+__device__ __forceinline__ void load_taps(float2 (&w)[W], float2& bias, const Args& a, int d) {
+    const bool in0 = d < a.D, in1 = d + 1 < a.D;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        w[j] = make_float2(in0 ? load_any(a.w, static_cast<int64_t>(d) * W + j, a.w_bf16) : 0.f,
+                           in1 ? load_any(a.w, static_cast<int64_t>(d + 1) * W + j, a.w_bf16) : 0.f);
+    bias = a.b ? make_float2(in0 ? load_any(a.b, d, a.w_bf16) : 0.f, in1 ? load_any(a.b, d + 1, a.w_bf16) : 0.f) : make_float2(0.f, 0.f);
+}
+
+struct Maps {
+    CUtensorMap x, dy;
+};
+
+// Rows staged for a block: the W - 1 before it, its own, and in the backward the W - 1 after it.
+template <int W, bool kBackward>
+constexpr int x_rows() { return kBlock + (W - 1) * (kBackward ? 2 : 1); }
+template <int W, bool kBackward>
+constexpr int dy_rows() { return kBackward ? kBlock + W - 1 : 0; }
+template <typename X, int W, bool kBackward>
+constexpr size_t stage_bytes() { return (x_rows<W, kBackward>() + dy_rows<W, kBackward>()) * kChannels * sizeof(X); }
+// 16-bit operands leave room for two stages and enough CTAs; 32-bit ones take more CTAs of one.
+template <typename X>
+constexpr int stages() { return sizeof(X) == 2 ? 2 : 1; }
+
+struct Shared {
+    uint64_t bar[2];
+    SeqBlock block[2];
+};
+
+// The blocks of one CTA, one after the other, in shared memory.
+template <typename X, int W, bool kBackward>
+struct Blocks {
+    const Args& a;
+    const Maps& maps;
+    X* stage;
+    Shared& sh;
+    int tile;
+
+    __device__ __forceinline__ X* x_at(int st) const { return stage + st * (stage_bytes<X, W, kBackward>() / sizeof(X)); }
+    __device__ __forceinline__ X* dy_at(int st) const { return x_at(st) + x_rows<W, kBackward>() * kChannels; }
+
+    // By warp 0: finds the block of a slot and starts its rows on their way.
+    __device__ __forceinline__ void fetch(int64_t slot, int st) const {
+        const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, slot);
+        if ((threadIdx.x & 31) == 0) {
+            sh.block[st] = b;
+            if (a.tma) {
+                const bool any = b.seq >= 0 && b.count > 0;
+                mbar_arrive_expect_tx(&sh.bar[st], any ? static_cast<uint32_t>(stage_bytes<X, W, kBackward>()) : 0u);
+                if (any) {
+                    tile_load(x_at(st), &maps.x, &sh.bar[st], tile * kChannels, b.start - (W - 1));
+                    if (kBackward) tile_load(dy_at(st), &maps.dy, &sh.bar[st], tile * kChannels, b.start);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    // Without TMA, by the whole CTA: rows outside the batch are not read.
+    __device__ __forceinline__ void copy(int st) const {
+        const SeqBlock& b = sh.block[st];
+        if (b.seq < 0 || b.count == 0) return;
+        copy_rows(x_at(st), a.x, a.x_st, b.start - (W - 1), x_rows<W, kBackward>());
+        if (kBackward) copy_rows(dy_at(st), a.dy, a.dy_st, b.start, dy_rows<W, kBackward>());
+    }
+    __device__ __forceinline__ void copy_rows(X* to, const void* base, int64_t stride, int first, int rows) const {
+#pragma unroll 4
+        for (int e = threadIdx.x; e < rows * kChannels; e += kThreads) {
+            const int r = e / kChannels, c = e % kChannels, d = tile * kChannels + c;
+            const int64_t t = static_cast<int64_t>(first) + r;
+            if (t >= 0 && t < a.T && d < a.D) to[e] = static_cast<const X*>(base)[t * stride + d];
+        }
+    }
+    // Calls f(block, x rows, dy rows) for every slot of this CTA.
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        const int warp = threadIdx.x >> 5;
+        const int64_t first = blockIdx.x / a.tiles;
+        if (threadIdx.x == 0) {
+            mbar_init(&sh.bar[0], 1);
+            mbar_init(&sh.bar[1], 1);
+        }
+        fence_mbar_init();
+        __syncthreads();
+        const int depth = a.tma ? stages<X>() : 1;
+        if (warp == 0)
+            for (int k = 0; k < depth; ++k)
+                if (first + static_cast<int64_t>(k) * a.columns < a.slots) fetch(first + static_cast<int64_t>(k) * a.columns, k);
+        uint32_t parity = 0;
+        int st = 0;
+        for (int64_t slot = first; slot < a.slots; slot += a.columns) {
+            if (a.tma) {
+                if (!mbar_wait(&sh.bar[st], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            } else {
+                __syncthreads();
+                copy(st);
+                __syncthreads();
+            }
+            f(sh.block[st], x_at(st), dy_at(st));
+            __syncthreads();  // everybody is done with this stage
+            const int64_t ahead = slot + static_cast<int64_t>(depth) * a.columns;
+            if (warp == 0 && ahead < a.slots) fetch(ahead, st);
+            if (++st == depth) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
+    }
+};
+
+template <typename X, int W>
+__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Shared sh;
+    const int tile = blockIdx.x % a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = tile * kChannels + 2 * lane;
+    if (tile == 0)
+        for (int64_t i = (blockIdx.x / a.tiles) * static_cast<int64_t>(kThreads) + threadIdx.x; i < a.N; i += static_cast<int64_t>(a.columns) * kThreads)
             check_cu(a.cu, a.cu64, a.N, a.T, i, a.status);
+    float2 w[W], bias;
+    load_taps<W>(w, bias, a, d);
+    Blocks<X, W, false> blocks{a, maps, reinterpret_cast<X*>(smem), sh, tile};
+    blocks.each([&](const SeqBlock& b, const X* xs, const X*) {
+        int64_t slot;
+        if (b.seq < 0 || !state_slot(a, b.seq, slot)) return;
+        const int k0 = warp * kSpan, n = min(kSpan, b.count - k0);
+        if (n > 0) {
+            float2 win[W];
+            const X* px = xs + k0 * kChannels + 2 * lane;  // row 0: the token W - 1 before the span
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                win[j + 1] = b.c == 0 && warp == 0 ? input_at<X, W>(a, b.first, slot, j - (W - 1), d) : staged2(px + j * kChannels);
+            px += (W - 1) * kChannels;
+            const int64_t t0 = static_cast<int64_t>(b.start) + k0;
+#pragma unroll 8
+            for (int k = 0; k < kSpan; ++k) {
+                if (k >= n) break;
+#pragma unroll
+                for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
+                win[W - 1] = staged2(px + k * kChannels);
+                float2 p = bias;
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
+                put_row2<X>(a.y, (t0 + k) * a.y_st, d, a.D, a.pair, make_float2(act_fwd(a.act, p.x), act_fwd(a.act, p.y)));
+            }
+        }
+        // The sequence's last W - 1 inputs.  With a pool they replace the rows that the sequence started from,
+        // which only this thread reads: they reach the first W - 1 tokens, and kSpan is no less.
+        if (b.c == 0 && warp == 0 && (a.fin || a.idx)) {
+            float2 f[W - 1];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) f[j] = input_at<X, W>(a, b.first, slot, static_cast<int64_t>(b.len) - (W - 1) + j, d);
+            void* to = a.idx ? const_cast<void*>(a.s0) : a.fin;
+            const int64_t row = (a.idx ? slot : b.seq) * (W - 1);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) put_row2<X>(to, (row + j) * a.D, d, a.D, 0, f[j]);
+        }
+    });
 }
 
-template <typename X, int W, int kVec>
-__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a) {
-    constexpr int kGroup = 8;  // tokens whose loads are issued together
-    const int64_t slot_id = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;
-    const int d = (blockIdx.x * 32 + (threadIdx.x & 31)) * kVec, warp = threadIdx.x >> 5;
-    if (slot_id >= a.T / kBlock + a.N) return;
-    check_boundaries(a, slot_id);
-    const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, slot_id);
-    int64_t slot;
-    if (b.seq < 0 || d >= a.D || !state_slot(a, b.seq, slot)) return;
-    const int k0 = warp * kSpan, n = min(kSpan, b.count - k0);
-    const int64_t p0 = static_cast<int64_t>(b.c) * kBlock + k0;
-    if (n > 0) {
-        float w[W][kVec], bias[kVec], win[W][kVec];
-        Packed<X, kVec> raw[kGroup];
-        Packed<X, kVec> before[W - 1];
+template <typename X, int W>
+__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Shared sh;
+    __shared__ float2 red[kWarps][W + 1][32];
+    const int tile = blockIdx.x % a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = tile * kChannels + 2 * lane;
+    if (tile == 0)
+        for (int64_t i = (blockIdx.x / a.tiles) * static_cast<int64_t>(kThreads) + threadIdx.x; i < a.N; i += static_cast<int64_t>(a.columns) * kThreads)
+            check_cu(a.cu, a.cu64, a.N, a.T, i, a.status);
+    float2 w[W], bias, dw[W], db = make_float2(0.f, 0.f);
+    load_taps<W>(w, bias, a, d);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) input_at<X, kVec, W>(before[j], a, b.first, slot, p0 - (W - 1) + j, d);
-        const X* px = static_cast<const X*>(a.x) + (static_cast<int64_t>(b.start) + k0) * a.x_st + d;
-        X* py = static_cast<X*>(a.y) + (static_cast<int64_t>(b.start) + k0) * a.y_st + d;
-        load_taps<kVec, W>(w, bias, a, d);
+    for (int j = 0; j < W; ++j) dw[j] = make_float2(0.f, 0.f);
+    Blocks<X, W, true> blocks{a, maps, reinterpret_cast<X*>(smem), sh, tile};
+    blocks.each([&](const SeqBlock& b, const X* xs, const X* dys) {
+        if (b.seq < 0) return;
+        const int k0 = warp * kSpan, n = min(kSpan, b.count - k0);
+        // the gradient that the final state's rows bring to the place f - (W - 1) before the sequence's end
+        auto add_final = [&](float2 v, int64_t f) {
+            if (a.dfin && f >= 0) {
+                const float2 e = row2<X>(a.dfin, (b.seq * static_cast<int64_t>(W - 1) + f) * a.D, d, a.D);
+                v.x += e.x;
+                v.y += e.y;
+            }
+            return v;
+        };
+        float2 dp0[W - 1];  // dp of the span's first tokens: what the state's rows reach
+        if (n > 0) {
+            const int64_t p0 = static_cast<int64_t>(b.c) * kBlock + k0, t0 = static_cast<int64_t>(b.start) + k0;
+            const int left = static_cast<int>(min(b.len - p0, static_cast<int64_t>(kSpan + W - 1)));  // tokens to the sequence's end
+            const bool near_end = left < kSpan + W - 1;
+            float2 win[W], dp[W];
+            const X* px = xs + k0 * kChannels + 2 * lane;
+            const X* pd = dys + k0 * kChannels + 2 * lane;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
+            for (int j = 0; j < W - 1; ++j) {
+                win[j + 1] = b.c == 0 && warp == 0 ? input_at<X, W>(a, b.first, b.seq, j - (W - 1), d) : staged2(px + j * kChannels);
+                dp[j + 1] = make_float2(0.f, 0.f);
+            }
+            px += (W - 1) * kChannels;
+            // one token further: win ends with token k, dp with its dp (0 beyond the end)
+            auto step = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) win[j + 1][i] = before[j].get(i);
-#pragma unroll
-        for (int g = 0; g < kSpan; g += kGroup) {
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k)
-                if (g + k < n) raw[k].load(px + (g + k) * a.x_st);
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k)
-                if (g + k < n) {
-                    float y[kVec];
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-                        for (int j = 0; j + 1 < W; ++j) win[j][i] = win[j + 1][i];
-                        win[W - 1][i] = raw[k].get(i);
-                        float p = bias[i];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                        y[i] = act_fwd(a.act, p);
-                    }
-                    store_packed<X, kVec>(py + (g + k) * a.y_st, y);
+                for (int j = 0; j + 1 < W; ++j) {
+                    win[j] = win[j + 1];
+                    dp[j] = dp[j + 1];
                 }
-        }
-    }
-    // The sequence's last W - 1 inputs.  With a pool they replace the rows that the sequence started
-    // from, which only this thread reads: they reach the first W - 1 tokens, and kSpan is no less.
-    if (b.c == 0 && warp == 0 && (a.fin || a.idx)) {
-        Packed<X, kVec> f[W - 1];
+                win[W - 1] = staged2(px + k * kChannels);
+                const float2 dy = staged2(pd + k * kChannels);
+                float2 p = bias, s;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) input_at<X, kVec, W>(f[j], a, b.first, slot, static_cast<int64_t>(b.len) - (W - 1) + j, d);
-        X* to = a.idx ? static_cast<X*>(const_cast<void*>(a.s0)) + slot * (W - 1) * a.D
-                      : static_cast<X*>(a.fin) + static_cast<int64_t>(b.seq) * (W - 1) * a.D;
+                for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
+                act_grad(a.act, p.x, s.x);
+                act_grad(a.act, p.y, s.y);
+                dp[W - 1] = make_float2(dy.x * s.x, dy.y * s.y);
+                if (k >= left) dp[W - 1] = win[W - 1] = make_float2(0.f, 0.f);
+            };
+            auto emit = [&](int k) {  // dx of token k, W - 1 behind
+                if (k < 0 || k >= n) return;
+                float2 dx = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            float v[kVec];
+                for (int j = 0; j < W; ++j) dx = fma2(w[j], dp[W - 1 - j], dx);
+                if (near_end) dx = add_final(dx, p0 + k - (static_cast<int64_t>(b.len) - (W - 1)));
+                put_row2<X>(a.dx, (t0 + k) * a.dx_st, d, a.D, a.pair, dx);
+            };
+            auto sum = [&]() {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] = f[j].get(i);
-            store_packed<X, kVec>(to + static_cast<int64_t>(j) * a.D + d, v);
-        }
-    }
-}
-
-template <typename X, int W, int kVec>
-__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a) {
-    constexpr int kGroup = 4, kSteps = (kSpan + W - 1 + kGroup - 1) / kGroup * kGroup;
-    __shared__ float red[kThreads / 32][W + 1][32 * kVec];
-    const int64_t slot_id = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;
-    const int lane = threadIdx.x & 31, d = (blockIdx.x * 32 + lane) * kVec, warp = threadIdx.x >> 5;
-    if (slot_id >= a.T / kBlock + a.N) return;
-    check_boundaries(a, slot_id);
-    const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, slot_id);
-    const bool mine = b.seq >= 0 && d < a.D;
-    float dw[W][kVec] = {}, db[kVec] = {};
-    const int k0 = warp * kSpan, n = min(kSpan, b.count - k0);
-    const int64_t p0 = static_cast<int64_t>(b.c) * kBlock + k0;
-    if (mine && n > 0) {
-        float w[W][kVec], bias[kVec], win[W][kVec], dp[W][kVec];
-        Packed<X, kVec> before[W - 1], raw[kGroup], raw_dy[kGroup];
+                for (int j = 0; j < W; ++j) dw[j] = fma2(dp[W - 1], win[j], dw[j]);
+                db.x += dp[W - 1].x;
+                db.y += dp[W - 1].y;
+            };
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) input_at<X, kVec, W>(before[j], a, b.first, b.seq, p0 - (W - 1) + j, d);
-        load_taps<kVec, W>(w, bias, a, d);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j + 1][i] = before[j].get(i);
-#pragma unroll
-            for (int j = 0; j < W; ++j) dp[j][i] = 0.f;
-        }
-        const int64_t t0 = static_cast<int64_t>(b.start) + k0;
-        const X* px = static_cast<const X*>(a.x) + t0 * a.x_st + d;
-        const X* pdy = static_cast<const X*>(a.dy) + t0 * a.dy_st + d;
-        X* pdx = static_cast<X*>(a.dx) + t0 * a.dx_st + d;
-        const int left = static_cast<int>(min(b.len - p0, static_cast<int64_t>(kSteps)));  // tokens from here to the sequence's end
-#pragma unroll
-        for (int g = 0; g < kSteps; g += kGroup) {
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k) {
-                if (g + k < kSpan + W - 1 && g + k < left) {
-                    raw[k].load(px + (g + k) * a.x_st);
-                    raw_dy[k].load(pdy + (g + k) * a.dy_st);
-                } else {  // beyond the end: dp = 0
-                    raw[k].zero();
-                    raw_dy[k].zero();
-                }
+            for (int k = 0; k < W - 1; ++k) {
+                step(k);
+                sum();
+                dp0[k] = dp[W - 1];
+            }
+#pragma unroll 4
+            for (int k = W - 1; k < kSpan; ++k) {
+                step(k);
+                sum();
+                emit(k - (W - 1));
             }
 #pragma unroll
-            for (int k = 0; k < kGroup; ++k) {
-                const int at = g + k;  // the token whose dp this step forms; dx follows W - 1 tokens behind
-                if (at >= kSpan + W - 1) continue;
-                float dx[kVec];
+            for (int k = kSpan; k < kSpan + W - 1; ++k) {
+                step(k);
+                emit(k - (W - 1));
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
+            for (int k = 0; k < W - 1; ++k) dp0[k] = make_float2(0.f, 0.f);
+        }
+        // d(initial state): the row at place s - (W - 1) is tap s - t of token t <= s
+        if (b.c == 0 && a.ds0 && warp == 0) {
 #pragma unroll
-                    for (int j = 0; j + 1 < W; ++j) {
-                        win[j][i] = win[j + 1][i];
-                        dp[j][i] = dp[j + 1][i];
-                    }
-                    win[W - 1][i] = raw[k].get(i);
-                    float p = bias[i], slope;
+            for (int s = 0; s < W - 1; ++s) {
+                float2 ds = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                    act_grad(a.act, p, slope);
-                    const float v = at < left ? raw_dy[k].get(i) * slope : 0.f;
-                    dp[W - 1][i] = v;
-                    if (at < kSpan) {
-                        if (at < left) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][i] = fmaf(v, win[j][i], dw[j][i]);
-                            db[i] += v;
-                        }
-                    }
-                    dx[i] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dx[i] = fmaf(w[j][i], dp[W - 1 - j][i], dx[i]);
-                }
-                const int out = at - (W - 1);
-                if (out >= 0 && out < n) {
-                    const int64_t f = p0 + out - (static_cast<int64_t>(b.len) - (W - 1));
-                    if (a.dfin && f >= 0) {
-                        Packed<X, kVec> e;
-                        e.load(static_cast<const X*>(a.dfin) + (b.seq * static_cast<int64_t>(W - 1) + f) * a.D + d);
-#pragma unroll
-                        for (int i = 0; i < kVec; ++i) dx[i] += e.get(i);
-                    }
-                    store_packed<X, kVec>(pdx + out * a.dx_st, dx);
-                }
+                for (int t = 0; t <= s; ++t) ds = fma2(w[s - t], dp0[t], ds);
+                ds = add_final(ds, static_cast<int64_t>(s) - b.len);
+                put_row2<X>(a.ds0, (b.seq * static_cast<int64_t>(W - 1) + s) * a.D, d, a.D, 0, ds);
             }
         }
-    }
-    // d(initial state): the rows before the first token, through the tokens they reach
-    if (mine && b.c == 0 && a.ds0 && warp == 0) {
-        float w[W][kVec], bias[kVec], dp[W - 1][kVec];
-        load_taps<kVec, W>(w, bias, a, d);
+    });
 #pragma unroll
-        for (int t = 0; t < W - 1; ++t) {
-            Packed<X, kVec> in[W], dy;
-            dy.zero();
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (t < b.len) input_at<X, kVec, W>(in[j], a, b.first, b.seq, t - (W - 1) + j, d);
-                else in[j].zero();
-            }
-            if (t < b.len) dy.load(static_cast<const X*>(a.dy) + (static_cast<int64_t>(b.first) + t) * a.dy_st + d);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                float p = bias[i], slope;
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][i], in[j].get(i), p);
-                act_grad(a.act, p, slope);
-                dp[t][i] = t < b.len ? slope * dy.get(i) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < W - 1; ++s) {  // the row at place s - (W - 1) is tap s - t of token t <= s
-            float ds[kVec];
-            Packed<X, kVec> e;
-            e.zero();
-            const int f = s - b.len;
-            if (a.dfin && f >= 0) e.load(static_cast<const X*>(a.dfin) + (b.seq * static_cast<int64_t>(W - 1) + f) * a.D + d);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                ds[i] = e.get(i);
-#pragma unroll
-                for (int t = 0; t <= s; ++t) ds[i] = fmaf(w[s - t][i], dp[t][i], ds[i]);
-            }
-            store_packed<X, kVec>(static_cast<X*>(a.ds0) + (b.seq * static_cast<int64_t>(W - 1) + s) * a.D + d, ds);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) red[warp][j][lane * kVec + i] = dw[j][i];
-        red[warp][W][lane * kVec + i] = db[i];
-    }
+    for (int j = 0; j < W; ++j) red[warp][j][lane] = dw[j];
+    red[warp][W][lane] = db;
     __syncthreads();
-    const int width = min(32 * kVec, a.D - static_cast<int>(blockIdx.x) * 32 * kVec);
-    for (int e = threadIdx.x; e < (W + 1) * 32 * kVec; e += kThreads) {
-        const int j = e / (32 * kVec), c = e % (32 * kVec);
-        if (c >= width) continue;
+    for (int e = threadIdx.x; e < (W + 1) * kChannels; e += kThreads) {
+        const int j = e / kChannels, c = e % kChannels;
+        if (tile * kChannels + c >= a.D) continue;
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) s += red[i][j][c];
-        a.part[(slot_id * (W + 1) + j) * a.D + blockIdx.x * 32 * kVec + c] = s;
+        for (int i = 0; i < kWarps; ++i) s += reinterpret_cast<const float*>(red[i][j])[c];
+        a.part[(static_cast<int64_t>(blockIdx.x / a.tiles) * (W + 1) + j) * a.D + tile * kChannels + c] = s;
     }
 }
 
-// dw[d][j] and db[d]: the partial sums of all slots.  A CTA takes 32 channels of one j; its 32 warps take
-// every 32nd slot, in order.
+// dw[d][j] and db[d]: the partial sums of all columns.  A CTA takes 32 channels of one j; its 32 warps
+// take every 32nd column, in order.
 template <int W>
-__global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int64_t slots, int D, void* dw, void* db,
+__global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int64_t columns, int D, void* dw, void* db,
                                                          int w_bf16) {
     __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.y;
@@ -289,7 +376,7 @@ __global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int6
     float s = 0.f;
     if (d < D) {
 #pragma unroll 8
-        for (int64_t k = warp; k < slots; k += 32) s += part[(k * (W + 1) + j) * D + d];
+        for (int64_t k = warp; k < columns; k += 32) s += part[(k * (W + 1) + j) * D + d];
     }
     sh[warp][lane] = s;
     __syncthreads();
@@ -312,13 +399,12 @@ __global__ void __launch_bounds__(kDecodeThreads) sconv_decode_kernel(const Args
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) in[j].load(st + static_cast<int64_t>(j) * a.D);
     in[W - 1].load(static_cast<const X*>(a.x) + i * a.x_st + d);
-    float w[W][kVec], bias[kVec], y[kVec];
-    load_taps<kVec, W>(w, bias, a, d);
+    float y[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-        float p = bias[e];
+        float p = a.b ? load_any(a.b, d + e, a.w_bf16) : 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(w[j][e], in[j].get(e), p);
+        for (int j = 0; j < W; ++j) p = fmaf(load_any(a.w, static_cast<int64_t>(d + e) * W + j, a.w_bf16), in[j].get(e), p);
         y[e] = act_fwd(a.act, p);
     }
 #pragma unroll
@@ -331,40 +417,69 @@ __global__ void __launch_bounds__(kDecodeThreads) sconv_decode_kernel(const Args
     store_packed<X, kVec>(static_cast<X*>(a.y) + i * a.y_st + d, y);
 }
 
-enum Which { kFwd, kBwd, kDecode };
+// CTAs of a channel tile: what the GPU holds at once (by shared memory, 3 or 6 an SM), no more than slots.
+int64_t bwd_columns(int64_t T, int32_t N, int32_t D) {
+    const int64_t tiles = (D + kChannels - 1) / kChannels;
+    return std::max<int64_t>(1, std::min<int64_t>(T / kBlock + N, kSms * 3 / tiles));
+}
 
-template <typename X, int W, int kVec>
-la_status launch(const Args& a, Which w, cudaStream_t s) {
-    const int64_t blocks = w == kDecode ? a.N : a.T / kBlock + a.N;
-    if (blocks == 0) return LA_OK;
-    const int64_t ny = std::min<int64_t>(blocks, 65535), nz = (blocks + ny - 1) / ny;
-    const int width = (w == kDecode ? kDecodeThreads : 32) * kVec;
-    const dim3 grid((a.D + width - 1) / width, static_cast<unsigned>(ny), static_cast<unsigned>(nz));
-    if (w == kFwd) sconv_fwd_kernel<X, W, kVec><<<grid, kThreads, 0, s>>>(a);
-    else if (w == kBwd) sconv_bwd_kernel<X, W, kVec><<<grid, kThreads, 0, s>>>(a);
-    else sconv_decode_kernel<X, W, kVec><<<grid, kDecodeThreads, 0, s>>>(a);
+template <auto kKernel>
+la_status launch_blocks(size_t smem, const Args& a, const Maps& maps, cudaStream_t s) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LA_ERR_CUDA;
+    }
+    kKernel<<<static_cast<unsigned>(a.tiles * a.columns), kThreads, smem, s>>>(a, maps);
     return launched();
+}
+
+template <typename X, int W>
+la_status run_blocks(Args& a, bool bwd, int32_t xd, cudaStream_t s) {
+    a.tiles = (a.D + kChannels - 1) / kChannels;
+    a.slots = a.T / kBlock + a.N;
+    if (a.slots == 0) return LA_OK;
+    a.columns = static_cast<int>(bwd ? bwd_columns(a.T, a.N, a.D)
+                                     : std::max<int64_t>(1, std::min<int64_t>(a.slots, kSms * 6 / a.tiles)));
+    Maps maps = {};
+    a.tma = tileable(a.x, a.x_st, a.T, a.D, xd) && (!bwd || tileable(a.dy, a.dy_st, a.T, a.D, xd));
+    if (a.tma && bwd)
+        a.tma = tile_map(&maps.x, a.x, a.x_st, a.T, a.D, xd, kChannels, x_rows<W, true>()) &&
+                tile_map(&maps.dy, a.dy, a.dy_st, a.T, a.D, xd, kChannels, dy_rows<W, true>());
+    else if (a.tma)
+        a.tma = tile_map(&maps.x, a.x, a.x_st, a.T, a.D, xd, kChannels, x_rows<W, false>());
+    const void* out = bwd ? a.dx : a.y;
+    const int64_t stride = bwd ? a.dx_st : a.y_st;
+    a.pair = a.D % 2 == 0 && aligned_to(out, 2 * sizeof(X)) && (a.T == 1 || stride % 2 == 0);
+    const int depth = a.tma ? stages<X>() : 1;
+    return bwd ? launch_blocks<sconv_bwd_kernel<X, W>>(depth * stage_bytes<X, W, true>(), a, maps, s)
+               : launch_blocks<sconv_fwd_kernel<X, W>>(depth * stage_bytes<X, W, false>(), a, maps, s);
 }
 
 // Four channels a lane where every operand's rows start on four of its elements.
 template <typename X, int W>
-la_status by_vec(const Args& a, Which w, cudaStream_t s) {
+la_status run_decode(const Args& a, cudaStream_t s) {
+    if (a.N == 0) return LA_OK;
     const int bytes = 4 * static_cast<int>(sizeof(X));
-    auto ok = [&](const void* p, int64_t st) { return !p || (aligned_to(p, bytes) && st % 4 == 0); };
-    const bool four = a.D % 4 == 0 && ok(a.x, a.x_st) && ok(a.y, a.y_st) && ok(a.dy, a.dy_st) && ok(a.dx, a.dx_st) && ok(a.s0, 0) &&
-                      ok(a.fin, 0) && ok(a.dfin, 0) && ok(a.ds0, 0);
-    return four ? launch<X, W, 4>(a, w, s) : launch<X, W, 1>(a, w, s);
+    auto ok = [&](const void* p, int64_t st) { return aligned_to(p, bytes) && st % 4 == 0; };
+    const bool four = a.D % 4 == 0 && ok(a.x, a.x_st) && ok(a.y, a.y_st) && ok(a.s0, 0);
+    const int ny = std::min(a.N, 65535), nz = (a.N + ny - 1) / ny, width = kDecodeThreads * (four ? 4 : 1);
+    const dim3 grid((a.D + width - 1) / width, ny, nz);
+    if (four) sconv_decode_kernel<X, W, 4><<<grid, kDecodeThreads, 0, s>>>(a);
+    else sconv_decode_kernel<X, W, 1><<<grid, kDecodeThreads, 0, s>>>(a);
+    return launched();
 }
 
-template <typename X>
-la_status dispatch_w(const Args& a, int W, Which w, cudaStream_t s) {
-    if (W == 2) return by_vec<X, 2>(a, w, s);
-    if (W == 3) return by_vec<X, 3>(a, w, s);
-    return by_vec<X, 4>(a, w, s);
+enum Which { kFwd, kBwd, kDecode };
+
+template <typename X, int W>
+la_status run(Args& a, Which w, int32_t xd, cudaStream_t s) {
+    return w == kDecode ? run_decode<X, W>(a, s) : run_blocks<X, W>(a, w == kBwd, xd, s);
 }
 
-la_status dispatch(const Args& a, int W, int32_t xd, Which w, cudaStream_t s) {
-    return xd == LA_DTYPE_BF16 ? dispatch_w<bf16>(a, W, w, s) : dispatch_w<float>(a, W, w, s);
+la_status dispatch(Args& a, int W, int32_t xd, Which w, cudaStream_t s) {
+    if (xd == LA_DTYPE_BF16) return W == 2 ? run<bf16, 2>(a, w, xd, s) : W == 3 ? run<bf16, 3>(a, w, xd, s) : run<bf16, 4>(a, w, xd, s);
+    return W == 2 ? run<float, 2>(a, w, xd, s) : W == 3 ? run<float, 3>(a, w, xd, s) : run<float, 4>(a, w, xd, s);
 }
 
 la_status check(int32_t D, int32_t W, int32_t xd, int32_t wd, int32_t act, const void* w, const void* b) {
@@ -381,7 +496,7 @@ extern "C" {
 
 size_t la_sconv_bwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t W) {
     if (T < 0 || N < 0 || D <= 0 || W < 2 || W > 4) return 0;
-    return (static_cast<size_t>(T / kBlock + N) * (W + 1) * D * 4 + 255) & ~size_t(255);
+    return (static_cast<size_t>(bwd_columns(T, N, D)) * (W + 1) * D * 4 + 255) & ~size_t(255);
 }
 
 la_status sconv_fwd(const la_sconv_fwd_params* p, void* stream) {
@@ -428,11 +543,11 @@ la_status sconv_bwd(const la_sconv_bwd_params* p, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = dispatch(a, p->W, p->x_dtype, kBwd, s)) != LA_OK) return st;
     const dim3 grid((a.D + 31) / 32, p->W + (p->bias ? 1 : 0));
-    const int64_t slots = a.T / kBlock + a.N;
+    const int64_t columns = a.slots ? a.columns : 0;
     void* db = p->bias ? p->d_bias : nullptr;
-    if (p->W == 2) sconv_sum_kernel<2><<<grid, 1024, 0, s>>>(a.part, slots, a.D, p->d_weight, db, a.w_bf16);
-    else if (p->W == 3) sconv_sum_kernel<3><<<grid, 1024, 0, s>>>(a.part, slots, a.D, p->d_weight, db, a.w_bf16);
-    else sconv_sum_kernel<4><<<grid, 1024, 0, s>>>(a.part, slots, a.D, p->d_weight, db, a.w_bf16);
+    if (p->W == 2) sconv_sum_kernel<2><<<grid, 1024, 0, s>>>(a.part, columns, a.D, p->d_weight, db, a.w_bf16);
+    else if (p->W == 3) sconv_sum_kernel<3><<<grid, 1024, 0, s>>>(a.part, columns, a.D, p->d_weight, db, a.w_bf16);
+    else sconv_sum_kernel<4><<<grid, 1024, 0, s>>>(a.part, columns, a.D, p->d_weight, db, a.w_bf16);
     return launched();
 }
 
