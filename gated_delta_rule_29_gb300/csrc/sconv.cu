@@ -388,6 +388,17 @@ __global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int6
     }
 }
 
+template <typename T, int kVec, int W>
+__device__ __forceinline__ void load_run(float (&w)[kVec * W], const void* base, int d) {
+#pragma unroll
+    for (int r = 0; r < W; ++r) {
+        Packed<T, kVec> q;
+        q.load(static_cast<const T*>(base) + static_cast<int64_t>(d) * W + r * kVec);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[r * kVec + i] = q.get(i);
+    }
+}
+
 template <typename X, int W, int kVec>
 __global__ void __launch_bounds__(kDecodeThreads) sconv_decode_kernel(const Args a) {
     const int i = blockIdx.y + gridDim.y * blockIdx.z;
@@ -399,12 +410,14 @@ __global__ void __launch_bounds__(kDecodeThreads) sconv_decode_kernel(const Args
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) in[j].load(st + static_cast<int64_t>(j) * a.D);
     in[W - 1].load(static_cast<const X*>(a.x) + i * a.x_st + d);
-    float y[kVec];
+    float w[kVec * W], y[kVec];  // the taps of the thread's channels follow one another
+    if (a.w_bf16) load_run<bf16, kVec, W>(w, a.w, d);
+    else load_run<float, kVec, W>(w, a.w, d);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
         float p = a.b ? load_any(a.b, d + e, a.w_bf16) : 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(load_any(a.w, static_cast<int64_t>(d + e) * W + j, a.w_bf16), in[j].get(e), p);
+        for (int j = 0; j < W; ++j) p = fmaf(w[e * W + j], in[j].get(e), p);
         y[e] = act_fwd(a.act, p);
     }
 #pragma unroll
@@ -462,7 +475,7 @@ la_status run_decode(const Args& a, cudaStream_t s) {
     if (a.N == 0) return LA_OK;
     const int bytes = 4 * static_cast<int>(sizeof(X));
     auto ok = [&](const void* p, int64_t st) { return aligned_to(p, bytes) && st % 4 == 0; };
-    const bool four = a.D % 4 == 0 && ok(a.x, a.x_st) && ok(a.y, a.y_st) && ok(a.s0, 0);
+    const bool four = a.D % 4 == 0 && ok(a.x, a.x_st) && ok(a.y, a.y_st) && ok(a.s0, 0) && aligned_to(a.w, a.w_bf16 ? 8 : 16);
     const int ny = std::min(a.N, 65535), nz = (a.N + ny - 1) / ny, width = kDecodeThreads * (four ? 4 : 1);
     const dim3 grid((a.D + width - 1) / width, ny, nz);
     if (four) sconv_decode_kernel<X, W, 4><<<grid, kDecodeThreads, 0, s>>>(a);

@@ -8,6 +8,7 @@ CUDA kernels.  Outputs and workspaces are allocated on the stream the call runs 
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -33,102 +34,116 @@ def _activation(name) -> int:
         raise ValueError(f"activation must be one of 'none', 'silu', 'sigmoid', got {name!r}") from None
 
 
-def _rows(name: str, x, rank: int, like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """A rank-2 or rank-3 CUDA operand with a contiguous innermost axis; `like`: the operand whose
+def _rows(name: str, x, rank: int, like: Optional[torch.Tensor] = None) -> tuple:
+    """Strides of a rank-2 or rank-3 CUDA operand with a contiguous innermost axis; `like`: the operand whose
     shape and device it must have."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dim() != rank:
-        raise ValueError(f"{name} must be rank {rank}, got shape {tuple(x.shape)}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
+    shape, strides = x.shape, x.stride()
+    if len(shape) != rank:
+        raise ValueError(f"{name} must be rank {rank}, got shape {tuple(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have a contiguous innermost axis")
-    if like is not None and (x.shape != like.shape or x.device != like.device):
-        raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(x.shape)} on {x.device}")
-    return x
+    if like is not None and (shape != like.shape or x.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(shape)} on {x.device}")
+    return strides
 
 
-def _packed(name: str, x, shape: tuple, dtypes: tuple, dev: torch.device) -> torch.Tensor:
-    """A contiguous operand of a known shape (a parameter, a state)."""
-    if not isinstance(x, torch.Tensor) or x.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
+def _packed(name: str, x, shape: tuple, dtypes: tuple, like: torch.Tensor) -> int:
+    """Address of a contiguous operand of a known shape (a parameter, a state) on the device of `like`."""
+    if not isinstance(x, torch.Tensor) or x.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a tensor on {like.device}")
     if x.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
-    if tuple(x.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(x.shape)}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return x
+    return x.data_ptr()
 
 
-def _result(name: str, x: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
-    """A caller's output with the shape and dtype of `like`, or a new contiguous one."""
+def _result(name: str, x: Optional[torch.Tensor], like: torch.Tensor) -> tuple:
+    """A caller's output with the shape and dtype of `like`, or a new contiguous one, and its strides."""
     if x is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _rows(name, x, like.dim(), like)
+        x = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return x, x.stride()
+    strides = _rows(name, x, like.dim(), like)
     if x.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {x.dtype}")
-    return x
+    return x, strides
 
 
-def _state_dest(name: str, x: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, dev) -> torch.Tensor:
+def _state_dest(name: str, x: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, like: torch.Tensor) -> tuple:
     if x is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _packed(name, x, shape, (dtype,), dev)
+        x = like.new_empty(shape, dtype=dtype)
+        return x, x.data_ptr()
+    return x, _packed(name, x, shape, (dtype,), like)
 
 
-def _sequences(p, cu_seqlens: torch.Tensor, dev: torch.device) -> int:
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.device != dev:
-        raise ValueError(f"cu_seqlens must be a tensor on {dev}")
+def _sequences(p, cu_seqlens: torch.Tensor, like: torch.Tensor) -> int:
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.get_device() != like.get_device():
+        raise ValueError(f"cu_seqlens must be a tensor on {like.device}")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous [N + 1] vector")
-    N = cu_seqlens.numel() - 1
-    p.cu_seqlens, p.cu_seqlens_bits, p.N = cu_seqlens.data_ptr(), _cu_bits(cu_seqlens), N
+    p.cu_seqlens, p.cu_seqlens_bits = cu_seqlens.data_ptr(), _cu_bits(cu_seqlens)
+    p.N = N = cu_seqlens.numel() - 1
     return N
 
 
-def _indices(p, state_indices, N: int, dev: torch.device) -> None:
-    if state_indices.dtype != torch.int32 or tuple(state_indices.shape) != (N,) or state_indices.device != dev \
-            or not state_indices.is_contiguous():
-        raise ValueError(f"state_indices must be a contiguous int32 [{N}] vector on {dev}")
+def _indices(p, state_indices, N: int, like: torch.Tensor) -> None:
+    if state_indices.dtype != torch.int32 or state_indices.shape != (N,) \
+            or state_indices.get_device() != like.get_device() or not state_indices.is_contiguous():
+        raise ValueError(f"state_indices must be a contiguous int32 [{N}] vector on {like.device}")
     p.state_indices = state_indices.data_ptr()
 
 
-def _workspace(p, workspace: Optional[torch.Tensor], need: int, dev: torch.device) -> Optional[torch.Tensor]:
+def _workspace(p, workspace: Optional[torch.Tensor], need: int, like: torch.Tensor) -> Optional[torch.Tensor]:
     if workspace is None:
         if need == 0:
             return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {like.device}")
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.nbytes
     return workspace
 
 
-def _status(p, status: Optional[torch.Tensor], dev: torch.device) -> None:
-    if status is not None:
-        if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
-            raise ValueError(f"status must be int32 on {dev}")
-        p.status = status.data_ptr()
+def _status(p, status: torch.Tensor, like: torch.Tensor) -> None:
+    if status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != like.get_device():
+        raise ValueError(f"status must be int32 on {like.device}")
+    p.status = status.data_ptr()
 
 
-class _on:
-    """Makes `stream` current while a call allocates and launches (nothing to do without one)."""
-    __slots__ = ("ctx",)
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on_stream(fn):
+    """Makes a wrapper's `stream` argument the current stream while it runs, so that what it allocates belongs to
+    that stream."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        if kwargs.get("stream") is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(kwargs["stream"]):
+            return fn(*args, **kwargs)
+    return call
 
 
-def _call(name: str, p, dev: torch.device) -> None:
-    B.check(getattr(B.load(), name)(ctypes.byref(p), torch.cuda.current_stream(dev).cuda_stream), name)
+_functions = {}
+
+
+def _call(name: str, p, like: torch.Tensor) -> None:
+    """One library call on the current stream of the operands' device."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(B.load(), name)
+    code = fn(ctypes.byref(p), _raw_stream(like.get_device()))
+    if code:
+        B.check(code, name)
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)  # the same without a Python Stream object
 
 
 # ------------------------------------------------------------------ gated linear recurrence
@@ -142,11 +157,24 @@ def _gate(p, gate_logsigmoid: bool, gate_lower_bound: Optional[float], complemen
     p.complement_input = int(bool(complement_input))
 
 
+_STATE_DTYPES = (torch.float32, torch.bfloat16)
+_FP32 = (torch.float32,)
+
+
 def glr_checkpoint_rows(T: int, N: int) -> int:
     """Rows of glr_fwd's checkpoints for T tokens in N sequences."""
     return int(B.load().la_glr_checkpoint_rows(int(T), int(N)))
 
 
+def _glr_inputs(p, x, g, gate_logsigmoid, gate_lower_bound, complement_input) -> tuple:
+    xs, gs = _rows("x", x, 2), _rows("g", g, 2, x)
+    p.x, p.x_dtype, p.g, p.g_dtype = x.data_ptr(), _dtype("x", x), g.data_ptr(), _dtype("g", g)
+    if gate_logsigmoid or gate_lower_bound is not None or complement_input:
+        _gate(p, gate_logsigmoid, gate_lower_bound, complement_input)
+    return xs[0], gs[0]
+
+
+@_on_stream
 def glr_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor, *,
             initial_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
             gate_logsigmoid: bool = False, gate_lower_bound: Optional[float] = None,
@@ -165,42 +193,39 @@ def glr_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor, *,
 
     output_checkpoints keeps the fp32 state entering every 128-token block for glr_bwd.  state_indices ([N]
     int32): initial_state is then a pool [P, D] and each sequence's end state is written back to its slot."""
-    with _on(stream):
-        p = B.GlrFwdParams()
-        _rows("x", x, 2)
-        _rows("g", g, 2, x)
-        T, D = x.shape
-        dev = x.device
-        N = _sequences(p, cu_seqlens, dev)
-        p.x, p.x_stride_t, p.x_dtype = x.data_ptr(), x.stride(0), _dtype("x", x)
-        p.g, p.g_stride_t, p.g_dtype = g.data_ptr(), g.stride(0), _dtype("g", g)
-        p.T, p.D = T, D
-        _gate(p, gate_logsigmoid, gate_lower_bound, complement_input)
-        if state_indices is not None:
-            if initial_state is None or initial_state.dim() != 2:
-                raise ValueError("state_indices needs initial_state as a contiguous pool [P, D]")
-            if final_state is not None:
-                raise ValueError("state_indices and final_state are exclusive")
-            _indices(p, state_indices, N, dev)
-            p.state_pool_size = initial_state.shape[0]
-            output_final_state = False
-        if initial_state is not None:
-            rows = N if state_indices is None else initial_state.shape[0]
-            _packed("initial_state", initial_state, (rows, D), (torch.float32, torch.bfloat16), dev)
-            p.initial_state, p.initial_state_dtype = initial_state.data_ptr(), _dtype("initial_state", initial_state)
-        h = _result("h", h, x)
-        p.h, p.h_stride_t = h.data_ptr(), h.stride(0)
-        final_state = _state_dest("final_state", final_state, (N, D), torch.float32, dev) if output_final_state else None
-        p.final_state = final_state.data_ptr() if final_state is not None else None
-        if output_checkpoints or checkpoints is not None:
-            checkpoints = _state_dest("checkpoints", checkpoints, (glr_checkpoint_rows(T, N), D), torch.float32, dev)
-            p.checkpoints = checkpoints.data_ptr()
-        ws = _workspace(p, workspace, B.load().la_glr_workspace_bytes(T, N, D, 0, 0), dev)  # noqa: F841
-        _status(p, status, dev)
-        _call("glr_fwd", p, dev)
+    p = B.GlrFwdParams()
+    p.x_stride_t, p.g_stride_t = _glr_inputs(p, x, g, gate_logsigmoid, gate_lower_bound, complement_input)
+    p.T, p.D = T, D = x.shape
+    N = _sequences(p, cu_seqlens, x)
+    if state_indices is not None:
+        if initial_state is None or initial_state.dim() != 2:
+            raise ValueError("state_indices needs initial_state as a contiguous pool [P, D]")
+        if final_state is not None:
+            raise ValueError("state_indices and final_state are exclusive")
+        _indices(p, state_indices, N, x)
+        p.state_pool_size = initial_state.shape[0]
+        output_final_state = False
+    if initial_state is not None:
+        rows = N if state_indices is None else initial_state.shape[0]
+        p.initial_state = _packed("initial_state", initial_state, (rows, D), _STATE_DTYPES, x)
+        p.initial_state_dtype = _DTYPES[initial_state.dtype]
+    h, strides = _result("h", h, x)
+    p.h, p.h_stride_t = h.data_ptr(), strides[0]
+    if output_final_state:
+        final_state, p.final_state = _state_dest("final_state", final_state, (N, D), torch.float32, x)
+    else:
+        final_state = None
+    if output_checkpoints or checkpoints is not None:
+        checkpoints, p.checkpoints = _state_dest("checkpoints", checkpoints, (glr_checkpoint_rows(T, N), D),
+                                                 torch.float32, x)
+    ws = _workspace(p, workspace, B.load().la_glr_workspace_bytes(T, N, D, 0, 0), x)  # noqa: F841
+    if status is not None:
+        _status(p, status, x)
+    _call("glr_fwd", p, x)
     return h, final_state, checkpoints
 
 
+@_on_stream
 def glr_bwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor, d_h: torch.Tensor, *,
             initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None,
             checkpoints: Optional[torch.Tensor] = None, gate_logsigmoid: bool = False,
@@ -212,40 +237,35 @@ def glr_bwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor, d_h: tor
     """Gradients of sum(d_h * h) + sum(d_final_state * final_state) for glr_fwd with the same inputs.  Returns (dx
     in x's dtype, dg of g as given in g's dtype, d_initial_state [N, D] fp32).  checkpoints: the forward's; without
     them the states are recomputed (one more forward pass)."""
-    with _on(stream):
-        p = B.GlrBwdParams()
-        _rows("x", x, 2)
-        _rows("g", g, 2, x)
-        _rows("d_h", d_h, 2, x)
-        if d_h.dtype != x.dtype:
-            raise TypeError(f"d_h must be {x.dtype}, got {d_h.dtype}")
-        T, D = x.shape
-        dev = x.device
-        N = _sequences(p, cu_seqlens, dev)
-        p.x, p.x_stride_t, p.x_dtype = x.data_ptr(), x.stride(0), _dtype("x", x)
-        p.g, p.g_stride_t, p.g_dtype = g.data_ptr(), g.stride(0), _dtype("g", g)
-        p.d_h, p.d_h_stride_t = d_h.data_ptr(), d_h.stride(0)
-        p.T, p.D = T, D
-        _gate(p, gate_logsigmoid, gate_lower_bound, complement_input)
-        if initial_state is not None:
-            _packed("initial_state", initial_state, (N, D), (torch.float32, torch.bfloat16), dev)
-            p.initial_state, p.initial_state_dtype = initial_state.data_ptr(), _dtype("initial_state", initial_state)
-        if d_final_state is not None:
-            p.d_final_state = _packed("d_final_state", d_final_state, (N, D), (torch.float32,), dev).data_ptr()
-        if checkpoints is not None:
-            p.checkpoints = _packed("checkpoints", checkpoints, (glr_checkpoint_rows(T, N), D), (torch.float32,),
-                                    dev).data_ptr()
-        dx, dg = _result("dx", dx, x), _result("dg", dg, g)
-        p.dx, p.dx_stride_t, p.dg, p.dg_stride_t = dx.data_ptr(), dx.stride(0), dg.data_ptr(), dg.stride(0)
-        d_initial_state = _state_dest("d_initial_state", d_initial_state, (N, D), torch.float32, dev)
-        p.d_initial_state = d_initial_state.data_ptr()
-        need = B.load().la_glr_workspace_bytes(T, N, D, 1, int(checkpoints is not None))
-        ws = _workspace(p, workspace, need, dev)  # noqa: F841
-        _status(p, status, dev)
-        _call("glr_bwd", p, dev)
+    p = B.GlrBwdParams()
+    p.x_stride_t, p.g_stride_t = _glr_inputs(p, x, g, gate_logsigmoid, gate_lower_bound, complement_input)
+    p.T, p.D = T, D = x.shape
+    N = _sequences(p, cu_seqlens, x)
+    p.d_h_stride_t = _rows("d_h", d_h, 2, x)[0]
+    if d_h.dtype != x.dtype:
+        raise TypeError(f"d_h must be {x.dtype}, got {d_h.dtype}")
+    p.d_h = d_h.data_ptr()
+    if initial_state is not None:
+        p.initial_state = _packed("initial_state", initial_state, (N, D), _STATE_DTYPES, x)
+        p.initial_state_dtype = _DTYPES[initial_state.dtype]
+    if d_final_state is not None:
+        p.d_final_state = _packed("d_final_state", d_final_state, (N, D), _FP32, x)
+    if checkpoints is not None:
+        p.checkpoints = _packed("checkpoints", checkpoints, (glr_checkpoint_rows(T, N), D), _FP32, x)
+    dx, strides = _result("dx", dx, x)
+    p.dx, p.dx_stride_t = dx.data_ptr(), strides[0]
+    dg, strides = _result("dg", dg, g)
+    p.dg, p.dg_stride_t = dg.data_ptr(), strides[0]
+    d_initial_state, p.d_initial_state = _state_dest("d_initial_state", d_initial_state, (N, D), torch.float32, x)
+    need = B.load().la_glr_workspace_bytes(T, N, D, 1, checkpoints is not None)
+    ws = _workspace(p, workspace, need, x)  # noqa: F841
+    if status is not None:
+        _status(p, status, x)
+    _call("glr_bwd", p, x)
     return dx, dg, d_initial_state
 
 
+@_on_stream
 def glr_decode(x: torch.Tensor, g: torch.Tensor, state_pool: torch.Tensor, *,
                state_indices: Optional[torch.Tensor] = None, gate_logsigmoid: bool = False,
                gate_lower_bound: Optional[float] = None, complement_input: bool = False,
@@ -253,52 +273,46 @@ def glr_decode(x: torch.Tensor, g: torch.Tensor, state_pool: torch.Tensor, *,
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One recurrence step for each of N sequences: x, g [N, D]; sequence i steps pool[state_indices[i]] (pool[i]
     without indices) of state_pool [P, D] (fp32 or bf16) in place.  Returns h [N, D] in x's dtype."""
-    with _on(stream):
-        p = B.GlrDecodeParams()
-        _rows("x", x, 2)
-        _rows("g", g, 2, x)
-        N, D = x.shape
-        dev = x.device
-        if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 2:
-            raise ValueError("state_pool must be a contiguous [P, D] tensor")
-        P = state_pool.shape[0]
-        _packed("state_pool", state_pool, (P, D), (torch.float32, torch.bfloat16), dev)
-        p.x, p.x_stride_n, p.x_dtype = x.data_ptr(), x.stride(0), _dtype("x", x)
-        p.g, p.g_stride_n, p.g_dtype = g.data_ptr(), g.stride(0), _dtype("g", g)
-        p.N, p.D = N, D
-        _gate(p, gate_logsigmoid, gate_lower_bound, complement_input)
-        p.state_pool, p.state_dtype, p.state_pool_size = state_pool.data_ptr(), _dtype("state_pool", state_pool), P
-        if state_indices is not None:
-            _indices(p, state_indices, N, dev)
-        h = _result("h", h, x)
-        p.h, p.h_stride_n = h.data_ptr(), h.stride(0)
-        _status(p, status, dev)
-        _call("glr_decode", p, dev)
+    p = B.GlrDecodeParams()
+    p.x_stride_n, p.g_stride_n = _glr_inputs(p, x, g, gate_logsigmoid, gate_lower_bound, complement_input)
+    p.N, p.D = N, D = x.shape
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 2:
+        raise ValueError("state_pool must be a contiguous [P, D] tensor")
+    p.state_pool_size = P = state_pool.shape[0]
+    p.state_pool = _packed("state_pool", state_pool, (P, D), _STATE_DTYPES, x)
+    p.state_dtype = _DTYPES[state_pool.dtype]
+    if state_indices is not None:
+        _indices(p, state_indices, N, x)
+    h, strides = _result("h", h, x)
+    p.h, p.h_stride_n = h.data_ptr(), strides[0]
+    if status is not None:
+        _status(p, status, x)
+    _call("glr_decode", p, x)
     return h
 
 
 # ------------------------------------------------------------------ group norm
-def _gn_common(p, x, weight, bias, z, center, activation, eps):
-    _rows("x", x, 3)
-    T, H, V = x.shape
-    dev = x.device
+def _gn_inputs(p, x, weight, bias, z, center, activation, eps) -> None:
+    _, p.x_stride_h, _ = strides = _rows("x", x, 3)
+    p.x, p.x_stride_t, p.x_dtype = x.data_ptr(), strides[0], _dtype("x", x)
+    p.T, p.H, p.V = _, H, V = x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
         raise ValueError("weight must be [V] or [H, V]")
-    shape = (V,) if weight.dim() == 1 else (H, V)
-    _packed("weight", weight, shape, (torch.float32, torch.bfloat16), dev)
+    per_head = weight.dim() == 2
+    shape = (H, V) if per_head else (V,)
+    p.weight, p.per_head = _packed("weight", weight, shape, _STATE_DTYPES, x), per_head
+    p.weight_dtype = _DTYPES[weight.dtype]
     if bias is not None:
-        p.bias = _packed("bias", bias, shape, (weight.dtype,), dev).data_ptr()
+        p.bias = _packed("bias", bias, shape, (weight.dtype,), x)
     if z is not None:
-        _rows("z", z, 3, x)
+        strides = _rows("z", z, 3, x)
         if z.dtype != x.dtype:
             raise TypeError(f"z must be {x.dtype}, got {z.dtype}")
-        p.z, p.z_stride_t, p.z_stride_h = z.data_ptr(), z.stride(0), z.stride(1)
-    p.x, p.x_stride_t, p.x_stride_h, p.x_dtype = x.data_ptr(), x.stride(0), x.stride(1), _dtype("x", x)
-    p.weight, p.weight_dtype, p.per_head = weight.data_ptr(), _dtype("weight", weight), int(weight.dim() == 2)
-    p.T, p.H, p.V = T, H, V
-    p.center, p.activation, p.eps = int(bool(center)), _activation(activation), float(eps)
+        p.z, p.z_stride_t, p.z_stride_h = z.data_ptr(), strides[0], strides[1]
+    p.center, p.activation, p.eps = bool(center), _activation(activation), eps
 
 
+@_on_stream
 def gn_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
            z: Optional[torch.Tensor] = None, center: bool = True, activation: Optional[str] = "silu",
            eps: float = 1e-5, y: Optional[torch.Tensor] = None,
@@ -306,61 +320,62 @@ def gn_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     """Group norm of every head's V channels of every token, x [T, H, V] (bf16 or fp32), with an activation:
     p = n weight + bias, y = activation(p) without z, y = p * activation(z) with the gate z [T, H, V].
     weight and bias are [V] (shared by the heads) or [H, V]; center=False leaves the mean in (RMS norm)."""
-    with _on(stream):
-        p = B.GnFwdParams()
-        _gn_common(p, x, weight, bias, z, center, activation, eps)
-        y = _result("y", y, x)
-        p.y, p.y_stride_t, p.y_stride_h = y.data_ptr(), y.stride(0), y.stride(1)
-        _call("gn_fwd", p, x.device)
+    p = B.GnFwdParams()
+    _gn_inputs(p, x, weight, bias, z, center, activation, eps)
+    y, strides = _result("y", y, x)
+    p.y, p.y_stride_t, p.y_stride_h = y.data_ptr(), strides[0], strides[1]
+    _call("gn_fwd", p, x)
     return y
 
 
+@_on_stream
 def gn_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
            z: Optional[torch.Tensor] = None, center: bool = True, activation: Optional[str] = "silu",
            eps: float = 1e-5, dx: Optional[torch.Tensor] = None, dz: Optional[torch.Tensor] = None,
            workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
            ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
     """Gradients of sum(dy * y) for gn_fwd with the same inputs: (dx, d_weight, d_bias or None, dz or None)."""
-    with _on(stream):
-        p = B.GnBwdParams()
-        _gn_common(p, x, weight, bias, z, center, activation, eps)
-        _rows("dy", dy, 3, x)
-        if dy.dtype != x.dtype:
-            raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
-        p.dy, p.dy_stride_t, p.dy_stride_h = dy.data_ptr(), dy.stride(0), dy.stride(1)
-        dx = _result("dx", dx, x)
-        p.dx, p.dx_stride_t, p.dx_stride_h = dx.data_ptr(), dx.stride(0), dx.stride(1)
-        if z is not None:
-            dz = _result("dz", dz, x)
-            p.dz, p.dz_stride_t, p.dz_stride_h = dz.data_ptr(), dz.stride(0), dz.stride(1)
-        else:
-            dz = None
-        d_weight = torch.empty_like(weight)
-        p.d_weight = d_weight.data_ptr()
-        d_bias = torch.empty_like(bias) if bias is not None else None
-        p.d_bias = d_bias.data_ptr() if bias is not None else None
-        need = B.load().la_gn_bwd_workspace_bytes(p.T, p.H, p.V, p.per_head)
-        ws = _workspace(p, workspace, need, x.device)  # noqa: F841
-        _call("gn_bwd", p, x.device)
+    p = B.GnBwdParams()
+    _gn_inputs(p, x, weight, bias, z, center, activation, eps)
+    strides = _rows("dy", dy, 3, x)
+    if dy.dtype != x.dtype:
+        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    p.dy, p.dy_stride_t, p.dy_stride_h = dy.data_ptr(), strides[0], strides[1]
+    dx, strides = _result("dx", dx, x)
+    p.dx, p.dx_stride_t, p.dx_stride_h = dx.data_ptr(), strides[0], strides[1]
+    if z is not None:
+        dz, strides = _result("dz", dz, x)
+        p.dz, p.dz_stride_t, p.dz_stride_h = dz.data_ptr(), strides[0], strides[1]
+    else:
+        dz = None
+    d_weight = torch.empty_like(weight)
+    p.d_weight = d_weight.data_ptr()
+    d_bias = None
+    if bias is not None:
+        d_bias = torch.empty_like(bias)
+        p.d_bias = d_bias.data_ptr()
+    ws = _workspace(p, workspace, B.load().la_gn_bwd_workspace_bytes(p.T, p.H, p.V, p.per_head), x)  # noqa: F841
+    _call("gn_bwd", p, x)
     return dx, d_weight, d_bias, dz
 
 
 # ------------------------------------------------------------------ short convolution
-def _sconv_common(p, x, weight, bias, activation) -> Tuple[int, int]:
-    _rows("x", x, 2)
-    D, dev = x.shape[1], x.device
+def _sconv_inputs(p, x, weight, bias, activation) -> int:
+    """Fills in the operands; returns x's row stride."""
+    strides = _rows("x", x, 2)
+    D = x.shape[1]
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [D, W]")
     W = weight.shape[1]
-    _packed("weight", weight, (D, W), (torch.float32, torch.bfloat16), dev)
+    p.weight, p.weight_dtype = _packed("weight", weight, (D, W), _STATE_DTYPES, x), _DTYPES[weight.dtype]
     if bias is not None:
-        p.bias = _packed("bias", bias, (D,), (weight.dtype,), dev).data_ptr()
-    p.weight, p.weight_dtype = weight.data_ptr(), _dtype("weight", weight)
+        p.bias = _packed("bias", bias, (D,), (weight.dtype,), x)
     p.x, p.x_dtype = x.data_ptr(), _dtype("x", x)
     p.D, p.W, p.activation = D, W, _activation(activation)
-    return D, W
+    return strides[0]
 
 
+@_on_stream
 def sconv_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
               activation: Optional[str] = "silu", initial_state: Optional[torch.Tensor] = None,
               output_final_state: bool = True, state_indices: Optional[torch.Tensor] = None,
@@ -373,32 +388,35 @@ def sconv_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, b
 
     initial_state [N, W - 1, D]: the tokens before each sequence's first (zeros without one).  state_indices ([N]
     int32): initial_state is then a pool [P, W - 1, D], updated in place, and no final_state is returned."""
-    with _on(stream):
-        p = B.SconvFwdParams()
-        D, W = _sconv_common(p, x, weight, bias, activation)
-        dev = x.device
-        N = _sequences(p, cu_seqlens, dev)
-        p.T, p.x_stride_t = x.shape[0], x.stride(0)
-        if state_indices is not None:
-            if initial_state is None or initial_state.dim() != 3:
-                raise ValueError("state_indices needs initial_state as a contiguous pool [P, W - 1, D]")
-            if final_state is not None:
-                raise ValueError("state_indices and final_state are exclusive")
-            _indices(p, state_indices, N, dev)
-            p.state_pool_size = initial_state.shape[0]
-            output_final_state = False
-        if initial_state is not None:
-            rows = N if state_indices is None else initial_state.shape[0]
-            p.initial_state = _packed("initial_state", initial_state, (rows, W - 1, D), (x.dtype,), dev).data_ptr()
-        y = _result("y", y, x)
-        p.y, p.y_stride_t = y.data_ptr(), y.stride(0)
-        final_state = _state_dest("final_state", final_state, (N, W - 1, D), x.dtype, dev) if output_final_state else None
-        p.final_state = final_state.data_ptr() if final_state is not None else None
-        _status(p, status, dev)
-        _call("sconv_fwd", p, dev)
+    p = B.SconvFwdParams()
+    p.x_stride_t = _sconv_inputs(p, x, weight, bias, activation)
+    p.T, D = x.shape
+    rows = weight.shape[1] - 1
+    N = _sequences(p, cu_seqlens, x)
+    states = N
+    if state_indices is not None:
+        if initial_state is None or initial_state.dim() != 3:
+            raise ValueError("state_indices needs initial_state as a contiguous pool [P, W - 1, D]")
+        if final_state is not None:
+            raise ValueError("state_indices and final_state are exclusive")
+        _indices(p, state_indices, N, x)
+        p.state_pool_size = states = initial_state.shape[0]
+        output_final_state = False
+    if initial_state is not None:
+        p.initial_state = _packed("initial_state", initial_state, (states, rows, D), (x.dtype,), x)
+    y, strides = _result("y", y, x)
+    p.y, p.y_stride_t = y.data_ptr(), strides[0]
+    if output_final_state:
+        final_state, p.final_state = _state_dest("final_state", final_state, (N, max(rows, 0), D), x.dtype, x)
+    else:
+        final_state = None
+    if status is not None:
+        _status(p, status, x)
+    _call("sconv_fwd", p, x)
     return y, final_state
 
 
+@_on_stream
 def sconv_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, dy: torch.Tensor,
               bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
               initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None,
@@ -407,57 +425,57 @@ def sconv_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, d
               ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], torch.Tensor]:
     """Gradients of sum(dy * y) + sum(d_final_state * final_state) for sconv_fwd with the same inputs: (dx, d_weight,
     d_bias or None, d_initial_state [N, W - 1, D] in x's dtype)."""
-    with _on(stream):
-        p = B.SconvBwdParams()
-        D, W = _sconv_common(p, x, weight, bias, activation)
-        dev = x.device
-        N = _sequences(p, cu_seqlens, dev)
-        _rows("dy", dy, 2, x)
-        if dy.dtype != x.dtype:
-            raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
-        T = x.shape[0]
-        p.T, p.x_stride_t = T, x.stride(0)
-        p.dy, p.dy_stride_t = dy.data_ptr(), dy.stride(0)
-        if initial_state is not None:
-            p.initial_state = _packed("initial_state", initial_state, (N, W - 1, D), (x.dtype,), dev).data_ptr()
-        if d_final_state is not None:
-            p.d_final_state = _packed("d_final_state", d_final_state, (N, W - 1, D), (x.dtype,), dev).data_ptr()
-        dx = _result("dx", dx, x)
-        p.dx, p.dx_stride_t = dx.data_ptr(), dx.stride(0)
-        d_weight = torch.empty_like(weight)
-        p.d_weight = d_weight.data_ptr()
-        d_bias = torch.empty_like(bias) if bias is not None else None
-        p.d_bias = d_bias.data_ptr() if bias is not None else None
-        d_initial_state = torch.empty((N, W - 1, D), dtype=x.dtype, device=dev)
-        p.d_initial_state = d_initial_state.data_ptr()
-        ws = _workspace(p, workspace, B.load().la_sconv_bwd_workspace_bytes(T, N, D, W), dev)  # noqa: F841
-        _status(p, status, dev)
-        _call("sconv_bwd", p, dev)
+    p = B.SconvBwdParams()
+    p.x_stride_t = _sconv_inputs(p, x, weight, bias, activation)
+    p.T, D = T, _ = x.shape
+    W = weight.shape[1]
+    N = _sequences(p, cu_seqlens, x)
+    p.dy_stride_t = _rows("dy", dy, 2, x)[0]
+    if dy.dtype != x.dtype:
+        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    p.dy = dy.data_ptr()
+    if initial_state is not None:
+        p.initial_state = _packed("initial_state", initial_state, (N, W - 1, D), (x.dtype,), x)
+    if d_final_state is not None:
+        p.d_final_state = _packed("d_final_state", d_final_state, (N, W - 1, D), (x.dtype,), x)
+    dx, strides = _result("dx", dx, x)
+    p.dx, p.dx_stride_t = dx.data_ptr(), strides[0]
+    d_weight = torch.empty_like(weight)
+    p.d_weight = d_weight.data_ptr()
+    d_bias = None
+    if bias is not None:
+        d_bias = torch.empty_like(bias)
+        p.d_bias = d_bias.data_ptr()
+    d_initial_state = x.new_empty((N, max(W - 1, 0), D))
+    p.d_initial_state = d_initial_state.data_ptr()
+    ws = _workspace(p, workspace, B.load().la_sconv_bwd_workspace_bytes(T, N, D, W), x)  # noqa: F841
+    if status is not None:
+        _status(p, status, x)
+    _call("sconv_bwd", p, x)
     return dx, d_weight, d_bias, d_initial_state
 
 
+@_on_stream
 def sconv_decode(x: torch.Tensor, weight: torch.Tensor, state_pool: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
                  state_indices: Optional[torch.Tensor] = None, activation: Optional[str] = "silu",
                  y: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One new token for each of N sequences: x [N, D]; sequence i's last W - 1 inputs are pool[state_indices[i]]
     (pool[i] without indices) of state_pool [P, W - 1, D] in x's dtype, moved on in place.  Returns y [N, D]."""
-    with _on(stream):
-        p = B.SconvDecodeParams()
-        D, W = _sconv_common(p, x, weight, bias, activation)
-        dev = x.device
-        N = x.shape[0]
-        if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 3:
-            raise ValueError("state_pool must be a contiguous [P, W - 1, D] tensor")
-        P = state_pool.shape[0]
-        p.state_pool = _packed("state_pool", state_pool, (P, W - 1, D), (x.dtype,), dev).data_ptr()
-        p.N, p.x_stride_n, p.state_pool_size = N, x.stride(0), P
-        if state_indices is not None:
-            _indices(p, state_indices, N, dev)
-        y = _result("y", y, x)
-        p.y, p.y_stride_n = y.data_ptr(), y.stride(0)
-        _status(p, status, dev)
-        _call("sconv_decode", p, dev)
+    p = B.SconvDecodeParams()
+    p.x_stride_n = _sconv_inputs(p, x, weight, bias, activation)
+    p.N, D = N, _ = x.shape
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 3:
+        raise ValueError("state_pool must be a contiguous [P, W - 1, D] tensor")
+    p.state_pool_size = P = state_pool.shape[0]
+    p.state_pool = _packed("state_pool", state_pool, (P, weight.shape[1] - 1, D), (x.dtype,), x)
+    if state_indices is not None:
+        _indices(p, state_indices, N, x)
+    y, strides = _result("y", y, x)
+    p.y, p.y_stride_n = y.data_ptr(), strides[0]
+    if status is not None:
+        _status(p, status, x)
+    _call("sconv_decode", p, x)
     return y
 
 
