@@ -30,6 +30,7 @@
 #pragma once
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "mixer.cuh"
 
@@ -58,14 +59,17 @@ __device__ __forceinline__ float one_minus_exp(float l, float e) {
     return fabsf(l) < 0.5f ? -l * p : 1.f - e;
 }
 
-// a, m and dl/dg of one gate value.  s(g) and 1 - s(g) come from e = exp(-|g|) without cancellation.
+// a, m and dl/dg of one gate value.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g), held below 2^115 so
+// that the product stays finite (s(g) is then 2^-115 instead of less; NaN stays NaN): no cancellation, no branch.
 template <int kMode, bool kComplement>
 __device__ __forceinline__ void gate(float lb, float g, float& a, float& m, float& slope) {
     float l = g;
     slope = 1.f;
     if (kMode != LA_GATE_LOG) {
-        const float e = exp_fast(-fabsf(g)), big = rcp_fast(1.f + e), small = e * big;
-        const float s = g >= 0.f ? big : small, rest = g >= 0.f ? small : big;
+        float e = g * -1.4426950408889634f;
+        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e));  // 115
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
+        const float s = rcp_fast(1.f + e), rest = e * s;
         if (kMode == LA_GATE_LOGSIGMOID) {
             a = s;
             slope = rest;
@@ -114,6 +118,14 @@ struct Args {
     uint2* states;     // [items][32]: the states leaving the item
     int tma;           // every operand can move by TMA
 };
+
+// Calls f with a constant that says whether the thread's span is whole, as all but a sequence's last are: its loops
+// then have no bounds to check.
+template <typename F>
+__device__ __forceinline__ void with_span(int n, F f) {
+    if (n >= kSpan) f(std::true_type());
+    else f(std::false_type());
+}
 
 // ---------------------------------------------------------------- a thread's four channels of one row in shared memory
 template <typename T>

@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
         }
         // the maps of the thread's span, h -> ca h + cu forwards and c -> ca c + cc backwards
         float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f};
-        {
+        with_span(n, [&](auto whole) {
 #pragma unroll
             for (int k = 0; k < kSpan; ++k)
-                if (k < n) {
+                if (whole || k < n) {
                     float x[4], g[4], d[4];
                     get4(wx + mine + k * kChannels, x);
                     get4(wg + mine + k * kChannels, g);
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
                         cc[i] = fmaf(ca[i], d[i], cc[i]);
                     }
                 }
-        }
+        });
         float oa[4], ou[4], oc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
         }
         __syncthreads();
         if (rows > 0) {
-            {
+            with_span(n, [&](auto whole) {
                 constexpr bool kSlope = kMode != LA_GATE_LOG;
                 // forwards for the states before each token; backwards evaluates the gate once more, since
                 // keeping it too would not fit the registers
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
                 get4(&sh.in[c4], e);
 #pragma unroll
                 for (int k = 0; k < kSpan; ++k)
-                    if (k < n) {
+                    if (whole || k < n) {
                         float x[4], g[4];
                         get4(wx + mine + k * kChannels, x);
                         get4(wg + mine + k * kChannels, g);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
                 asm volatile("" ::: "memory");  // the compiler would keep the gates, in local memory
 #pragma unroll
                 for (int k = kSpan - 1; k >= 0; --k)
-                    if (k < n) {
+                    if (whole || k < n) {
                         float x[4], g[4], d[4];
                         if (kCompl) get4(wx + mine + k * kChannels, x);
                         get4(wg + mine + k * kChannels, g);
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
                         put4(wx + mine + k * kChannels, d);
                         put4(wg + mine + k * kChannels, g);
                     }
-            }
+            });
             if (a.tma && rows == kWarpRows) {
                 fence_proxy_async_smem();
                 __syncwarp();

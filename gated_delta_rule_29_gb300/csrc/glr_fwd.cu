@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
         }
         // the map of the thread's span
         float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
-        {
+        with_span(n, [&](auto whole) {
 #pragma unroll
             for (int k = 0; k < kSpan; ++k)
-                if (k < n) {
+                if (whole || k < n) {
                     float x[4], g[4];
                     get4(sx + k * kChannels, x);
                     get4(sg + k * kChannels, g);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
                         ca[i] *= dec;
                     }
                 }
-        }
+        });
         // the other half's: the lower one's map enters the upper one, both make the warp's
         float oa[4], ou[4];
 #pragma unroll
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
             get4(&sh.in[c4], h);
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = fmaf(pa[e], h[e], pu[e]);
-            {
+            with_span(n, [&](auto whole) {
 #pragma unroll
                 for (int k = 0; k < kSpan; ++k)
-                    if (k < n) {
+                    if (whole || k < n) {
                         float x[4], g[4];
                         get4(sx + k * kChannels, x);
                         get4(sg + k * kChannels, g);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
                         }
                         put4(sx + k * kChannels, h);
                     }
-            }
+            });
             // whole tiles by TMA; the last rows of a sequence one by one
             if (a.tma && rows == kWarpRows) {
                 fence_proxy_async_smem();

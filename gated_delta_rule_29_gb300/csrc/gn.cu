@@ -16,6 +16,7 @@
 // gradients' sums in registers over all its rows; a CTA adds its groups' sums and a second kernel the
 // CTAs', both in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "mixer.cuh"
 
@@ -131,8 +132,28 @@ __device__ __forceinline__ void load_weights(float (&w)[NV][kVec], const void* p
     }
 }
 
+// Calls f with the activation and whether it is a gate's as constants.
+template <typename F>
+__device__ __forceinline__ void with_act(const Args& a, F f) {
+    typedef std::integral_constant<int, LA_ACT_NONE> None;
+    typedef std::integral_constant<int, LA_ACT_SILU> Silu;
+    typedef std::integral_constant<int, LA_ACT_SIGMOID> Sigmoid;
+    if (a.z) {
+        if (a.act == LA_ACT_SILU) f(Silu(), std::true_type());
+        else if (a.act == LA_ACT_SIGMOID) f(Sigmoid(), std::true_type());
+        else f(None(), std::true_type());
+    } else {
+        if (a.act == LA_ACT_SILU) f(Silu(), std::false_type());
+        else if (a.act == LA_ACT_SIGMOID) f(Sigmoid(), std::false_type());
+        else f(None(), std::false_type());
+    }
+}
+
+// Resident CTAs to compile for: more, with fewer registers each, where a lane holds little.
+constexpr int ctas(int elements, int few, int many) { return elements <= 8 ? many : elements <= 16 ? few : 1; }
+
 template <typename X, int kVec, int NV, bool kBlock>
-__global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, 4)) gn_fwd_kernel(const Args a) {
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
     const Walk r = walk(a);
@@ -168,27 +189,29 @@ __global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const Args a) {
         X* to = static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh;
         LA_EACH_VECTOR(k, c) {
             float y[kVec];
+            with_act(a, [&](auto act, auto gated) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float p = fmaf(x[k][i], w[k][i], b[k][i]);
-                y[i] = a.z ? p * act_fwd(a.act, z[k].get(i)) : act_fwd(a.act, p);
-            }
+                for (int i = 0; i < kVec; ++i) {
+                    const float p = fmaf(x[k][i], w[k][i], b[k][i]);
+                    y[i] = gated ? p * act_fwd(act, z[k].get(i)) : act_fwd(act, p);
+                }
+            });
             store_packed<X, kVec>(to + c, y);
         }
     }
 }
 
-template <typename X, int kVec, int NV, bool kBlock>
-__global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const Args a) {
+template <typename X, int kVec, int NV, bool kBlock, bool kBias>
+__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias && NV * kVec == 8 ? 2 : 3)) gn_bwd_kernel(const Args a) {
     extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
     const Walk r = walk(a);
     const int64_t rounds = (a.T + r.step - 1) / r.step;
     const float inv_v = 1.f / a.V;
-    float w[NV][kVec], b[NV][kVec], dw[NV][kVec] = {}, db[NV][kVec] = {};
+    float w[NV][kVec], b[NV][kVec], dw[NV][kVec] = {}, db[NV][kVec] = {};  // b and db: unused without a bias
     load_weights<kVec, NV>(w, a.w, r.h, lane, 0.f, a);
-    load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
+    if (kBias) load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
     Packed<X, kVec> raw[NV], z[NV], dy[NV], next[NV], next_z[NV], next_dy[NV];
     auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], Packed<X, kVec> (&d)[NV], int64_t t) {
         load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
@@ -217,24 +240,28 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const Args a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float dz[kVec];
+            with_act(a, [&](auto act, auto gated) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const float p = kBias ? fmaf(n[k][i], w[k][i], b[k][i]) : n[k][i] * w[k][i];
+                    float d, v = dy[k].get(i);  // 0 beyond V and where not live, and so is all that follows from it
+                    if (gated) {
+                        const float f = act_grad(act, z[k].get(i), d);
+                        dz[i] = v * p * d;
+                        g[k][i] = v * f;
+                    } else {
+                        act_grad(act, p, d);
+                        g[k][i] = v * d;
+                    }
+                }
+            });
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                const float p = fmaf(n[k][i], w[k][i], b[k][i]);
-                float d, v = dy[k].get(i);  // 0 beyond V and where not live, and so is all that follows from it
-                if (a.z) {
-                    const float f = act_grad(a.act, z[k].get(i), d);
-                    dz[i] = v * p * d;
-                    v *= f;
-                } else {
-                    act_grad(a.act, p, d);
-                    v *= d;
-                }
-                dw[k][i] = fmaf(v, n[k][i], dw[k][i]);
-                db[k][i] += v;
-                v *= w[k][i];
-                g[k][i] = v;
-                sg += v;
-                sgn = fmaf(v, n[k][i], sgn);
+                dw[k][i] = fmaf(g[k][i], n[k][i], dw[k][i]);
+                if (kBias) db[k][i] += g[k][i];
+                g[k][i] *= w[k][i];
+                sg += g[k][i];
+                sgn = fmaf(g[k][i], n[k][i], sgn);
             }
             const int c = (lane + k * a.lanes) * kVec;
             if (a.z && live && c < a.V) store_packed<X, kVec>(static_cast<X*>(a.dz) + t * a.dz_st + r.h * a.dz_sh + c, dz);
@@ -253,9 +280,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const Args a) {
     // the CTA's sums, group by group
     const int groups = kThreads / a.lanes, u = threadIdx.x / a.lanes;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < (kBias ? 2 : 1); ++which) {
         float* out = which ? a.pb : a.pw;
-        if (!out) continue;
         __syncthreads();
         LA_EACH_VECTOR(k, c) {
 #pragma unroll
@@ -331,7 +357,8 @@ la_status launch(const Args& a, bool bwd, cudaStream_t s) {
     if (bwd) {
         const size_t smem = static_cast<size_t>(groups) * a.V * sizeof(float);
         const unsigned grid = static_cast<unsigned>(bwd_ctas(a.T, a.H, a.V, a.per_head));
-        gn_bwd_kernel<X, kVec, NV, kBlock><<<grid, kThreads, smem, s>>>(a);
+        if (a.b) gn_bwd_kernel<X, kVec, NV, kBlock, true><<<grid, kThreads, smem, s>>>(a);
+        else gn_bwd_kernel<X, kVec, NV, kBlock, false><<<grid, kThreads, smem, s>>>(a);
     } else {
         int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 16);
         if (a.per_head) grid = (grid + a.H - 1) / a.H * a.H;

@@ -15,6 +15,7 @@
 // Memory bound by its bytes (2 rows forward, 3 backward), close behind comes the arithmetic: about 16
 // instructions an element forward and 33 backward at W = 4 with the activation's two special functions.
 #include <algorithm>
+#include <type_traits>
 
 #include "mixer.cuh"
 
@@ -198,7 +199,7 @@ struct Blocks {
     }
 };
 
-template <typename X, int W>
+template <typename X, int W, int kAct>
 __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -220,17 +221,22 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const
             for (int j = 0; j < W - 1; ++j)
                 win[j + 1] = b.c == 0 && warp == 0 ? input_at<X, W>(a, b.first, slot, j - (W - 1), d) : staged2(px + j * kChannels);
             px += (W - 1) * kChannels;
-            const int64_t t0 = static_cast<int64_t>(b.start) + k0;
-#pragma unroll 8
-            for (int k = 0; k < kSpan; ++k) {
-                if (k >= n) break;
+            X* py = static_cast<X*>(a.y) + (static_cast<int64_t>(b.start) + k0) * a.y_st;
+            auto token = [&](int k) {
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
                 win[W - 1] = staged2(px + k * kChannels);
                 float2 p = bias;
 #pragma unroll
                 for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
-                put_row2<X>(a.y, (t0 + k) * a.y_st, d, a.D, a.pair, make_float2(act_fwd(a.act, p.x), act_fwd(a.act, p.y)));
+                put_row2<X>(py, 0, d, a.D, a.pair, make_float2(act_fwd(kAct, p.x), act_fwd(kAct, p.y)));
+                py += a.y_st;
+            };
+            if (n == kSpan) {
+#pragma unroll 8
+                for (int k = 0; k < kSpan; ++k) token(k);
+            } else {
+                for (int k = 0; k < n; ++k) token(k);
             }
         }
         // The sequence's last W - 1 inputs.  With a pool they replace the rows that the sequence started from,
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const
     });
 }
 
-template <typename X, int W>
+template <typename X, int W, int kAct>
 __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -275,9 +281,9 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
         };
         float2 dp0[W - 1];  // dp of the span's first tokens: what the state's rows reach
         if (n > 0) {
-            const int64_t p0 = static_cast<int64_t>(b.c) * kBlock + k0, t0 = static_cast<int64_t>(b.start) + k0;
+            const int64_t p0 = static_cast<int64_t>(b.c) * kBlock + k0;
+            X* pdx = static_cast<X*>(a.dx) + (static_cast<int64_t>(b.start) + k0) * a.dx_st;
             const int left = static_cast<int>(min(b.len - p0, static_cast<int64_t>(kSpan + W - 1)));  // tokens to the sequence's end
-            const bool near_end = left < kSpan + W - 1;
             float2 win[W], dp[W];
             const X* px = xs + k0 * kChannels + 2 * lane;
             const X* pd = dys + k0 * kChannels + 2 * lane;
@@ -287,54 +293,60 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                 dp[j + 1] = make_float2(0.f, 0.f);
             }
             px += (W - 1) * kChannels;
-            // one token further: win ends with token k, dp with its dp (0 beyond the end)
-            auto step = [&](int k) {
+            // `whole`: every token that the span reads is in the sequence, so that nothing is masked
+            auto walk = [&](auto whole) {
+                // one token further: win ends with token k, dp with its dp (0 beyond the end)
+                auto step = [&](int k) {
 #pragma unroll
-                for (int j = 0; j + 1 < W; ++j) {
-                    win[j] = win[j + 1];
-                    dp[j] = dp[j + 1];
+                    for (int j = 0; j + 1 < W; ++j) {
+                        win[j] = win[j + 1];
+                        dp[j] = dp[j + 1];
+                    }
+                    win[W - 1] = staged2(px + k * kChannels);
+                    const float2 dy = staged2(pd + k * kChannels);
+                    float2 p = bias, s;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
+                    act_grad(kAct, p.x, s.x);
+                    act_grad(kAct, p.y, s.y);
+                    dp[W - 1] = make_float2(dy.x * s.x, dy.y * s.y);
+                    if (!whole && k >= left) dp[W - 1] = win[W - 1] = make_float2(0.f, 0.f);
+                };
+                auto emit = [&](int k) {  // dx of token k, W - 1 behind
+                    if (!whole && k >= n) return;
+                    float2 dx = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dx = fma2(w[j], dp[W - 1 - j], dx);
+                    if (!whole) dx = add_final(dx, p0 + k - (static_cast<int64_t>(b.len) - (W - 1)));
+                    put_row2<X>(pdx, 0, d, a.D, a.pair, dx);
+                    pdx += a.dx_st;
+                };
+                auto sum = [&]() {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j] = fma2(dp[W - 1], win[j], dw[j]);
+                    db.x += dp[W - 1].x;
+                    db.y += dp[W - 1].y;
+                };
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) {
+                    step(k);
+                    sum();
+                    dp0[k] = dp[W - 1];
                 }
-                win[W - 1] = staged2(px + k * kChannels);
-                const float2 dy = staged2(pd + k * kChannels);
-                float2 p = bias, s;
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
-                act_grad(a.act, p.x, s.x);
-                act_grad(a.act, p.y, s.y);
-                dp[W - 1] = make_float2(dy.x * s.x, dy.y * s.y);
-                if (k >= left) dp[W - 1] = win[W - 1] = make_float2(0.f, 0.f);
-            };
-            auto emit = [&](int k) {  // dx of token k, W - 1 behind
-                if (k < 0 || k >= n) return;
-                float2 dx = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < W; ++j) dx = fma2(w[j], dp[W - 1 - j], dx);
-                if (near_end) dx = add_final(dx, p0 + k - (static_cast<int64_t>(b.len) - (W - 1)));
-                put_row2<X>(a.dx, (t0 + k) * a.dx_st, d, a.D, a.pair, dx);
-            };
-            auto sum = [&]() {
-#pragma unroll
-                for (int j = 0; j < W; ++j) dw[j] = fma2(dp[W - 1], win[j], dw[j]);
-                db.x += dp[W - 1].x;
-                db.y += dp[W - 1].y;
-            };
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-                step(k);
-                sum();
-                dp0[k] = dp[W - 1];
-            }
 #pragma unroll 4
-            for (int k = W - 1; k < kSpan; ++k) {
-                step(k);
-                sum();
-                emit(k - (W - 1));
-            }
+                for (int k = W - 1; k < kSpan; ++k) {
+                    step(k);
+                    sum();
+                    emit(k - (W - 1));
+                }
 #pragma unroll
-            for (int k = kSpan; k < kSpan + W - 1; ++k) {
-                step(k);
-                emit(k - (W - 1));
-            }
+                for (int k = kSpan; k < kSpan + W - 1; ++k) {
+                    step(k);
+                    emit(k - (W - 1));
+                }
+            };
+            if (left >= kSpan + W - 1) walk(std::true_type());
+            else walk(std::false_type());
         } else {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) dp0[k] = make_float2(0.f, 0.f);
@@ -465,8 +477,14 @@ la_status run_blocks(Args& a, bool bwd, int32_t xd, cudaStream_t s) {
     const int64_t stride = bwd ? a.dx_st : a.y_st;
     a.pair = a.D % 2 == 0 && aligned_to(out, 2 * sizeof(X)) && (a.T == 1 || stride % 2 == 0);
     const int depth = a.tma ? stages<X>() : 1;
-    return bwd ? launch_blocks<sconv_bwd_kernel<X, W>>(depth * stage_bytes<X, W, true>(), a, maps, s)
-               : launch_blocks<sconv_fwd_kernel<X, W>>(depth * stage_bytes<X, W, false>(), a, maps, s);
+    auto start = [&](auto act) {
+        constexpr int kAct = decltype(act)::value;
+        return bwd ? launch_blocks<sconv_bwd_kernel<X, W, kAct>>(depth * stage_bytes<X, W, true>(), a, maps, s)
+                   : launch_blocks<sconv_fwd_kernel<X, W, kAct>>(depth * stage_bytes<X, W, false>(), a, maps, s);
+    };
+    if (a.act == LA_ACT_SILU) return start(std::integral_constant<int, LA_ACT_SILU>());
+    if (a.act == LA_ACT_SIGMOID) return start(std::integral_constant<int, LA_ACT_SIGMOID>());
+    return start(std::integral_constant<int, LA_ACT_NONE>());
 }
 
 // Four channels a lane where every operand's rows start on four of its elements.
