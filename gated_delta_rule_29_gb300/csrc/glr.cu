@@ -23,9 +23,13 @@ __global__ void __launch_bounds__(kThreads) glr_decode_kernel(const Args a) {
             return;
         }
     }
-    float dec, m, slope;
+    float dec, m;
     const float g = to_f(static_cast<const G*>(a.g)[i * a.g_st + d]);
-    with_gate(a.mode, a.compl_in, [&](auto gt) { gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, g, dec, m, slope); });
+    with_gate(a.mode, a.compl_in, [&](auto gt) {
+        const Gated t = gate<decltype(gt)::mode, decltype(gt)::complement>(a.lb, both(g));
+        dec = t.a.x;
+        m = t.m.x;
+    });
     const float h = fmaf(dec, load_any(a.s0, slot * a.D + d, a.s0_bf16), m * to_f(static_cast<const X*>(a.x)[i * a.x_st + d]));
     store_any(const_cast<void*>(a.s0), slot * a.D + d, a.s0_bf16, h);
     static_cast<X*>(a.h)[i * a.h_st + d] = from_f<X>(h);
@@ -50,14 +54,7 @@ la_status run_scan(Args& a, int32_t xd, int32_t gd, Which w, void* ws, cudaStrea
         a.states = reinterpret_cast<uint2*>(static_cast<uint8_t*>(ws) + maps);
         if (cudaMemsetAsync(ws, 0xFF, table_bytes(a.T, a.N, a.D), s) != cudaSuccess) return LA_ERR_CUDA;
     }
-    Maps maps = {};
-    auto tile = [&](CUtensorMap* m, const void* p, int64_t stride, int32_t dtype) {
-        return tileable(p, stride, a.T, a.D, dtype) && tile_map(m, p, stride, a.T, a.D, dtype, kChannels, kWarpRows);
-    };
-    a.tma = tile(&maps.x, a.x, a.x_st, xd) && tile(&maps.g, a.g, a.g_st, gd);
-    if (w == kFwd) a.tma = a.tma && (!a.h || tile(&maps.out, a.h, a.h_st, xd));
-    else a.tma = a.tma && tile(&maps.dh, a.dh, a.dh_st, xd) && tile(&maps.out, a.dx, a.dx_st, xd) && tile(&maps.dg, a.dg, a.dg_st, gd);
-    return w == kFwd ? run_fwd(a, maps, xd, gd, s) : run_bwd(a, maps, xd, gd, s);
+    return w == kFwd ? run_fwd(a, xd, gd, s) : run_bwd(a, xd, gd, s);
 }
 
 template <typename X, typename G>

@@ -10,8 +10,8 @@
 //   dg_t = dl_t dl/dg,  d(initial) = a_1 e_1.
 //
 // Every step is the affine map h -> a h + u, and maps compose, so the time axis is split.  A CTA takes
-// a block of 128 tokens x 64 channels into shared memory, each warp its own 16 tokens by TMA, each
-// thread 8 tokens of 4 channels.  First pass: the block's composed map.  Then one number per channel
+// a block of 128 tokens x 64 channels into shared memory, each warp its own 16 or 32 tokens by TMA,
+// each thread half of them of 4 channels.  First pass: the block's composed map.  Then one number per channel
 // from the block before, the state entering it.  Second pass: the block again from shared memory (the
 // gate is cheaper to evaluate twice than to keep), results over the inputs, stored by TMA.
 //
@@ -39,48 +39,57 @@ namespace glr {
 
 using namespace la::mixer;
 
-constexpr int kWarps = 8;                        // of a scan CTA
-constexpr int kScanThreads = 32 * kWarps;
-constexpr int kSpan = 8;                         // tokens of a thread
-constexpr int kWarpRows = 2 * kSpan;             // tokens of a warp: its halves take one span each
-constexpr int kBlock = kWarpRows * kWarps;       // tokens of a block, and between saved states
+constexpr int kBlock = 128;                      // tokens of a block, and between saved states
 constexpr int kChannels = 64;                    // of a CTA, four a lane
 constexpr uint64_t kWaitNs = 1000000000ull;      // a bounded wait gives up after a second
-static_assert(kBlock == 128, "the checkpoint cadence of the interface");
 
-// 1 - e^l given e^l: the Taylor series (to l^7 / 7!, 2e-7 of it at 1/2) where the difference would cancel.
-__device__ __forceinline__ float one_minus_exp(float l, float e) {
-    float p = fmaf(l, 1.f / 7.f, 1.f);
-    p = fmaf(l * (1.f / 6.f), p, 1.f);
-    p = fmaf(l * (1.f / 5.f), p, 1.f);
-    p = fmaf(l * (1.f / 4.f), p, 1.f);
-    p = fmaf(l * (1.f / 3.f), p, 1.f);
-    p = fmaf(l * (1.f / 2.f), p, 1.f);
-    return fabsf(l) < 0.5f ? -l * p : 1.f - e;
+// A CTA's kWarps warps take 128 / kWarps tokens each, half a warp half of those.
+template <int kWarps>
+constexpr int span() { return kBlock / kWarps / 2; }
+
+// 1 - e^l given e^l, for two values: the Taylor series (to l^7 / 7!, 2e-7 of it at 1/2) where the difference would
+// cancel.
+__device__ __forceinline__ float2 one_minus_exp(float2 l, float2 e) {
+    float2 p = fma2(l, both(1.f / 7.f), both(1.f));
+    p = fma2(mul2(l, both(1.f / 6.f)), p, both(1.f));
+    p = fma2(mul2(l, both(1.f / 5.f)), p, both(1.f));
+    p = fma2(mul2(l, both(1.f / 4.f)), p, both(1.f));
+    p = fma2(mul2(l, both(1.f / 3.f)), p, both(1.f));
+    p = fma2(mul2(l, both(1.f / 2.f)), p, both(1.f));
+    p = mul2(mul2(l, both(-1.f)), p);
+    const float2 d = fma2(e, both(-1.f), both(1.f));
+    return make_float2(fabsf(l.x) < 0.5f ? p.x : d.x, fabsf(l.y) < 0.5f ? p.y : d.y);
 }
 
-// a, m and dl/dg of one gate value.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g), held below 2^115 so
+// a, m and dl/dg of two gate values.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g), held below 2^115 so
 // that the product stays finite (s(g) is then 2^-115 instead of less; NaN stays NaN): no cancellation, no branch.
+struct Gated {
+    float2 a, m, slope;
+};
 template <int kMode, bool kComplement>
-__device__ __forceinline__ void gate(float lb, float g, float& a, float& m, float& slope) {
-    float l = g;
-    slope = 1.f;
+__device__ __forceinline__ Gated gate(float lb, float2 g) {
+    Gated r;
+    float2 l = g;
+    r.slope = both(1.f);
     if (kMode != LA_GATE_LOG) {
-        float e = g * -1.4426950408889634f;
-        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e));  // 115
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
-        const float s = rcp_fast(1.f + e), rest = e * s;
+        float2 e = mul2(g, both(-kLog2e));
+        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e.x));  // 115
+        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e.y));
+        e = make_float2(ex2(e.x), ex2(e.y));
+        const float2 q = add2(e, both(1.f)), s = make_float2(rcp_fast(q.x), rcp_fast(q.y)), rest = mul2(e, s);
         if (kMode == LA_GATE_LOGSIGMOID) {
-            a = s;
-            slope = rest;
-            m = kComplement ? rest : 1.f;
-            return;
+            r.a = s;
+            r.slope = rest;
+            r.m = kComplement ? rest : both(1.f);
+            return r;
         }
-        l = lb * s;
-        slope = l * rest;
+        l = mul2(both(lb), s);
+        r.slope = mul2(l, rest);
     }
-    a = exp_fast(l);
-    m = kComplement ? one_minus_exp(l, a) : 1.f;
+    const float2 t = mul2(l, both(kLog2e));
+    r.a = make_float2(ex2(t.x), ex2(t.y));
+    r.m = kComplement ? one_minus_exp(l, r.a) : both(1.f);
+    return r;
 }
 
 // Calls f with the gate's mode and complement as constants.
@@ -121,38 +130,49 @@ struct Args {
 
 // Calls f with a constant that says whether the thread's span is whole, as all but a sequence's last are: its loops
 // then have no bounds to check.
-template <typename F>
+template <int kSpan, typename F>
 __device__ __forceinline__ void with_span(int n, F f) {
     if (n >= kSpan) f(std::true_type());
     else f(std::false_type());
 }
 
 // ---------------------------------------------------------------- a thread's four channels of one row in shared memory
+struct Four {
+    float2 v[2];
+};
 template <typename T>
-__device__ __forceinline__ void get4(const T* p, float (&v)[4]) {
+__device__ __forceinline__ Four get4(const T* p) {
+    Four r;
     if (sizeof(T) == 2) {
         const uint2 w = *reinterpret_cast<const uint2*>(p);
-        v[0] = __uint_as_float(w.x << 16);
-        v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(w.y << 16);
-        v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+        r.v[0] = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+        r.v[1] = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
     } else {
         const float4 w = *reinterpret_cast<const float4*>(p);
-        v[0] = w.x;
-        v[1] = w.y;
-        v[2] = w.z;
-        v[3] = w.w;
+        r.v[0] = make_float2(w.x, w.y);
+        r.v[1] = make_float2(w.z, w.w);
     }
+    return r;
 }
 template <typename T>
-__device__ __forceinline__ void put4(T* p, const float (&v)[4]) {
+__device__ __forceinline__ void put4(T* p, const Four& f) {
     if (sizeof(T) == 2) {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        __nv_bfloat162 lo = __floats2bfloat162_rn(f.v[0].x, f.v[0].y), hi = __floats2bfloat162_rn(f.v[1].x, f.v[1].y);
         *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
     } else {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p) = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
     }
 }
+__device__ __forceinline__ Four four(float x) { return {{both(x), both(x)}}; }
+__device__ __forceinline__ Four fma4(const Four& a, const Four& b, const Four& c) {
+    return {{fma2(a.v[0], b.v[0], c.v[0]), fma2(a.v[1], b.v[1], c.v[1])}};
+}
+__device__ __forceinline__ Four mul4(const Four& a, const Four& b) { return {{mul2(a.v[0], b.v[0]), mul2(a.v[1], b.v[1])}}; }
+__device__ __forceinline__ Four other_half(const Four& a) {
+    return {{make_float2(__shfl_xor_sync(0xffffffffu, a.v[0].x, 16), __shfl_xor_sync(0xffffffffu, a.v[0].y, 16)),
+             make_float2(__shfl_xor_sync(0xffffffffu, a.v[1].x, 16), __shfl_xor_sync(0xffffffffu, a.v[1].y, 16))}};
+}
+
 // ---------------------------------------------------------------- a warp's rows between global and shared memory
 // Without TMA: lane by lane, rows [0, n) of the warp, channels below D.
 template <typename T>
@@ -331,8 +351,8 @@ __device__ __forceinline__ void chain(const Args& a, int64_t j, const Item& it, 
 }
 
 __device__ __forceinline__ void check_boundaries(const Args& a) {
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kScanThreads) + threadIdx.x; i < a.N;
-         i += static_cast<int64_t>(gridDim.x) * kScanThreads)
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < a.N;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
         check_cu(a.cu, a.cu64, a.N, a.T, i, a.status);
 }
 
@@ -340,10 +360,12 @@ struct Maps {
     CUtensorMap x, g, dh, out, dg;  // out: h, or dx in the backward
 };
 
-// What both directions keep beside the staged rows.
+// What a scan keeps beside the staged rows.
+template <int kWarps, bool kBackward>
 struct Shared {
-    float a[kWarps][kChannels], u[kWarps][kChannels], c[kWarps][kChannels];  // each warp's map (c: the gradients')
-    float in[kChannels], h0[kChannels];
+    alignas(16) float a[kWarps][kChannels], u[kWarps][kChannels];  // each warp's map
+    alignas(16) float c[kBackward ? kWarps : 1][kChannels];        // and the gradients'
+    alignas(16) float in[kChannels], h0[kBackward ? kChannels : 4];
     uint64_t bar[kWarps];
     Item items[2];
 };
@@ -353,13 +375,13 @@ constexpr size_t stage_bytes() { return static_cast<size_t>(kBlock) * kChannels 
 
 // CTAs that an SM of the current device holds of a kernel (0: an error), looked up once per device.
 template <auto kKernel>
-int resident_ctas(int dev, size_t smem) {
+int resident_ctas(int dev, int threads, size_t smem) {
     static std::atomic<int> known[128];
     if (dev < 0 || dev >= 128) return 0;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
         if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, kScanThreads, smem) != cudaSuccess || n < 1) {
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, smem) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
             return 0;
         }
@@ -369,24 +391,29 @@ int resident_ctas(int dev, size_t smem) {
 }
 
 template <auto kKernel>
-la_status launch_scan(size_t smem, Args& a, Maps& maps, cudaStream_t s) {
+la_status launch_scan(int threads, size_t smem, Args& a, Maps& maps, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return LA_ERR_CUDA;
-    const int per_sm = resident_ctas<kKernel>(dev, smem);
+    const int per_sm = resident_ctas<kKernel>(dev, threads, smem);
     if (per_sm == 0) return LA_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.items, static_cast<int64_t>(sms) * per_sm));
     void* args[] = {&a, &maps};
-    if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kKernel), dim3(grid), dim3(kScanThreads), args, smem, s) != cudaSuccess) {
+    if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kKernel), dim3(grid), dim3(threads), args, smem, s) != cudaSuccess) {
         (void)cudaGetLastError();
         return LA_ERR_CUDA;
     }
     return LA_OK;
 }
 
-// The scans, for every type and gate (a.maps and the rest of Args set up by the caller).
-la_status run_fwd(Args& a, Maps& maps, int32_t x_dtype, int32_t g_dtype, cudaStream_t s);
-la_status run_bwd(Args& a, Maps& maps, int32_t x_dtype, int32_t g_dtype, cudaStream_t s);
+// The scans, for every type and gate; the caller has set up a but for its tma.
+la_status run_fwd(Args& a, int32_t x_dtype, int32_t g_dtype, cudaStream_t s);
+la_status run_bwd(Args& a, int32_t x_dtype, int32_t g_dtype, cudaStream_t s);
+
+// A map of one operand's tiles (one warp's rows); false where TMA cannot move them.
+inline bool row_map(CUtensorMap* m, const Args& a, const void* p, int64_t stride, int32_t dtype, int rows) {
+    return tileable(p, stride, a.T, a.D, dtype) && tile_map(m, p, stride, a.T, a.D, dtype, kChannels, rows);
+}
 
 }  // namespace glr
 }  // namespace la

@@ -5,14 +5,17 @@ namespace la {
 namespace glr {
 namespace {
 
-// CTAs of an SM: as many as the staged rows leave room for.
+// Warps of a CTA, and CTAs of an SM (as many as the staged rows leave room for).  Short spans: the states before
+// each of its tokens stay in registers.
+constexpr int kWarps = 8;
 template <typename X, typename G>
-constexpr int bwd_ctas() { return sizeof(X) + sizeof(G) == 8 ? 2 : 3; }
+constexpr int ctas() { return sizeof(X) == 4 ? 2 : 3; }
 
 template <typename X, typename G, int kMode, bool kCompl>
-__global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(32 * kWarps, (ctas<X, G>())) glr_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    constexpr int kSpan = span<kWarps>(), kWarpRows = 2 * kSpan;
     extern __shared__ __align__(128) uint8_t stage[];
-    __shared__ Shared sh;
+    __shared__ Shared<kWarps, true> sh;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = lane >> 4, c4 = (lane & 15) * 4;
     constexpr int kPlane = kBlock * kChannels;
     X* wx = reinterpret_cast<X*>(stage) + w * kWarpRows * kChannels;
@@ -56,43 +59,31 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
         if (w == 1 && it.count > 0) load2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
         __syncwarp();
         if (a.tma && rows > 0) {
-            if (!mbar_wait(&sh.bar[w], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            if (!mbar_wait(&sh.bar[w], parity, kWaitNs, true)) raise_status(a.status, LA_ERR_TIMEOUT);
             parity ^= 1;
         }
         // the maps of the thread's span, h -> ca h + cu forwards and c -> ca c + cc backwards
-        float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f};
-        with_span(n, [&](auto whole) {
+        Four ca = four(1.f), cu = four(0.f), cc = four(0.f);
+        with_span<kSpan>(n, [&](auto whole) {
 #pragma unroll
             for (int k = 0; k < kSpan; ++k)
                 if (whole || k < n) {
-                    float x[4], g[4], d[4];
-                    get4(wx + mine + k * kChannels, x);
-                    get4(wg + mine + k * kChannels, g);
-                    get4(wd + mine + k * kChannels, d);
+                    const Four x = get4(wx + mine + k * kChannels), g = get4(wg + mine + k * kChannels),
+                               d = get4(wd + mine + k * kChannels);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float dec, m, slope;
-                        gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
-                        cu[i] = fmaf(dec, cu[i], kCompl ? m * x[i] : x[i]);
-                        ca[i] *= dec;
-                        cc[i] = fmaf(ca[i], d[i], cc[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const Gated t = gate<kMode, kCompl>(a.lb, g.v[i]);
+                        cu.v[i] = fma2(t.a, cu.v[i], kCompl ? mul2(t.m, x.v[i]) : x.v[i]);
+                        ca.v[i] = mul2(ca.v[i], t.a);
+                        cc.v[i] = fma2(ca.v[i], d.v[i], cc.v[i]);
                     }
                 }
         });
-        float oa[4], ou[4], oc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            oa[i] = __shfl_xor_sync(0xffffffffu, ca[i], 16);
-            ou[i] = __shfl_xor_sync(0xffffffffu, cu[i], 16);
-            oc[i] = __shfl_xor_sync(0xffffffffu, cc[i], 16);
-        }
+        const Four oa = other_half(ca), ou = other_half(cu), oc = other_half(cc);
         if (half == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sh.a[w][c4 + i] = ca[i] * oa[i];
-                sh.u[w][c4 + i] = fmaf(oa[i], cu[i], ou[i]);
-                sh.c[w][c4 + i] = fmaf(ca[i], oc[i], cc[i]);
-            }
+            put4(&sh.a[w][c4], mul4(ca, oa));
+            put4(&sh.u[w][c4], fma4(oa, cu, ou));
+            put4(&sh.c[w][c4], fma4(ca, oc, cc));
         }
         if (w == 1) *reinterpret_cast<float2*>(&sh.h0[2 * lane]) = in;
         __syncthreads();
@@ -114,79 +105,54 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
                 store2_any(a.ds0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, out.x, out.y);
         }
         // while the chain goes on: the state entering the thread's span, and the gradients' map after it
-        float h[4], pa[4] = {1.f, 1.f, 1.f, 1.f}, pc[4] = {0.f, 0.f, 0.f, 0.f};
-        get4(&sh.h0[c4], h);
-        for (int i = 0; i < w; ++i) {
-            float qa[4], qu[4];
-            get4(&sh.a[i][c4], qa);
-            get4(&sh.u[i][c4], qu);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = fmaf(qa[e], h[e], qu[e]);
-        }
+        Four h = get4(&sh.h0[c4]), pa = four(1.f), pc = four(0.f);
+        for (int i = 0; i < w; ++i) h = fma4(get4(&sh.a[i][c4]), h, get4(&sh.u[i][c4]));
         if (half == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = fmaf(oa[e], h[e], ou[e]);
+            h = fma4(oa, h, ou);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pa[e] = oa[e];
-                pc[e] = oc[e];
-            }
+            pa = oa;
+            pc = oc;
         }
         for (int i = w + 1; i < kWarps; ++i) {
-            float qa[4], qc[4];
-            get4(&sh.a[i][c4], qa);
-            get4(&sh.c[i][c4], qc);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pc[e] = fmaf(pa[e], qc[e], pc[e]);
-                pa[e] *= qa[e];
-            }
+            pc = fma4(pa, get4(&sh.c[i][c4]), pc);
+            pa = mul4(pa, get4(&sh.a[i][c4]));
         }
         __syncthreads();
         if (rows > 0) {
-            with_span(n, [&](auto whole) {
+            with_span<kSpan>(n, [&](auto whole) {
                 constexpr bool kSlope = kMode != LA_GATE_LOG;
                 // forwards for the states before each token; backwards evaluates the gate once more, since
                 // keeping it too would not fit the registers
-                float prev[kSpan][4], e[4];
-                get4(&sh.in[c4], e);
+                Four prev[kSpan], e = fma4(pa, get4(&sh.in[c4]), pc);
 #pragma unroll
                 for (int k = 0; k < kSpan; ++k)
                     if (whole || k < n) {
-                        float x[4], g[4];
-                        get4(wx + mine + k * kChannels, x);
-                        get4(wg + mine + k * kChannels, g);
+                        const Four x = get4(wx + mine + k * kChannels), g = get4(wg + mine + k * kChannels);
+                        prev[k] = h;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float dec, m, slope;
-                            gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
-                            prev[k][i] = h[i];
-                            h[i] = fmaf(dec, h[i], kCompl ? m * x[i] : x[i]);
+                        for (int i = 0; i < 2; ++i) {
+                            const Gated t = gate<kMode, kCompl>(a.lb, g.v[i]);
+                            h.v[i] = fma2(t.a, h.v[i], kCompl ? mul2(t.m, x.v[i]) : x.v[i]);
+                            if (kCompl) prev[k].v[i] = fma2(x.v[i], both(-1.f), prev[k].v[i]);
                         }
                     }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = fmaf(pa[i], e[i], pc[i]);
                 asm volatile("" ::: "memory");  // the compiler would keep the gates, in local memory
 #pragma unroll
                 for (int k = kSpan - 1; k >= 0; --k)
                     if (whole || k < n) {
-                        float x[4], g[4], d[4];
-                        if (kCompl) get4(wx + mine + k * kChannels, x);
-                        get4(wg + mine + k * kChannels, g);
-                        get4(wd + mine + k * kChannels, d);
+                        const Four g = get4(wg + mine + k * kChannels), d = get4(wd + mine + k * kChannels);
+                        Four dx, dg;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float dec, m, slope;
-                            gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
-                            e[i] += d[i];
-                            d[i] = kCompl ? m * e[i] : e[i];
-                            e[i] *= dec;
-                            g[i] = e[i] * (kCompl ? prev[k][i] - x[i] : prev[k][i]);
-                            if (kSlope) g[i] *= slope;
+                        for (int i = 0; i < 2; ++i) {
+                            const Gated t = gate<kMode, kCompl>(a.lb, g.v[i]);
+                            e.v[i] = add2(e.v[i], d.v[i]);
+                            dx.v[i] = kCompl ? mul2(t.m, e.v[i]) : e.v[i];
+                            e.v[i] = mul2(e.v[i], t.a);
+                            dg.v[i] = mul2(e.v[i], prev[k].v[i]);
+                            if (kSlope) dg.v[i] = mul2(dg.v[i], t.slope);
                         }
-                        put4(wx + mine + k * kChannels, d);
-                        put4(wg + mine + k * kChannels, g);
+                        put4(wx + mine + k * kChannels, dx);
+                        put4(wg + mine + k * kChannels, dg);
                     }
             });
             if (a.tma && rows == kWarpRows) {
@@ -214,19 +180,24 @@ __global__ void __launch_bounds__(kScanThreads, (bwd_ctas<X, G>())) glr_bwd_kern
 }
 
 template <typename X, typename G>
-la_status by_gate(Args& a, Maps& maps, cudaStream_t s) {
+la_status by_gate(Args& a, int32_t xd, int32_t gd, cudaStream_t s) {
+    constexpr int kRows = 2 * span<kWarps>();
+    Maps maps = {};
+    a.tma = row_map(&maps.x, a, a.x, a.x_st, xd, kRows) && row_map(&maps.g, a, a.g, a.g_st, gd, kRows) &&
+            row_map(&maps.dh, a, a.dh, a.dh_st, xd, kRows) && row_map(&maps.out, a, a.dx, a.dx_st, xd, kRows) &&
+            row_map(&maps.dg, a, a.dg, a.dg_st, gd, kRows);
     la_status st = LA_ERR_INVALID_ARG;
     with_gate(a.mode, a.compl_in, [&](auto gt) {
-        st = launch_scan<glr_bwd_kernel<X, G, decltype(gt)::mode, decltype(gt)::complement>>(stage_bytes<X, G, 2>(), a, maps, s);
+        st = launch_scan<glr_bwd_kernel<X, G, decltype(gt)::mode, decltype(gt)::complement>>(32 * kWarps, stage_bytes<X, G, 2>(), a, maps, s);
     });
     return st;
 }
 
 }  // namespace
 
-la_status run_bwd(Args& a, Maps& maps, int32_t xd, int32_t gd, cudaStream_t s) {
-    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? by_gate<bf16, bf16>(a, maps, s) : by_gate<bf16, float>(a, maps, s);
-    return gd == LA_DTYPE_BF16 ? by_gate<float, bf16>(a, maps, s) : by_gate<float, float>(a, maps, s);
+la_status run_bwd(Args& a, int32_t xd, int32_t gd, cudaStream_t s) {
+    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? by_gate<bf16, bf16>(a, xd, gd, s) : by_gate<bf16, float>(a, xd, gd, s);
+    return gd == LA_DTYPE_BF16 ? by_gate<float, bf16>(a, xd, gd, s) : by_gate<float, float>(a, xd, gd, s);
 }
 
 }  // namespace glr

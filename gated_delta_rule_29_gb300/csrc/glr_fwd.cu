@@ -5,13 +5,20 @@ namespace la {
 namespace glr {
 namespace {
 
-// CTAs of an SM: as many as the staged rows leave room for.
+// Warps of a CTA and CTAs of an SM (as many as the staged rows leave room for).  With 16-bit operands the
+// arithmetic is what fills the time: longer spans leave less of it between them.  With fp32 gates the bytes do,
+// and shorter spans give more warps to wait for them (fwd of 8 x 8192 x 4096, bf16 gates: 304 us with 4 warps, 339
+// with 8; three sequences of 4096 x 2048 in fp32: 36 and 26 us).
 template <typename X, typename G>
-constexpr int fwd_ctas() { return sizeof(X) + sizeof(G) == 4 ? 5 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
+constexpr int warps() { return sizeof(X) + sizeof(G) == 4 ? 4 : 8; }
+template <typename X, typename G>
+constexpr int ctas() { return sizeof(X) + sizeof(G) == 4 ? 6 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
+
 template <typename X, typename G, int kMode, bool kCompl>
-__global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    constexpr int kWarps = warps<X, G>(), kSpan = span<kWarps>(), kWarpRows = 2 * kSpan;
     extern __shared__ __align__(128) uint8_t stage[];
-    __shared__ Shared sh;
+    __shared__ Shared<kWarps, false> sh;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, half = lane >> 4, c4 = (lane & 15) * 4;
     X* wx = reinterpret_cast<X*>(stage) + w * kWarpRows * kChannels;                       // the warp's rows
     G* wg = reinterpret_cast<G*>(stage + sizeof(X) * kBlock * kChannels) + w * kWarpRows * kChannels;
@@ -52,40 +59,29 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
             load2_any(a.s0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, in.x, in.y);
         __syncwarp();
         if (a.tma && rows > 0) {
-            if (!mbar_wait(&sh.bar[w], parity, kWaitNs)) raise_status(a.status, LA_ERR_TIMEOUT);
+            if (!mbar_wait(&sh.bar[w], parity, kWaitNs, true)) raise_status(a.status, LA_ERR_TIMEOUT);
             parity ^= 1;
         }
         // the map of the thread's span
-        float ca[4] = {1.f, 1.f, 1.f, 1.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
-        with_span(n, [&](auto whole) {
-#pragma unroll
+        Four ca = four(1.f), cu = four(0.f);
+        with_span<kSpan>(n, [&](auto whole) {
+#pragma unroll 8
             for (int k = 0; k < kSpan; ++k)
                 if (whole || k < n) {
-                    float x[4], g[4];
-                    get4(sx + k * kChannels, x);
-                    get4(sg + k * kChannels, g);
+                    const Four x = get4(sx + k * kChannels), g = get4(sg + k * kChannels);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float dec, m, slope;
-                        gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
-                        cu[i] = fmaf(dec, cu[i], kCompl ? m * x[i] : x[i]);
-                        ca[i] *= dec;
+                    for (int i = 0; i < 2; ++i) {
+                        const Gated t = gate<kMode, kCompl>(a.lb, g.v[i]);
+                        cu.v[i] = fma2(t.a, cu.v[i], kCompl ? mul2(t.m, x.v[i]) : x.v[i]);
+                        ca.v[i] = mul2(ca.v[i], t.a);
                     }
                 }
         });
         // the other half's: the lower one's map enters the upper one, both make the warp's
-        float oa[4], ou[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            oa[i] = __shfl_xor_sync(0xffffffffu, ca[i], 16);
-            ou[i] = __shfl_xor_sync(0xffffffffu, cu[i], 16);
-        }
+        const Four oa = other_half(ca), ou = other_half(cu);
         if (half == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sh.a[w][c4 + i] = ca[i] * oa[i];
-                sh.u[w][c4 + i] = fmaf(oa[i], cu[i], ou[i]);
-            }
+            put4(&sh.a[w][c4], mul4(ca, oa));
+            put4(&sh.u[w][c4], fma4(oa, cu, ou));
         }
         __syncthreads();
         if (w == kWarps - 1 && jn < a.items) locate<false>(a, jn, &sh.items[at ^ 1]);
@@ -111,42 +107,28 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
             }
         }
         // while the chain goes on: the map of the rows before this warp's (the thread's, in the upper half)
-        float pa[4] = {1.f, 1.f, 1.f, 1.f}, pu[4] = {0.f, 0.f, 0.f, 0.f};
+        Four pa = four(1.f), pu = four(0.f);
         for (int i = 0; i < w; ++i) {
-            float qa[4], qu[4];
-            get4(&sh.a[i][c4], qa);
-            get4(&sh.u[i][c4], qu);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pu[e] = fmaf(qa[e], pu[e], qu[e]);
-                pa[e] *= qa[e];
-            }
+            const Four qa = get4(&sh.a[i][c4]);
+            pu = fma4(qa, pu, get4(&sh.u[i][c4]));
+            pa = mul4(pa, qa);
         }
         if (half == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pu[e] = fmaf(oa[e], pu[e], ou[e]);
-                pa[e] *= oa[e];
-            }
+            pu = fma4(oa, pu, ou);
+            pa = mul4(pa, oa);
         }
         __syncthreads();
         if (a.h && rows > 0) {
-            float h[4];
-            get4(&sh.in[c4], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = fmaf(pa[e], h[e], pu[e]);
-            with_span(n, [&](auto whole) {
-#pragma unroll
+            Four h = fma4(pa, get4(&sh.in[c4]), pu);
+            with_span<kSpan>(n, [&](auto whole) {
+#pragma unroll 8
                 for (int k = 0; k < kSpan; ++k)
                     if (whole || k < n) {
-                        float x[4], g[4];
-                        get4(sx + k * kChannels, x);
-                        get4(sg + k * kChannels, g);
+                        const Four x = get4(sx + k * kChannels), g = get4(sg + k * kChannels);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float dec, m, slope;
-                            gate<kMode, kCompl>(a.lb, g[i], dec, m, slope);
-                            h[i] = fmaf(dec, h[i], kCompl ? m * x[i] : x[i]);
+                        for (int i = 0; i < 2; ++i) {
+                            const Gated t = gate<kMode, kCompl>(a.lb, g.v[i]);
+                            h.v[i] = fma2(t.a, h.v[i], kCompl ? mul2(t.m, x.v[i]) : x.v[i]);
                         }
                         put4(sx + k * kChannels, h);
                     }
@@ -175,19 +157,23 @@ __global__ void __launch_bounds__(kScanThreads, (fwd_ctas<X, G>())) glr_fwd_kern
 }
 
 template <typename X, typename G>
-la_status by_gate(Args& a, Maps& maps, cudaStream_t s) {
+la_status by_gate(Args& a, int32_t xd, int32_t gd, cudaStream_t s) {
+    constexpr int kWarps = warps<X, G>(), kRows = 2 * span<kWarps>();
+    Maps maps = {};
+    a.tma = row_map(&maps.x, a, a.x, a.x_st, xd, kRows) && row_map(&maps.g, a, a.g, a.g_st, gd, kRows) &&
+            (!a.h || row_map(&maps.out, a, a.h, a.h_st, xd, kRows));
     la_status st = LA_ERR_INVALID_ARG;
     with_gate(a.mode, a.compl_in, [&](auto gt) {
-        st = launch_scan<glr_fwd_kernel<X, G, decltype(gt)::mode, decltype(gt)::complement>>(stage_bytes<X, G, 1>(), a, maps, s);
+        st = launch_scan<glr_fwd_kernel<X, G, decltype(gt)::mode, decltype(gt)::complement>>(32 * kWarps, stage_bytes<X, G, 1>(), a, maps, s);
     });
     return st;
 }
 
 }  // namespace
 
-la_status run_fwd(Args& a, Maps& maps, int32_t xd, int32_t gd, cudaStream_t s) {
-    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? by_gate<bf16, bf16>(a, maps, s) : by_gate<bf16, float>(a, maps, s);
-    return gd == LA_DTYPE_BF16 ? by_gate<float, bf16>(a, maps, s) : by_gate<float, float>(a, maps, s);
+la_status run_fwd(Args& a, int32_t xd, int32_t gd, cudaStream_t s) {
+    if (xd == LA_DTYPE_BF16) return gd == LA_DTYPE_BF16 ? by_gate<bf16, bf16>(a, xd, gd, s) : by_gate<bf16, float>(a, xd, gd, s);
+    return gd == LA_DTYPE_BF16 ? by_gate<float, bf16>(a, xd, gd, s) : by_gate<float, float>(a, xd, gd, s);
 }
 
 }  // namespace glr

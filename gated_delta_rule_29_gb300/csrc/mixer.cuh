@@ -77,6 +77,31 @@ __device__ __forceinline__ void store_packed(T* p, const float (&v)[kVec]) {
     }
 }
 
+// ---------------------------------------------------------------- two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // ---------------------------------------------------------------- exponentials and activations
 // e^l as 2^(l log2 e): the product's rounding is off by |l| 2^-24 of the result, which is small where
 // the result is not; results below 2^-126 are zero.
@@ -90,6 +115,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 // 1 / (1 + e^-x); e^-x may overflow to infinity, which gives the right 0.
 __device__ __forceinline__ float sigmoidf(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 
@@ -111,6 +142,29 @@ __device__ __forceinline__ float act_grad(int kind, float p, float& d) {
     }
     d = s * (1.f + p * (1.f - s));
     return p * s;
+}
+
+// The same for two values at once.
+template <int kAct>
+__device__ __forceinline__ float2 act_fwd2(float2 p) {
+    if (kAct == LA_ACT_NONE) return p;
+    const float2 t = mul2(p, both(-kLog2e));
+    const float2 q = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f)), s = make_float2(rcp_fast(q.x), rcp_fast(q.y));
+    return kAct == LA_ACT_SIGMOID ? s : mul2(p, s);
+}
+template <int kAct>
+__device__ __forceinline__ float2 act_grad2(float2 p, float2& d) {
+    if (kAct == LA_ACT_NONE) {
+        d = both(1.f);
+        return p;
+    }
+    const float2 s = act_fwd2<LA_ACT_SIGMOID>(p), rest = fma2(s, both(-1.f), both(1.f));
+    if (kAct == LA_ACT_SIGMOID) {
+        d = mul2(s, rest);
+        return s;
+    }
+    d = mul2(s, fma2(p, rest, both(1.f)));
+    return mul2(p, s);
 }
 
 // ---------------------------------------------------------------- sequence blocks

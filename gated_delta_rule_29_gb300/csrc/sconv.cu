@@ -80,7 +80,6 @@ __device__ __forceinline__ float2 staged2(const T* p) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
 
 // The input at place pos of the sequence that starts at `first`: a token, or a row of the state before it.
 template <typename X, int W>
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const
                 float2 p = bias;
 #pragma unroll
                 for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
-                put_row2<X>(py, 0, d, a.D, a.pair, make_float2(act_fwd(kAct, p.x), act_fwd(kAct, p.y)));
+                put_row2<X>(py, 0, d, a.D, a.pair, act_fwd2<kAct>(p));
                 py += a.y_st;
             };
             if (n == kSpan) {
@@ -307,9 +306,8 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                     float2 p = bias, s;
 #pragma unroll
                     for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
-                    act_grad(kAct, p.x, s.x);
-                    act_grad(kAct, p.y, s.y);
-                    dp[W - 1] = make_float2(dy.x * s.x, dy.y * s.y);
+                    act_grad2<kAct>(p, s);
+                    dp[W - 1] = mul2(dy, s);
                     if (!whole && k >= left) dp[W - 1] = win[W - 1] = make_float2(0.f, 0.f);
                 };
                 auto emit = [&](int k) {  // dx of token k, W - 1 behind
@@ -324,8 +322,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                 auto sum = [&]() {
 #pragma unroll
                     for (int j = 0; j < W; ++j) dw[j] = fma2(dp[W - 1], win[j], dw[j]);
-                    db.x += dp[W - 1].x;
-                    db.y += dp[W - 1].y;
+                    db = add2(db, dp[W - 1]);
                 };
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) {
