@@ -8,8 +8,8 @@
 //
 // The sums over the tokens apart, every token needs its W - 1 neighbours only.  A CTA takes blocks of 128
 // tokens x 64 channels (with their W - 1 rows before, and after in the backward) into shared memory by TMA,
-// the next block on its way while this one is worked on; each warp walks 32 tokens, each lane two channels
-// with the window in registers.  A CTA keeps to one channel tile: the taps stay in registers, and in the
+// the next block on its way while this one is worked on; each warp walks a span of 32 tokens (16 in the
+// backward), each lane two channels with the window in registers.  A CTA keeps to one channel tile: the taps stay in registers, and in the
 // backward (which recomputes p) so do the sums of dw and db over all its blocks, which a second kernel adds
 // over the CTAs in order.  Rows that TMA cannot move go through the same shared memory with plain loads.
 // Memory bound by its bytes (2 rows forward, 3 backward), close behind comes the arithmetic: about 16
@@ -24,8 +24,13 @@ namespace {
 using namespace la;
 using namespace la::mixer;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kDecodeThreads = 128;
-constexpr int kBlock = 128, kSpan = kBlock / kWarps;  // tokens of a block, and of a warp
+constexpr int kDecodeThreads = 128;
+constexpr int kBlock = 128;  // tokens of a block
+// Warps of a CTA, one span of the block each.  Longer spans repeat less (W - 1 tokens of a span are looked at twice
+// in the backward), more warps hide more: 8 x 8192 x 4096 bf16 forward 184 us with 4 warps, 209 with 8; the skewed
+// batch of 49344 x 2048 backward 160 and 147.
+template <bool kBackward>
+constexpr int warps() { return kBackward ? 8 : 4; }
 constexpr int kChannels = 64;                          // of a CTA, two a lane
 constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -61,18 +66,16 @@ __device__ __forceinline__ float2 row2(const void* base, int64_t at, int d, int 
     return make_float2(d < D ? to_f(p[d]) : 0.f, d + 1 < D ? to_f(p[d + 1]) : 0.f);
 }
 template <typename T>
-__device__ __forceinline__ void put_row2(void* base, int64_t at, int d, int D, int pair, float2 v) {
+__device__ __forceinline__ void put_row2(void* base, int64_t at, int d, int D, float2 v) {
     T* p = static_cast<T*>(base) + at + d;
-    if (pair) {
-        const float x[2] = {v.x, v.y};
-        if (d < D) {
-            if (sizeof(T) == 4) *reinterpret_cast<float2*>(p) = v;
-            else store_packed<T, 2>(p, x);
-        }
-        return;
-    }
     if (d < D) p[0] = from_f<T>(v.x);
     if (d + 1 < D) p[1] = from_f<T>(v.y);
+}
+// Two channels, stored as a pair.
+template <typename T>
+__device__ __forceinline__ void put2(T* p, float2 v) {
+    if (sizeof(T) == 4) *reinterpret_cast<float2*>(p) = v;
+    else *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 template <typename T>
 __device__ __forceinline__ float2 staged2(const T* p) {
@@ -155,7 +158,7 @@ struct Blocks {
     }
     __device__ __forceinline__ void copy_rows(X* to, const void* base, int64_t stride, int first, int rows) const {
 #pragma unroll 4
-        for (int e = threadIdx.x; e < rows * kChannels; e += kThreads) {
+        for (int e = threadIdx.x; e < rows * kChannels; e += 32 * warps<kBackward>()) {
             const int r = e / kChannels, c = e % kChannels, d = tile * kChannels + c;
             const int64_t t = static_cast<int64_t>(first) + r;
             if (t >= 0 && t < a.T && d < a.D) to[e] = static_cast<const X*>(base)[t * stride + d];
@@ -199,7 +202,8 @@ struct Blocks {
 };
 
 template <typename X, int W, int kAct>
-__global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(32 * warps<false>()) sconv_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    constexpr int kWarps = warps<false>(), kThreads = 32 * kWarps, kSpan = kBlock / kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const int tile = blockIdx.x % a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = tile * kChannels + 2 * lane;
@@ -221,21 +225,24 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const
                 win[j + 1] = b.c == 0 && warp == 0 ? input_at<X, W>(a, b.first, slot, j - (W - 1), d) : staged2(px + j * kChannels);
             px += (W - 1) * kChannels;
             X* py = static_cast<X*>(a.y) + (static_cast<int64_t>(b.start) + k0) * a.y_st;
-            auto token = [&](int k) {
+            const bool in = d < a.D;
+            auto token = [&](int k, auto pair) {
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
                 win[W - 1] = staged2(px + k * kChannels);
                 float2 p = bias;
 #pragma unroll
                 for (int j = 0; j < W; ++j) p = fma2(w[j], win[j], p);
-                put_row2<X>(py, 0, d, a.D, a.pair, act_fwd2<kAct>(p));
+                const float2 y = act_fwd2<kAct>(p);
+                if (!pair) put_row2<X>(py, 0, d, a.D, y);
+                else if (in) put2<X>(py + d, y);
                 py += a.y_st;
             };
-            if (n == kSpan) {
+            if (n == kSpan && a.pair) {
 #pragma unroll 8
-                for (int k = 0; k < kSpan; ++k) token(k);
+                for (int k = 0; k < kSpan; ++k) token(k, std::true_type());
             } else {
-                for (int k = 0; k < n; ++k) token(k);
+                for (int k = 0; k < n; ++k) token(k, std::false_type());
             }
         }
         // The sequence's last W - 1 inputs.  With a pool they replace the rows that the sequence started from,
@@ -247,16 +254,16 @@ __global__ void __launch_bounds__(kThreads) sconv_fwd_kernel(const Args a, const
             void* to = a.idx ? const_cast<void*>(a.s0) : a.fin;
             const int64_t row = (a.idx ? slot : b.seq) * (W - 1);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) put_row2<X>(to, (row + j) * a.D, d, a.D, 0, f[j]);
+            for (int j = 0; j < W - 1; ++j) put_row2<X>(to, (row + j) * a.D, d, a.D, f[j]);
         }
     });
 }
 
 template <typename X, int W, int kAct>
-__global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(32 * warps<true>()) sconv_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+    constexpr int kWarps = warps<true>(), kThreads = 32 * kWarps, kSpan = kBlock / kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
-    __shared__ float2 red[kWarps][W + 1][32];
     const int tile = blockIdx.x % a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = tile * kChannels + 2 * lane;
     if (tile == 0)
         for (int64_t i = (blockIdx.x / a.tiles) * static_cast<int64_t>(kThreads) + threadIdx.x; i < a.N; i += static_cast<int64_t>(a.columns) * kThreads)
@@ -292,7 +299,9 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                 dp[j + 1] = make_float2(0.f, 0.f);
             }
             px += (W - 1) * kChannels;
-            // `whole`: every token that the span reads is in the sequence, so that nothing is masked
+            // `whole`: every token that the span reads is in the sequence, so that nothing is masked, and results are
+            // stored in pairs
+            const bool in = d < a.D;
             auto walk = [&](auto whole) {
                 // one token further: win ends with token k, dp with its dp (0 beyond the end)
                 auto step = [&](int k) {
@@ -315,8 +324,8 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                     float2 dx = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < W; ++j) dx = fma2(w[j], dp[W - 1 - j], dx);
-                    if (!whole) dx = add_final(dx, p0 + k - (static_cast<int64_t>(b.len) - (W - 1)));
-                    put_row2<X>(pdx, 0, d, a.D, a.pair, dx);
+                    if (!whole) put_row2<X>(pdx, 0, d, a.D, add_final(dx, p0 + k - (static_cast<int64_t>(b.len) - (W - 1))));
+                    else if (in) put2<X>(pdx + d, dx);
                     pdx += a.dx_st;
                 };
                 auto sum = [&]() {
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                     sum();
                     dp0[k] = dp[W - 1];
                 }
-#pragma unroll 4
+#pragma unroll 8
                 for (int k = W - 1; k < kSpan; ++k) {
                     step(k);
                     sum();
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
                     emit(k - (W - 1));
                 }
             };
-            if (left >= kSpan + W - 1) walk(std::true_type());
+            if (left >= kSpan + W - 1 && a.pair) walk(std::true_type());
             else walk(std::false_type());
         } else {
 #pragma unroll
@@ -356,10 +365,12 @@ __global__ void __launch_bounds__(kThreads) sconv_bwd_kernel(const Args a, const
 #pragma unroll
                 for (int t = 0; t <= s; ++t) ds = fma2(w[s - t], dp0[t], ds);
                 ds = add_final(ds, static_cast<int64_t>(s) - b.len);
-                put_row2<X>(a.ds0, (b.seq * static_cast<int64_t>(W - 1) + s) * a.D, d, a.D, 0, ds);
+                put_row2<X>(a.ds0, (b.seq * static_cast<int64_t>(W - 1) + s) * a.D, d, a.D, ds);
             }
         }
     });
+    float2(*red)[W + 1][32] = reinterpret_cast<float2(*)[W + 1][32]>(smem);  // the stages are free
+    static_assert(sizeof(float2) * kWarps * (W + 1) * 32 <= stage_bytes<X, W, true>(), "the sums fit a stage");
 #pragma unroll
     for (int j = 0; j < W; ++j) red[warp][j][lane] = dw[j];
     red[warp][W][lane] = db;
@@ -446,13 +457,13 @@ int64_t bwd_columns(int64_t T, int32_t N, int32_t D) {
 }
 
 template <auto kKernel>
-la_status launch_blocks(size_t smem, const Args& a, const Maps& maps, cudaStream_t s) {
+la_status launch_blocks(int threads, size_t smem, const Args& a, const Maps& maps, cudaStream_t s) {
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
         (void)cudaGetLastError();
         return LA_ERR_CUDA;
     }
-    kKernel<<<static_cast<unsigned>(a.tiles * a.columns), kThreads, smem, s>>>(a, maps);
+    kKernel<<<static_cast<unsigned>(a.tiles * a.columns), threads, smem, s>>>(a, maps);
     return launched();
 }
 
@@ -476,8 +487,8 @@ la_status run_blocks(Args& a, bool bwd, int32_t xd, cudaStream_t s) {
     const int depth = a.tma ? stages<X>() : 1;
     auto start = [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        return bwd ? launch_blocks<sconv_bwd_kernel<X, W, kAct>>(depth * stage_bytes<X, W, true>(), a, maps, s)
-                   : launch_blocks<sconv_fwd_kernel<X, W, kAct>>(depth * stage_bytes<X, W, false>(), a, maps, s);
+        return bwd ? launch_blocks<sconv_bwd_kernel<X, W, kAct>>(32 * warps<true>(), depth * stage_bytes<X, W, true>(), a, maps, s)
+                   : launch_blocks<sconv_fwd_kernel<X, W, kAct>>(32 * warps<false>(), depth * stage_bytes<X, W, false>(), a, maps, s);
     };
     if (a.act == LA_ACT_SILU) return start(std::integral_constant<int, LA_ACT_SILU>());
     if (a.act == LA_ACT_SIGMOID) return start(std::integral_constant<int, LA_ACT_SIGMOID>());
