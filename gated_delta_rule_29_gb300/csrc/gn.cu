@@ -320,30 +320,29 @@ __global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const flo
 }
 
 // ---------------------------------------------------------------- shapes
-// How a row is spread over lanes: vectors of 16 bytes, of 8 (bf16), or single elements; as few lanes as
-// hold it at one vector each, up to a warp, then more vectors a lane up to kPerLane elements, then the
-// whole CTA.
+// How a row is spread over lanes: vectors of 16 bytes, of 8 (bf16), or single elements; as few lanes as hold it at 8
+// elements each, up to a warp (the fewer lanes, the fewer shuffles a row), then up to kPerLane elements a lane, then
+// the whole CTA.
 constexpr int kPerLane = 32;
 
 struct Shape {
-    int vec, lanes, nv;
+    int lanes, nv;
 };
 Shape shape(int V, int vec) {
-    Shape s = {vec, 1, 1};
-    const int n = V / vec;
-    while (s.lanes < 32 && s.lanes < n) s.lanes *= 2;
-    if (n > 32 * (kPerLane / vec)) s.lanes = kThreads;
+    const int n = (V + vec - 1) / vec;  // vectors
+    Shape s = {1, 1};
+    while (s.lanes < 32 && s.lanes * (8 / vec) < n) s.lanes *= 2;
+    if (V > 32 * kPerLane) s.lanes = kThreads;
     s.nv = (n + s.lanes - 1) / s.lanes;
     return s;
 }
 
 // CTAs of the backward: a few waves' worth, with at least kMinRows rows for a group of lanes, and a
-// multiple of the heads where each CTA keeps to one.  By V alone, not by the alignment, so that the
+// multiple of the heads where each CTA keeps to one.  The lanes of a row do not depend on its alignment, so the
 // workspace's size follows from the shape.
 constexpr int kMaxCtas = 152 * 6, kMinRows = 8;
 int64_t bwd_ctas(int64_t T, int H, int V, int per_head) {
     const int64_t rows = T * H, most = rows / kMinRows;
-    // groups of a CTA at single elements a lane, the fewest there can be
     const int64_t groups = kThreads / shape(V, 1).lanes;
     int64_t n = std::max<int64_t>(1, std::min<int64_t>(kMaxCtas, most / groups));
     if (per_head) n = (n + H - 1) / H * H;
@@ -360,7 +359,7 @@ la_status launch(const Args& a, bool bwd, cudaStream_t s) {
         if (a.b) gn_bwd_kernel<X, kVec, NV, kBlock, true><<<grid, kThreads, smem, s>>>(a);
         else gn_bwd_kernel<X, kVec, NV, kBlock, false><<<grid, kThreads, smem, s>>>(a);
     } else {
-        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 16);
+        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 8);
         if (a.per_head) grid = (grid + a.H - 1) / a.H * a.H;
         else grid = std::max<int64_t>(grid, (a.H + groups - 1) / groups);
         gn_fwd_kernel<X, kVec, NV, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
@@ -375,8 +374,7 @@ la_status by_row(Args& a, bool bwd, cudaStream_t s) {
     constexpr int kMost = kPerLane / kVec;
     a.lanes = r.lanes;
     if (r.lanes == kThreads) return launch<X, kVec, kMost, true>(a, bwd, s);
-    if (r.nv == 1) return launch<X, kVec, 1, false>(a, bwd, s);
-    if (r.nv <= kMost / 4) return launch<X, kVec, (kMost / 4 > 1 ? kMost / 4 : 2), false>(a, bwd, s);
+    if (r.nv <= kMost / 4) return launch<X, kVec, kMost / 4, false>(a, bwd, s);
     return launch<X, kVec, kMost, false>(a, bwd, s);
 }
 

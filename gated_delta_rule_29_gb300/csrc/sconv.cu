@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(32 * warps<false>()) sconv_fwd_kernel(const Ar
                 py += a.y_st;
             };
             if (n == kSpan && a.pair) {
-#pragma unroll 8
+#pragma unroll 2
                 for (int k = 0; k < kSpan; ++k) token(k, std::true_type());
             } else {
                 for (int k = 0; k < n; ++k) token(k, std::false_type());
