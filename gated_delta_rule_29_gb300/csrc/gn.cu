@@ -78,10 +78,8 @@ __device__ __forceinline__ Walk walk(const Args& a) {
     return r;
 }
 
-// Vector k of a lane starts at channel (lane + k * lanes) * kVec.
-#define LA_EACH_VECTOR(k, c)                                                        \
-    _Pragma("unroll") for (int k = 0; k < NV; ++k) if (const int c = (lane + k * a.lanes) * kVec; c < a.V)
-
+// A lane's part of a row: NV vectors of kVec elements, vector k from channel (lane + k * lanes) * kVec on; in fp32 as
+// pairs, element e being element e % kVec of vector e / kVec.
 template <typename X, int kVec, int NV>
 __device__ __forceinline__ void load_row(Packed<X, kVec> (&v)[NV], const void* base, int64_t at, bool live, int lane, const Args& a) {
 #pragma unroll
@@ -91,45 +89,71 @@ __device__ __forceinline__ void load_row(Packed<X, kVec> (&v)[NV], const void* b
         else v[k].zero();
     }
 }
-
-// n from a row; returns r.  Places beyond V stay 0.
-template <typename X, int kVec, int NV, bool kBlock>
-__device__ __forceinline__ float normalise(const Packed<X, kVec> (&raw)[NV], float (&x)[NV][kVec], const Args& a, float inv_v, int lane, float* red) {
-    float s = 0.f, mu = 0.f;
-    if (a.center) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) s += raw[k].get(i);
-        mu = row_sum<kBlock>(s, a.lanes, red) * inv_v;
-        s = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const bool in = (lane + k * a.lanes) * kVec < a.V;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            x[k][i] = in ? raw[k].get(i) - mu : 0.f;
-            s = fmaf(x[k][i], x[k][i], s);
-        }
-    }
-    const float r = 1.f / sqrtf(row_sum<kBlock>(s, a.lanes, red) * inv_v + a.eps);
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) x[k][i] *= r;
-    return r;
+template <typename X, int kVec, int NV>
+__device__ __forceinline__ float2 pair_of(const Packed<X, kVec> (&v)[NV], int j) {
+    return make_float2(v[2 * j / kVec].get(2 * j % kVec), v[(2 * j + 1) / kVec].get((2 * j + 1) % kVec));
 }
-
-template <int kVec, int NV>
-__device__ __forceinline__ void load_weights(float (&w)[NV][kVec], const void* p, int h, int lane, float missing, const Args& a) {
+template <typename X, int kVec, int NV>
+__device__ __forceinline__ void store_row(X* to, const float2 (&v)[NV * kVec / 2], int lane, const Args& a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (lane + k * a.lanes) * kVec;
+        float y[kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            w[k][i] = p && c < a.V ? load_any(p, (a.per_head ? static_cast<int64_t>(h) * a.V : 0) + c + i, a.w_bf16) : missing;
+        for (int i = 0; i < kVec; ++i) y[i] = (k * kVec + i) % 2 ? v[(k * kVec + i) / 2].y : v[(k * kVec + i) / 2].x;
+        if (c < a.V) store_packed<X, kVec>(to + c, y);
     }
+}
+
+// n from a row; returns r.  Places beyond V stay 0.
+template <typename X, int kVec, int NV, bool kBlock>
+__device__ __forceinline__ float normalise(const Packed<X, kVec> (&raw)[NV], float2 (&x)[NV * kVec / 2], const Args& a, float inv_v, int lane, float* red) {
+    constexpr int kPairs = NV * kVec / 2;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) x[j] = pair_of<X, kVec, NV>(raw, j);
+    float2 s;
+    if (a.center) {
+        s = x[0];
+#pragma unroll
+        for (int j = 1; j < kPairs; ++j) s = add2(s, x[j]);
+        const float mu = row_sum<kBlock>(s.x + s.y, a.lanes, red) * inv_v;
+        // what is subtracted from each of a pair's elements: the mean, but 0 beyond V
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const int k0 = 2 * j / kVec, k1 = (2 * j + 1) / kVec;
+            x[j] = add2(x[j], make_float2((lane + k0 * a.lanes) * kVec < a.V ? -mu : 0.f, (lane + k1 * a.lanes) * kVec < a.V ? -mu : 0.f));
+        }
+    }
+    s = mul2(x[0], x[0]);
+#pragma unroll
+    for (int j = 1; j < kPairs; ++j) s = fma2(x[j], x[j], s);
+    const float v = fmaf(row_sum<kBlock>(s.x + s.y, a.lanes, red), inv_v, a.eps);
+    // the reciprocal square root and one step of Newton's method for 1 / r^2 = v (where r^2 v is finite)
+    const float r0 = rsqrtf(v), e = fmaf(-v * r0, r0, 1.f), r = fabsf(e) < 0.5f ? fmaf(0.5f * r0, e, r0) : r0;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) x[j] = mul2(x[j], both(r));
+    return r;
+}
+
+// A parameter's values for a lane's channels.
+template <typename W, int kVec, int NV>
+__device__ __forceinline__ void load_parameter(float2 (&w)[NV * kVec / 2], const void* p, int64_t at, int lane, const Args& a) {
+    float e[NV * kVec];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int c = (lane + k * a.lanes) * kVec + i;
+            e[k * kVec + i] = p && c < a.V ? to_f(static_cast<const W*>(p)[at + c]) : 0.f;
+        }
+#pragma unroll
+    for (int j = 0; j < NV * kVec / 2; ++j) w[j] = make_float2(e[2 * j], e[2 * j + 1]);
+}
+template <int kVec, int NV>
+__device__ __forceinline__ void load_weights(float2 (&w)[NV * kVec / 2], const void* p, int h, int lane, const Args& a) {
+    const int64_t at = a.per_head ? static_cast<int64_t>(h) * a.V : 0;
+    if (a.w_bf16) load_parameter<bf16, kVec, NV>(w, p, at, lane, a);
+    else load_parameter<float, kVec, NV>(w, p, at, lane, a);
 }
 
 // Calls f with the activation and whether it is a gate's as constants.
@@ -153,15 +177,16 @@ __device__ __forceinline__ void with_act(const Args& a, F f) {
 constexpr int ctas(int elements, int few, int many) { return elements <= 8 ? many : elements <= 16 ? few : 1; }
 
 template <typename X, int kVec, int NV, bool kBlock>
-__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, 4)) gn_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, sizeof(X) == 4 ? 3 : 4)) gn_fwd_kernel(const Args a) {
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
     const Walk r = walk(a);
     const int64_t rounds = (a.T + r.step - 1) / r.step;  // the same for every lane of a warp: the shuffles need them all
     const float inv_v = 1.f / a.V;
-    float w[NV][kVec], b[NV][kVec];
-    load_weights<kVec, NV>(w, a.w, r.h, lane, 0.f, a);
-    load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
+    constexpr int kPairs = NV * kVec / 2;
+    float2 w[kPairs], b[kPairs];
+    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
+    load_weights<kVec, NV>(b, a.b, r.h, lane, a);
     Packed<X, kVec> raw[NV], z[NV], next[NV], next_z[NV];
     auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], int64_t t) {
         load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
@@ -183,35 +208,34 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, 4)) gn_fwd_kernel
         } else {
             load(raw, z, t);
         }
-        float x[NV][kVec];
+        float2 x[kPairs];
         normalise<X, kVec, NV, kBlock>(raw, x, a, inv_v, lane, red);
         if (!live) continue;
-        X* to = static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh;
-        LA_EACH_VECTOR(k, c) {
-            float y[kVec];
-            with_act(a, [&](auto act, auto gated) {
+        with_act(a, [&](auto act, auto gated) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const float p = fmaf(x[k][i], w[k][i], b[k][i]);
-                    y[i] = gated ? p * act_fwd(act, z[k].get(i)) : act_fwd(act, p);
-                }
-            });
-            store_packed<X, kVec>(to + c, y);
-        }
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 p = fma2(x[j], w[j], b[j]);
+                x[j] = gated ? mul2(p, act_fwd2<act>(pair_of<X, kVec, NV>(z, j))) : act_fwd2<act>(p);
+            }
+        });
+        store_row<X, kVec, NV>(static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh, x, lane, a);
     }
 }
 
 template <typename X, int kVec, int NV, bool kBlock, bool kBias>
-__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias && NV * kVec == 8 ? 2 : 3)) gn_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X) == 4 ? 2 : 3)) gn_bwd_kernel(const Args a) {
     extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
     const Walk r = walk(a);
     const int64_t rounds = (a.T + r.step - 1) / r.step;
     const float inv_v = 1.f / a.V;
-    float w[NV][kVec], b[NV][kVec], dw[NV][kVec] = {}, db[NV][kVec] = {};  // b and db: unused without a bias
-    load_weights<kVec, NV>(w, a.w, r.h, lane, 0.f, a);
-    if (kBias) load_weights<kVec, NV>(b, a.b, r.h, lane, 0.f, a);
+    constexpr int kPairs = NV * kVec / 2;
+    float2 w[kPairs], b[kPairs], dw[kPairs], db[kPairs];  // b and db: unused without a bias
+    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
+    if (kBias) load_weights<kVec, NV>(b, a.b, r.h, lane, a);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) dw[j] = db[j] = both(0.f);
     Packed<X, kVec> raw[NV], z[NV], dy[NV], next[NV], next_z[NV], next_dy[NV];
     auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], Packed<X, kVec> (&d)[NV], int64_t t) {
         load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
@@ -234,48 +258,41 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias && NV * kVe
         } else {
             load(raw, z, dy, t);
         }
-        float n[NV][kVec], g[NV][kVec];
+        float2 n[kPairs], g[kPairs], sg = both(0.f), sgn = both(0.f);
         const float rs = normalise<X, kVec, NV, kBlock>(raw, n, a, inv_v, lane, red);
-        float sg = 0.f, sgn = 0.f;
+        X* to_dz = static_cast<X*>(a.dz) + t * a.dz_st + r.h * a.dz_sh;
+        with_act(a, [&](auto act, auto gated) {
+            float2 dz[kPairs];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float dz[kVec];
-            with_act(a, [&](auto act, auto gated) {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const float p = kBias ? fmaf(n[k][i], w[k][i], b[k][i]) : n[k][i] * w[k][i];
-                    float d, v = dy[k].get(i);  // 0 beyond V and where not live, and so is all that follows from it
-                    if (gated) {
-                        const float f = act_grad(act, z[k].get(i), d);
-                        dz[i] = v * p * d;
-                        g[k][i] = v * f;
-                    } else {
-                        act_grad(act, p, d);
-                        g[k][i] = v * d;
-                    }
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 p = kBias ? fma2(n[j], w[j], b[j]) : mul2(n[j], w[j]);
+                const float2 v = pair_of<X, kVec, NV>(dy, j);  // 0 beyond V and where not live, and so is all that follows from it
+                float2 d;
+                if (gated) {
+                    const float2 f = act_grad2<act>(pair_of<X, kVec, NV>(z, j), d);
+                    dz[j] = mul2(mul2(v, p), d);
+                    g[j] = mul2(v, f);
+                } else {
+                    act_grad2<act>(p, d);
+                    g[j] = mul2(v, d);
                 }
-            });
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                dw[k][i] = fmaf(g[k][i], n[k][i], dw[k][i]);
-                if (kBias) db[k][i] += g[k][i];
-                g[k][i] *= w[k][i];
-                sg += g[k][i];
-                sgn = fmaf(g[k][i], n[k][i], sgn);
             }
-            const int c = (lane + k * a.lanes) * kVec;
-            if (a.z && live && c < a.V) store_packed<X, kVec>(static_cast<X*>(a.dz) + t * a.dz_st + r.h * a.dz_sh + c, dz);
-        }
-        const float mg = a.center ? row_sum<kBlock>(sg, a.lanes, red) * inv_v : 0.f;
-        const float mgn = row_sum<kBlock>(sgn, a.lanes, red) * inv_v;
-        if (!live) continue;
-        X* to = static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh;
-        LA_EACH_VECTOR(k, c) {
-            float dx[kVec];
+            if (gated && live) store_row<X, kVec, NV>(to_dz, dz, lane, a);
+        });
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) dx[i] = rs * (g[k][i] - mg - n[k][i] * mgn);
-            store_packed<X, kVec>(to + c, dx);
+        for (int j = 0; j < kPairs; ++j) {
+            dw[j] = fma2(g[j], n[j], dw[j]);
+            if (kBias) db[j] = add2(db[j], g[j]);
+            g[j] = mul2(g[j], w[j]);
+            sg = add2(sg, g[j]);
+            sgn = fma2(g[j], n[j], sgn);
         }
+        const float mg = a.center ? row_sum<kBlock>(sg.x + sg.y, a.lanes, red) * inv_v : 0.f;
+        const float mgn = row_sum<kBlock>(sgn.x + sgn.y, a.lanes, red) * inv_v;
+        if (!live) continue;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) g[j] = mul2(both(rs), fma2(n[j], both(-mgn), add2(g[j], both(-mg))));
+        store_row<X, kVec, NV>(static_cast<X*>(a.y) + t * a.y_st + r.h * a.y_sh, g, lane, a);
     }
     // the CTA's sums, group by group
     const int groups = kThreads / a.lanes, u = threadIdx.x / a.lanes;
@@ -283,9 +300,11 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias && NV * kVe
     for (int which = 0; which < (kBias ? 2 : 1); ++which) {
         float* out = which ? a.pb : a.pw;
         __syncthreads();
-        LA_EACH_VECTOR(k, c) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) sums[u * a.V + c + i] = which ? db[k][i] : dw[k][i];
+        for (int e = 0; e < NV * kVec; ++e) {
+            const int c = (lane + e / kVec * a.lanes) * kVec + e % kVec;
+            const float2 v = which ? db[e / 2] : dw[e / 2];
+            if (c < a.V) sums[u * a.V + c] = e % 2 ? v.y : v.x;
         }
         __syncthreads();
         for (int c = threadIdx.x; c < a.V; c += kThreads) {
