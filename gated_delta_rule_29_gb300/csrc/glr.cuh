@@ -47,18 +47,34 @@ constexpr uint64_t kWaitNs = 1000000000ull;      // a bounded wait gives up afte
 template <int kWarps>
 constexpr int span() { return kBlock / kWarps / 2; }
 
-// 1 - e^l given e^l, for two values: the Taylor series (to l^7 / 7!, 2e-7 of it at 1/2) where the difference would
-// cancel.
-__device__ __forceinline__ float2 one_minus_exp(float2 l, float2 e) {
-    float2 p = fma2(l, both(1.f / 7.f), both(1.f));
-    p = fma2(mul2(l, both(1.f / 6.f)), p, both(1.f));
-    p = fma2(mul2(l, both(1.f / 5.f)), p, both(1.f));
-    p = fma2(mul2(l, both(1.f / 4.f)), p, both(1.f));
-    p = fma2(mul2(l, both(1.f / 3.f)), p, both(1.f));
-    p = fma2(mul2(l, both(1.f / 2.f)), p, both(1.f));
-    p = mul2(mul2(l, both(-1.f)), p);
-    const float2 d = fma2(e, both(-1.f), both(1.f));
-    return make_float2(fabsf(l.x) < 0.5f ? p.x : d.x, fabsf(l.y) < 0.5f ? p.y : d.y);
+// e^l and, for the complement, 1 - e^l, of two values.  kNear: l itself is the input, so that decays near 1 may be
+// the same for many tokens, and an error in them adds up over some 1 / |l| tokens; ex2's is not evenly spread there,
+// and below 1/16 the Taylor series to l^4 (off by 8e-9) takes its place (the bounded gate's l differ from token to
+// token: their errors average out, and the series costs a seventh of its forward's time).  With the complement the
+// series goes to l^7 and 1/2 (2e-7 of 1 - e^l there), as the difference would cancel.
+template <bool kComplement, bool kNear>
+__device__ __forceinline__ void exp_both(float2 l, float2& e, float2& rest) {
+    const float2 t = mul2(l, both(kLog2e));
+    e = make_float2(ex2(t.x), ex2(t.y));
+    rest = both(1.f);
+    if (!kComplement && !kNear) return;
+    float2 q = both(1.f / 24.f);  // (e^l - 1) / l
+    if (kComplement) {
+        q = fma2(l, both(1.f / 5040.f), both(1.f / 720.f));
+        q = fma2(l, q, both(1.f / 120.f));
+        q = fma2(l, q, both(1.f / 24.f));
+    }
+    q = fma2(l, q, both(1.f / 6.f));
+    q = fma2(l, q, both(0.5f));
+    q = fma2(l, q, both(1.f));
+    const float2 p = fma2(l, q, both(1.f));
+    constexpr float kSmall = kComplement ? 0.5f : 0.0625f;
+    const bool s0 = fabsf(l.x) < kSmall, s1 = fabsf(l.y) < kSmall;
+    if (kComplement) {
+        const float2 r = mul2(mul2(l, both(-1.f)), q), d = fma2(e, both(-1.f), both(1.f));
+        rest = make_float2(s0 ? r.x : d.x, s1 ? r.y : d.y);
+    }
+    e = make_float2(s0 ? p.x : e.x, s1 ? p.y : e.y);
 }
 
 // a, m and dl/dg of two gate values.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g), held below 2^115 so
@@ -86,9 +102,7 @@ __device__ __forceinline__ Gated gate(float lb, float2 g) {
         l = mul2(both(lb), s);
         r.slope = mul2(l, rest);
     }
-    const float2 t = mul2(l, both(kLog2e));
-    r.a = make_float2(ex2(t.x), ex2(t.y));
-    r.m = kComplement ? one_minus_exp(l, r.a) : both(1.f);
+    exp_both<kComplement, kMode == LA_GATE_LOG>(l, r.a, r.m);
     return r;
 }
 
