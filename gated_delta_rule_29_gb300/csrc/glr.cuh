@@ -193,6 +193,7 @@ template <typename T>
 __device__ __forceinline__ void rows_in(T* s, const void* base, int64_t stride, int64_t token, int n, int d, int D) {
     const int lane = threadIdx.x & 31;
     const T* p = static_cast<const T*>(base) + token * stride + d;
+#pragma unroll 8
     for (int r = 0; r < n; ++r)
 #pragma unroll
         for (int c = 0; c < kChannels; c += 32) s[r * kChannels + c + lane] = d + c + lane < D ? p[r * stride + c + lane] : from_f<T>(0.f);

@@ -59,6 +59,7 @@ template <typename T, int kVec>
 __device__ __forceinline__ void store_packed(T* p, const float (&v)[kVec]) {
     if (sizeof(T) == 4) {
         if (kVec == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[kVec > 1 ? 1 : 0], v[kVec > 2 ? 2 : 0], v[kVec > 3 ? 3 : 0]);
+        else if (kVec == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[kVec > 1 ? 1 : 0]);
         else
 #pragma unroll
             for (int i = 0; i < kVec; ++i) p[i] = from_f<T>(v[i]);
