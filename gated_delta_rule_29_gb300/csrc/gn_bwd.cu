@@ -15,10 +15,6 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X
     const float inv_v = 1.f / a.V;
     constexpr int kPairs = NV * kVec / 2;
     float2 w[kPairs], b[kPairs], dw[kPairs], db[kPairs];  // b and db: unused without a bias
-    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
-    if (kBias) load_weights<kVec, NV>(b, a.b, r.h, lane, a);
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) dw[j] = db[j] = both(0.f);
     Packed<X, kVec> raw[NV], z[NV], dy[NV], next[NV], next_z[NV], next_dy[NV];
     auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], Packed<X, kVec> (&d)[NV], int64_t t) {
         load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
@@ -28,6 +24,10 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X
     constexpr bool kAhead = NV * kVec <= 8 && kVec * sizeof(X) >= 8;
     int64_t t = r.t0;
     if (kAhead) load(next, next_z, next_dy, t);
+    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
+    if (kBias) load_weights<kVec, NV>(b, a.b, r.h, lane, a);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) dw[j] = db[j] = both(0.f);
     for (int64_t round = 0; round < rounds; ++round, t += r.step) {
         const bool live = t < a.T;
         if (kAhead) {

@@ -14,8 +14,6 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, sizeof(X) == 4 ||
     const float inv_v = 1.f / a.V;
     constexpr int kPairs = NV * kVec / 2;
     float2 w[kPairs], b[kPairs];
-    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
-    load_weights<kVec, NV>(b, a.b, r.h, lane, a);
     Packed<X, kVec> raw[NV], z[NV], next[NV], next_z[NV];
     auto load = [&](Packed<X, kVec> (&x)[NV], Packed<X, kVec> (&g)[NV], int64_t t) {
         load_row<X, kVec, NV>(x, a.x, t * a.x_st + r.h * a.x_sh, t < a.T, lane, a);
@@ -25,6 +23,8 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, sizeof(X) == 4 ||
     constexpr bool kAhead = NV * kVec <= 8 && kVec * sizeof(X) >= 8;
     int64_t t = r.t0;
     if (kAhead) load(next, next_z, t);
+    load_weights<kVec, NV>(w, a.w, r.h, lane, a);
+    load_weights<kVec, NV>(b, a.b, r.h, lane, a);
     for (int64_t n = 0; n < rounds; ++n, t += r.step) {
         const bool live = t < a.T;
         if (kAhead) {

@@ -39,13 +39,13 @@ def _rows(name: str, x, rank: int, like: Optional[torch.Tensor] = None) -> tuple
     shape and device it must have."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape, strides = x.shape, x.stride()
-    if len(shape) != rank:
-        raise ValueError(f"{name} must be rank {rank}, got shape {tuple(shape)}")
-    if strides[-1] != 1 and shape[-1] > 1:
+    strides = x.stride()
+    if len(strides) != rank:
+        raise ValueError(f"{name} must be rank {rank}, got shape {tuple(x.shape)}")
+    if strides[-1] != 1 and x.shape[-1] > 1:
         raise ValueError(f"{name} must have a contiguous innermost axis")
-    if like is not None and (shape != like.shape or x.get_device() != like.get_device()):
-        raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(shape)} on {x.device}")
+    if like is not None and (x.shape != like.shape or x.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(x.shape)} on {x.device}")
     return strides
 
 
@@ -75,7 +75,7 @@ def _result(name: str, x: Optional[torch.Tensor], like: torch.Tensor) -> tuple:
 
 def _state_dest(name: str, x: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, like: torch.Tensor) -> tuple:
     if x is None:
-        x = like.new_empty(shape, dtype=dtype)
+        x = torch.empty(shape, dtype=dtype, device=like.device)
         return x, x.data_ptr()
     return x, _packed(name, x, shape, (dtype,), like)
 
@@ -446,7 +446,7 @@ def sconv_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, d
     if bias is not None:
         d_bias = torch.empty_like(bias)
         p.d_bias = d_bias.data_ptr()
-    d_initial_state = x.new_empty((N, max(W - 1, 0), D))
+    d_initial_state = torch.empty((N, max(W - 1, 0), D), dtype=x.dtype, device=x.device)
     p.d_initial_state = d_initial_state.data_ptr()
     ws = _workspace(p, workspace, B.load().la_sconv_bwd_workspace_bytes(T, N, D, W), x)  # noqa: F841
     if status is not None:
