@@ -10,6 +10,8 @@ using namespace la::glr;
 
 constexpr int kThreads = 128;
 
+// One thread a channel: a step of 8 x 2048 takes 4 us on the GPU, all latency (state index, then state), and the call
+// 12 us of host time.
 template <typename X, typename G>
 __global__ void __launch_bounds__(kThreads) glr_decode_kernel(const Args a) {
     const int i = blockIdx.y + gridDim.y * blockIdx.z;

@@ -14,6 +14,10 @@ constexpr int warps() { return sizeof(X) + sizeof(G) == 4 ? 4 : 8; }
 template <typename X, typename G>
 constexpr int ctas() { return sizeof(X) + sizeof(G) == 4 ? 6 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
 
+// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 350 us, 6.1 TB/s (92 % of the measured copy rate), bound by
+// its bytes; with bf16 logits of a complement gate 300 us, 5.4 TB/s, where the gate evaluated twice (16 of 28
+// instructions an element) takes over half of the issue slots.  One sequence of 131072 x 1000: 195 us, 4.0 TB/s:
+// every block waits for the slowest of the 57 blocks of its channels that are in flight before it.
 template <typename X, typename G, int kMode, bool kCompl>
 __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
     constexpr int kWarps = warps<X, G>(), kSpan = span<kWarps>(), kWarpRows = 2 * kSpan;
