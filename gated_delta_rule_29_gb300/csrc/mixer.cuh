@@ -104,48 +104,28 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // ---------------------------------------------------------------- exponentials and activations
-// e^l as 2^(l log2 e): the product's rounding is off by |l| 2^-24 of the result, which is small where
-// the result is not; results below 2^-126 are zero.
-__device__ __forceinline__ float exp_fast(float l) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l * 1.4426950408889634f));
-    return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// e^l is ex2(l kLog2e): the product's rounding is off by |l| 2^-24 of the result, which is small where the result is
+// not; results below 2^-126 are zero.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 1 / (1 + e^-x); e^-x may overflow to infinity, which gives the right 0.
-__device__ __forceinline__ float sigmoidf(float x) { return rcp_fast(1.f + exp_fast(-x)); }
+__device__ __forceinline__ float sigmoidf(float x) { return rcp_fast(1.f + ex2(-x * kLog2e)); }
 
 __device__ __forceinline__ float act_fwd(int kind, float p) {
     if (kind == LA_ACT_NONE) return p;
     const float s = sigmoidf(p);
     return kind == LA_ACT_SIGMOID ? s : p * s;
 }
-// act(p) and act'(p).  silu' = s (1 + p (1 - s)); sigmoid' = s (1 - s).
-__device__ __forceinline__ float act_grad(int kind, float p, float& d) {
-    if (kind == LA_ACT_NONE) {
-        d = 1.f;
-        return p;
-    }
-    const float s = sigmoidf(p);
-    if (kind == LA_ACT_SIGMOID) {
-        d = s * (1.f - s);
-        return s;
-    }
-    d = s * (1.f + p * (1.f - s));
-    return p * s;
-}
-
-// The same for two values at once.
+// The same for two values at once, and act' beside it: silu' = s (1 + p (1 - s)), sigmoid' = s (1 - s).
 template <int kAct>
 __device__ __forceinline__ float2 act_fwd2(float2 p) {
     if (kAct == LA_ACT_NONE) return p;
