@@ -137,8 +137,8 @@ struct Args {
     int32_t* status;
     int tiles;         // channel tiles
     int64_t items;     // (T / kBlock + N) * tiles
-    ulonglong2* maps;  // [items][32]: (A, B) of a lane's two channels; null when no sequence has two blocks
-    uint2* states;     // [items][32]: the states leaving the item
+    ulonglong2* maps;  // [slots][tiles][32]: (A, B) of a lane's two channels; null when no sequence has two blocks
+    uint2* states;     // [slots][tiles][32]: the states leaving the block
     int tma;           // every operand can move by TMA
 };
 
@@ -218,41 +218,87 @@ __device__ __forceinline__ void store2_any(void* base, int64_t at, int d, int D,
 }
 
 // ---------------------------------------------------------------- items and the chain between them
-// Item j is block `slot` and channel tile j mod tiles; slots ascend in the forward and descend in the
-// backward, so that the neighbour whose state an item needs is item j - tiles.
+// Item j is channel tile j mod tiles of a block.  Up to 32 sequences are taken side by side, first the first block
+// of each (the last, in the backward), then the second of each that has one, and so on: the state that a block needs
+// was then published a round of items earlier, and is read ahead of its rows (`peek`).  More sequences, and a single
+// one, go slot by slot.  Either way a block comes after the one whose state it needs, its neighbour in the table of
+// slots.
 struct Item {
     int32_t start, count;  // tokens of the block
     int32_t d;             // first channel
     int32_t order;         // place in the sequence's chain: 0 needs no neighbour
-    int32_t slot;          // block slot (the checkpoint row)
+    int32_t slot;          // block slot (the checkpoint row); its words in the table: slot * tiles + tile
     int32_t state;         // row of the initial state
+    int32_t tile;
     bool last, dead;       // end of the chain; nothing to do (no block, or a bad state index)
 };
 
 // By a whole warp.
 template <bool kBackward>
 __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
+    const int lane = threadIdx.x & 31;
     Item it;
     const int32_t s = static_cast<int32_t>(j / a.tiles);
-    it.slot = kBackward ? static_cast<int32_t>(a.T / kBlock) + a.N - 1 - s : s;
-    it.d = static_cast<int32_t>(j - static_cast<int64_t>(s) * a.tiles) * kChannels;
-    const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, it.slot);
-    it.start = b.start;
-    it.count = b.count;
-    it.dead = b.seq < 0;
-    const int32_t blocks = max(1, (b.len + kBlock - 1) / kBlock);
-    it.order = kBackward ? blocks - 1 - b.c : b.c;
+    it.tile = static_cast<int32_t>(j - static_cast<int64_t>(s) * a.tiles);
+    it.d = it.tile * kChannels;
+    int32_t seq = -1, start = 0, len = 0, c = 0;
+    if (a.N > 1 && a.N <= 32) {
+        // lane i holds sequence i; the blocks of rounds before round r are sum_i min(blocks_i, r)
+        int64_t s0 = 0, s1 = -1;
+        if (lane < a.N) {
+            s0 = cu_load(a.cu, a.cu64, lane);
+            s1 = cu_load(a.cu, a.cu64, lane + 1);
+        }
+        const bool valid = s0 >= 0 && s1 >= s0 && s1 <= a.T;
+        const uint32_t mine = valid ? max(1u, static_cast<uint32_t>((s1 - s0 + kBlock - 1) / kBlock)) : 0u;
+        uint32_t lo = 0, hi = __reduce_max_sync(0xffffffffu, mine), before = 0;
+        while (lo < hi) {  // the last round that begins at or before block s
+            const uint32_t mid = (lo + hi + 1) / 2, sum = __reduce_add_sync(0xffffffffu, min(mine, mid));
+            if (sum <= static_cast<uint32_t>(s)) {
+                lo = mid;
+                before = sum;
+            } else {
+                hi = mid - 1;
+            }
+        }
+        const unsigned in_round = __ballot_sync(0xffffffffu, mine > lo);
+        const int nth = static_cast<int>(s - before) + 1;  // of those that have this round
+        const bool chosen = (in_round >> lane & 1u) && __popc(in_round & ((2u << lane) - 1u)) == nth;
+        const unsigned who = __ballot_sync(0xffffffffu, chosen);
+        if (who) {
+            seq = __ffs(who) - 1;
+            const int32_t first = __shfl_sync(0xffffffffu, static_cast<int32_t>(s0), seq);
+            len = __shfl_sync(0xffffffffu, static_cast<int32_t>(s1 - s0), seq);
+            const int32_t blocks = static_cast<int32_t>(__shfl_sync(0xffffffffu, mine, seq));
+            c = kBackward ? blocks - 1 - static_cast<int32_t>(lo) : static_cast<int32_t>(lo);
+            start = first + c * kBlock;
+            it.slot = first / kBlock + seq + c;
+            it.count = min(kBlock, first + len - start);
+        }
+    } else {
+        it.slot = kBackward ? static_cast<int32_t>(a.T / kBlock) + a.N - 1 - s : s;
+        const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, it.slot);
+        seq = b.seq;
+        start = b.start;
+        len = b.len;
+        c = b.c;
+        it.count = b.count;
+    }
+    it.start = start;
+    it.dead = seq < 0;
+    const int32_t blocks = max(1, (len + kBlock - 1) / kBlock);
+    it.order = kBackward ? blocks - 1 - c : c;
     it.last = it.order == blocks - 1;
-    it.state = b.seq;
+    it.state = seq;
     if (!kBackward && a.idx && !it.dead) {
-        it.state = a.idx[b.seq];
+        it.state = a.idx[seq];
         if (it.state < 0 || it.state >= a.pool) {
             raise_status(a.status, LA_ERR_BAD_STATE_INDEX);
             it.dead = true;
         }
     }
     if (it.dead) it.count = 0;
-    if ((threadIdx.x & 31) == 0) *to = it;
+    if (lane == 0) *to = it;
     __syncwarp();
 }
 
@@ -286,16 +332,17 @@ __device__ __forceinline__ void publish_map(ulonglong2* p, float4 m) {
     asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word(m.x, m.z)), "l"(word(m.y, m.w)) : "memory");
 }
 
-// The state entering item j for this lane's two channels: the nearest published state among up to
+// The state entering the block with words w for this lane's two channels: the nearest published state among up to
 // kWindow predecessors that only published maps lie after, with those maps folded in order.  The
 // window's words are read together.  A wait over a second gives up (status).
 constexpr int kWindow = 32, kBatch = 4;
-__device__ __forceinline__ float2 look_back(const Args& a, int64_t j, int32_t order) {
+template <bool kBackward>
+__device__ __forceinline__ float2 look_back(const Args& a, int64_t w, int32_t order) {
     const int lane = threadIdx.x & 31;
     const int n = min(order, kWindow);
-    const int64_t stride = static_cast<int64_t>(a.tiles) * 32;
-    const uint2* states = a.states + (j - a.tiles) * 32 + lane;      // the predecessor's, and back from it
-    const ulonglong2* maps = a.maps + (j - a.tiles) * 32 + lane;
+    const int64_t stride = (kBackward ? -32 : 32) * static_cast<int64_t>(a.tiles);
+    const uint2* states = a.states + w * 32 + lane - stride;  // the predecessor's, and back from it
+    const ulonglong2* maps = a.maps + w * 32 + lane - stride;
     uint64_t t0 = 0;
     float2 h = make_float2(0.f, 0.f);
     int k = 0, found = -1;  // the nearest k predecessors have published maps, but no state when last looked at
@@ -347,22 +394,35 @@ __device__ __forceinline__ float2 look_back(const Args& a, int64_t j, int32_t or
     return h;
 }
 
-// One warp: publishes the item's map, finds the entering state (`in` where the chain begins), publishes
-// the leaving one.
-__device__ __forceinline__ void chain(const Args& a, int64_t j, const Item& it, float4 map, float2& in, float2& out) {
+__device__ __forceinline__ int64_t words_of(const Args& a, const Item& it) {
+    return static_cast<int64_t>(it.slot) * a.tiles + it.tile;
+}
+// The predecessor's state if it is there already (unset words otherwise, and where there is none).
+template <bool kBackward>
+__device__ __forceinline__ uint2 peek(const Args& a, const Item& it) {
+    if (it.dead || it.order == 0) return make_uint2(kUnset, kUnset);
+    return load_state(a.states + (words_of(a, it) + (kBackward ? a.tiles : -a.tiles)) * 32 + (threadIdx.x & 31));
+}
+
+// One warp: finds the entering state (`in` where the chain begins; what `peek` saw; or by looking back, for which the
+// item's map is published first) and publishes the leaving one.  Nobody waits for a dead item.
+template <bool kBackward>
+__device__ __forceinline__ void chain(const Args& a, const Item& it, float4 map, uint2 seen, float2& in, float2& out) {
     const int lane = threadIdx.x & 31;
-    if (it.dead) {
-        if (a.states) publish_state(a.states + j * 32 + lane, make_float2(0.f, 0.f));
-        return;
-    }
+    if (it.dead) return;
+    const int64_t w = words_of(a, it);
     map.x = settled(map.x);
     map.y = settled(map.y);
     if (it.order > 0) {
-        if (!it.last) publish_map(a.maps + j * 32 + lane, map);
-        in = look_back(a, j, it.order);
+        if (__all_sync(0xffffffffu, seen.x != kUnset && seen.y != kUnset)) {
+            in = make_float2(__uint_as_float(seen.x), __uint_as_float(seen.y));
+        } else {
+            if (!it.last) publish_map(a.maps + w * 32 + lane, map);
+            in = look_back<kBackward>(a, w, it.order);
+        }
     }
     out = make_float2(fmaf(map.x, in.x, map.z), fmaf(map.y, in.y, map.w));
-    if (a.states && !it.last) publish_state(a.states + j * 32 + lane, out);
+    if (a.states && !it.last) publish_state(a.states + w * 32 + lane, out);
 }
 
 __device__ __forceinline__ void check_boundaries(const Args& a) {

@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(32 * kWarps, (ctas<X, G>())) glr_bwd_kernel(co
         const int rows = min(it.count - w * kWarpRows, kWarpRows);
         const int n = rows - half * kSpan;
         float2 in = make_float2(0.f, 0.f);
+        uint2 seen = make_uint2(kUnset, kUnset);
+        if (w == 0 && a.N > 1) seen = peek<true>(a, it);
         if (w == 0 && it.order == 0 && !it.dead && a.dfin)
             load2_any(a.dfin, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
         if (w == 1 && it.count > 0) load2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(32 * kWarps, (ctas<X, G>())) glr_bwd_kernel(co
                 map.y *= qa.y;
             }
             float2 out;
-            chain(a, j, it, map, in, out);
+            chain<true>(a, it, map, seen, in, out);
             *reinterpret_cast<float2*>(&sh.in[2 * lane]) = in;
             if (it.last && !it.dead && a.ds0)
                 store2_any(a.ds0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, out.x, out.y);

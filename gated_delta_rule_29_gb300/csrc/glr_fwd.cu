@@ -5,17 +5,17 @@ namespace la {
 namespace glr {
 namespace {
 
-// Warps of a CTA and CTAs of an SM (as many as the staged rows leave room for).  With 16-bit operands the
-// arithmetic is what fills the time: longer spans leave less of it between them.  With fp32 gates the bytes do,
-// and shorter spans give more warps to wait for them (fwd of 8 x 8192 x 4096, bf16 gates: 304 us with 4 warps, 339
-// with 8; three sequences of 4096 x 2048 in fp32: 36 and 26 us).
+// Warps of a CTA and CTAs of an SM (as many as the staged rows leave room for).  With 16-bit inputs longer spans leave
+// less arithmetic between them (8 x 8192 x 4096, fp32 decays: 335 us with 4 warps, 348 with 8; bf16 gates 304 and
+// 339); fp32 rows leave room for three CTAs only, which need the warps (three sequences of 4096 x 2048: 36 and 26 us).
+// The unrolling is short because the code is long: 8 tokens at a time cost one long sequence 9 % in instruction misses.
 template <typename X, typename G>
-constexpr int warps() { return sizeof(X) + sizeof(G) == 4 ? 4 : 8; }
+constexpr int warps() { return sizeof(X) + sizeof(G) <= 6 ? 4 : 8; }
 template <typename X, typename G>
 constexpr int ctas() { return sizeof(X) + sizeof(G) == 4 ? 6 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
 
-// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 350 us, 6.1 TB/s (92 % of the measured copy rate), bound by
-// its bytes; with bf16 logits of a complement gate 300 us, 5.4 TB/s, where the gate evaluated twice (16 of 28
+// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 335 us, 6.4 TB/s (96 % of the measured copy rate), bound by
+// its bytes; with bf16 logits of a complement gate 285 us, 5.6 TB/s, where the gate evaluated twice (16 of 28
 // instructions an element) takes over half of the issue slots.  One sequence of 131072 x 1000: 195 us, 4.0 TB/s:
 // every block waits for the slowest of the 57 blocks of its channels that are in flight before it.
 template <typename X, typename G, int kMode, bool kCompl>
@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_ke
         const int rows = min(it.count - w * kWarpRows, kWarpRows);  // of the warp
         const int n = rows - half * kSpan;                          // of the thread (may exceed kSpan)
         float2 in = make_float2(0.f, 0.f);
+        uint2 seen = make_uint2(kUnset, kUnset);
+        if (w == 0 && a.N > 1) seen = peek<false>(a, it);
         if (w == 0 && it.order == 0 && !it.dead && a.s0)
             load2_any(a.s0, it.state * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, a.s0_bf16, in.x, in.y);
         __syncwarp();
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_ke
         // the map of the thread's span
         Four ca = four(1.f), cu = four(0.f);
         with_span<kSpan>(n, [&](auto whole) {
-#pragma unroll 8
+#pragma unroll (decltype(whole)::value ? 4 : 1)
             for (int k = 0; k < kSpan; ++k)
                 if (whole || k < n) {
                     const Four x = get4(sx + k * kChannels), g = get4(sg + k * kChannels);
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_ke
                 map.y *= qa.y;
             }
             float2 out;
-            chain(a, j, it, map, in, out);
+            chain<false>(a, it, map, seen, in, out);
             *reinterpret_cast<float2*>(&sh.in[2 * lane]) = in;
             if (!it.dead) {
                 if (a.ckpt && it.count > 0) store2_any(a.ckpt, it.slot * static_cast<int64_t>(a.D), it.d + 2 * lane, a.D, 0, in.x, in.y);
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_ke
         if (a.h && rows > 0) {
             Four h = fma4(pa, get4(&sh.in[c4]), pu);
             with_span<kSpan>(n, [&](auto whole) {
-#pragma unroll 8
+#pragma unroll (decltype(whole)::value ? 4 : 1)
                 for (int k = 0; k < kSpan; ++k)
                     if (whole || k < n) {
                         const Four x = get4(sx + k * kChannels), g = get4(sg + k * kChannels);

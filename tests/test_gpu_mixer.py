@@ -133,3 +133,37 @@ def test_repeated_calls_give_the_same_bits():
         got = (h, fin) + la.glr_bwd(x, g, cu, dh, checkpoints=ck)
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("N", [2, 7, 31, 32])
+@pytest.mark.parametrize("D", [64, 200])
+def test_sequences_side_by_side(N, D):
+    """Up to 32 sequences are taken block by block in turn, single ones block after block: the same bits, for sequences of
+    no, one and many blocks, forwards and backwards, and through pool slots."""
+    rng = np.random.default_rng(N + D)
+    lens = [int(v) for v in rng.integers(0, 1500, N)]
+    lens[0], lens[-1] = 4000, 128
+    if N > 5:
+        lens[2], lens[3], lens[4] = 0, 1, 129
+    T, gen = sum(lens), torch.Generator().manual_seed(N)
+    x, dh = (torch.randn(T, D, generator=gen).to(BF).to(dev()) for _ in range(2))
+    g = (-0.1 * torch.rand(T, D, generator=gen)).to(dev())
+    s0, dfin = (torch.randn(N, D, generator=gen).to(dev()) for _ in range(2))
+    cu = cu_of(lens)
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    h, fin, ck = la.glr_fwd(x, g, cu, initial_state=s0, output_checkpoints=True, status=status)
+    dx, dg, ds0 = la.glr_bwd(x, g, cu, dh, initial_state=s0, d_final_state=dfin, checkpoints=ck, status=status)
+    pool = torch.zeros(N + 2, D, device=dev())
+    slots = torch.randperm(N + 2, generator=gen)[:N].to(torch.int32).to(dev())
+    pool[slots.long()] = s0
+    hp, _, _ = la.glr_fwd(x, g, cu, initial_state=pool, state_indices=slots, status=status)
+    assert la.read_status(status) == 0
+    assert torch.equal(hp, h) and torch.equal(pool[slots.long()], fin)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    for i in range(N):
+        a, b, one = starts[i], starts[i + 1], cu_of([lens[i]])
+        h1, fin1, ck1 = la.glr_fwd(x[a:b], g[a:b], one, initial_state=s0[i:i + 1], output_checkpoints=True)
+        dx1, dg1, ds1 = la.glr_bwd(x[a:b], g[a:b], one, dh[a:b], initial_state=s0[i:i + 1],
+                                   d_final_state=dfin[i:i + 1], checkpoints=ck1)
+        for whole, alone in ((h[a:b], h1), (fin[i:i + 1], fin1), (dx[a:b], dx1), (dg[a:b], dg1), (ds0[i:i + 1], ds1)):
+            assert torch.equal(whole, alone), i
