@@ -57,7 +57,7 @@ struct Launch {
     template <typename X, int kVec, int NV, bool kBlock>
     static la_status run(const Args& a, cudaStream_t s) {
         const int groups = kThreads / a.lanes;
-        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 8);
+        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 4);
         if (a.per_head) grid = (grid + a.H - 1) / a.H * a.H;
         else grid = std::max<int64_t>(grid, (a.H + groups - 1) / groups);
         gn_fwd_kernel<X, kVec, NV, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
