@@ -5,9 +5,9 @@ namespace la {
 namespace gn {
 namespace {
 
-// Bound by its bytes where there are many (5 rows with a gate): 65536 x 32 x 128 bf16 in 428 us, 6.3 TB/s (94 % of
+// Bound by its bytes where there are many (5 rows with a gate): 65536 x 32 x 128 bf16 in 423 us, 6.3 TB/s (95 % of
 // the measured copy rate); the paired arithmetic took it there from 479.  Small batches are bound by the rounds of a
-// group, each a load, two to four reductions over its lanes and a store: 4099 x 10 x 100, 27 us of a 5 us floor.
+// group, each a load, two to four reductions over its lanes and a store: 4099 x 10 x 100, 17 us of a 4 us floor.
 template <typename X, int kVec, int NV, bool kBlock, bool kBias>
 __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X) == 4 || kVec < 4 ? 2 : 3)) gn_bwd_kernel(const Args a) {
     extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X
     }
 }
 
-// 912 rows of 128 in 9 us: two round trips' latency and a launch, not bytes.
+// 912 rows of 128 in 7.5 us: a launch and two round trips, not bytes.
 // out[c] = the sum over the CTAs' partial sums of column c: rows c / V, + heads, + 2 heads, ... (per
 // head), or all rows (shared).  A CTA takes 32 columns; its 32 warps take every 32nd row, in order.
 __global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const float* pb, int64_t rows, int V, int heads,
@@ -113,8 +113,7 @@ __global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const flo
     float s = 0.f;
     if (c < static_cast<int64_t>(V) * heads) {
         const int64_t step = 32ll * heads;
-#pragma unroll 16
-        for (int64_t u = c / V + static_cast<int64_t>(w) * heads; u < rows; u += step) s += p[u * V + c % V];
+        s = strided_sum<16>(p + c % V, V, c / V + static_cast<int64_t>(w) * heads, rows, step);
     }
     part[w][lane] = s;
     __syncthreads();

@@ -148,6 +148,20 @@ __device__ __forceinline__ float2 act_grad2(float2 p, float2& d) {
     return mul2(p, s);
 }
 
+// p[first pitch] + p[(first + step) pitch] + ... below row `rows`, in order, kGroup loads at a time.
+template <int kGroup>
+__device__ __forceinline__ float strided_sum(const float* p, int64_t pitch, int64_t first, int64_t rows, int64_t step) {
+    float s = 0.f;
+    for (int64_t r = first; r < rows; r += kGroup * step) {
+        float v[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) v[i] = r + i * step < rows ? p[(r + i * step) * pitch] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) s += v[i];
+    }
+    return s;
+}
+
 // ---------------------------------------------------------------- sequence blocks
 // The packed batch is cut into blocks of `B` tokens that start at each sequence's own first
 // token, so that what a block computes does not depend on the batch around its sequence.  Block

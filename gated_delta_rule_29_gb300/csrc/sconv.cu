@@ -396,10 +396,7 @@ __global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int6
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.y;
     const int d = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (d < D) {
-#pragma unroll 16
-        for (int64_t k = warp; k < columns; k += 32) s += part[(k * (W + 1) + j) * D + d];
-    }
+    if (d < D) s = strided_sum<2>(part + static_cast<int64_t>(j) * D + d, static_cast<int64_t>(W + 1) * D, warp, columns, 32);
     sh[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && d < D) {
