@@ -21,8 +21,8 @@
 // after it in order.  The state leaving a block is always fma(A, entering, B), whoever computes it, so
 // the bits do not depend on what was published when.  The launch is cooperative (all CTAs resident),
 // every CTA walks its items in ascending order and items only wait for lower ones, so the lowest
-// unfinished item never waits and the waits end; they are bounded all the same.  Each operand is read
-// once and each result written once.
+// unfinished item never waits and the waits end; they are bounded all the same (LA_ERR_TIMEOUT).  Each
+// operand is read once and each result written once.
 //
 // The backward runs the same chain from each sequence's end, over the gradient leaving a token,
 // c_t = a_t (dh_t + c_{t+1}); the states entering its blocks come from the forward's checkpoints (one
@@ -241,6 +241,7 @@ __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
     const int32_t s = static_cast<int32_t>(j / a.tiles);
     it.tile = static_cast<int32_t>(j - static_cast<int64_t>(s) * a.tiles);
     it.d = it.tile * kChannels;
+    it.slot = it.count = 0;
     int32_t seq = -1, start = 0, len = 0, c = 0;
     if (a.N > 1 && a.N <= 32) {
         // lane i holds sequence i; the blocks of rounds before round r are sum_i min(blocks_i, r)

@@ -14,8 +14,8 @@ constexpr int warps() { return sizeof(X) + sizeof(G) <= 6 ? 4 : 8; }
 template <typename X, typename G>
 constexpr int ctas() { return sizeof(X) + sizeof(G) == 4 ? 6 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
 
-// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 335 us, 6.4 TB/s (96 % of the measured copy rate), bound by
-// its bytes; with bf16 logits of a complement gate 285 us, 5.6 TB/s, where the gate evaluated twice (16 of 28
+// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 342 us, 6.3 TB/s (94 % of the measured copy rate), bound by
+// its bytes; with bf16 logits of a complement gate 301 us, 5.4 TB/s, where the gate evaluated twice (16 of 28
 // instructions an element) takes over half of the issue slots.  One sequence of 131072 x 1000: 195 us, 4.0 TB/s:
 // every block waits for the slowest of the 57 blocks of its channels that are in flight before it.
 template <typename X, typename G, int kMode, bool kCompl>
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_ke
     fence_mbar_init();
     check_boundaries(a);
 
-    // The warp's rows of an item on their way into shared memory; false when it has none.
+    // The warp's rows of an item on their way into shared memory.
     auto fetch = [&](const Item& it) {
         const int n = min(it.count - w * kWarpRows, kWarpRows), token = it.start + w * kWarpRows;
         if (n <= 0) return;
