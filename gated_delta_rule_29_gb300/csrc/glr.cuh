@@ -243,6 +243,7 @@ __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
     it.d = it.tile * kChannels;
     it.slot = it.count = 0;
     int32_t seq = -1, start = 0, len = 0, c = 0;
+    bool chained = true;  // the neighbour holds the block that this one follows (invalid boundaries may leave it none)
     if (a.N > 1 && a.N <= 32) {
         // lane i holds sequence i; the blocks of rounds before round r are sum_i min(blocks_i, r)
         int64_t s0 = 0, s1 = -1;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
         }
     } else {
         it.slot = kBackward ? static_cast<int32_t>(a.T / kBlock) + a.N - 1 - s : s;
-        const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, it.slot);
+        const SeqBlock b = find_block<kBlock>(a.cu, a.cu64, a.N, a.T, it.slot, it.slot + (kBackward ? 1 : -1), chained);
         seq = b.seq;
         start = b.start;
         len = b.len;
@@ -287,9 +288,9 @@ __device__ __forceinline__ void locate(const Args& a, int64_t j, Item* to) {
     }
     it.start = start;
     it.dead = seq < 0;
-    const int32_t blocks = max(1, (len + kBlock - 1) / kBlock);
-    it.order = kBackward ? blocks - 1 - c : c;
-    it.last = it.order == blocks - 1;
+    const ChainPlace place = chain_place<kBlock, kBackward>(c, len, chained);
+    it.order = place.order;
+    it.last = place.last;
     it.state = seq;
     if (!kBackward && a.idx && !it.dead) {
         it.state = a.idx[seq];

@@ -10,6 +10,7 @@
 
 #include "../../include/liblinattn.h"
 #include "ptx.cuh"
+#include "seq_search.h"
 
 namespace la {
 namespace mixer {
@@ -163,20 +164,6 @@ __device__ __forceinline__ float strided_sum(const float* p, int64_t pitch, int6
 }
 
 // ---------------------------------------------------------------- sequence blocks
-// The packed batch is cut into blocks of `B` tokens that start at each sequence's own first
-// token, so that what a block computes does not depend on the batch around its sequence.  Block
-// c of sequence i is slot cu[i] / B + i + c: these numbers are all different (a sequence of L
-// tokens from cu[i] on needs at most floor((cu[i] + L) / B) - floor(cu[i] / B) + 1 of them), there
-// are T / B + N slots, each sequence has at least one (an empty one too), and no table is needed.
-struct SeqBlock {
-    int32_t seq;    // -1: the slot holds no block
-    int32_t start;  // first token of the block
-    int32_t count;  // tokens in the block (0 only for the block of an empty sequence)
-    int32_t c;      // block number within the sequence
-    int32_t len;    // tokens in the sequence
-    int32_t first;  // first token of the sequence
-};
-
 __device__ __forceinline__ int64_t cu_load(const void* cu, int cu64, int64_t i) {
     return cu64 ? static_cast<const int64_t*>(cu)[i] : static_cast<int64_t>(static_cast<const int32_t*>(cu)[i]);
 }
@@ -187,35 +174,27 @@ __device__ __forceinline__ void raise_status(int32_t* status, int32_t code) {
 
 // The block in `slot`; called by whole warps.  32-ary search over cu[i] / B + i, one round of loads
 // for up to 32 sequences, two for up to 1024.  With invalid cu_seqlens the answer is some block
-// inside [0, T), so that no access leaves the operands.
+// inside [0, T), so that no access leaves the operands, and `same` says whether the same search for the
+// slot `beside` ends at the same sequence (as it does where boundaries are valid and the sequence has a
+// block there).
+template <int B>
+__device__ __forceinline__ SeqBlock find_block(const void* cu, int cu64, int32_t N, int64_t T, int64_t slot, int64_t beside, bool& same) {
+    const int lane = threadIdx.x & 31;
+    SlotSearch f = {0, N, true};
+    while (f.n > 1) {
+        const int32_t i = f.lo + lane * f.step();
+        const bool live = lane * f.step() < f.n;
+        const int64_t v = live ? cu_load(cu, cu64, i) / B + i : 0;
+        const unsigned here = __ballot_sync(0xffffffffu, live && v <= slot);
+        f.narrow(here, beside == slot ? here : __ballot_sync(0xffffffffu, live && v <= beside));
+    }
+    same = f.same;
+    return block_of<B>(f.lo, cu_load(cu, cu64, f.lo), cu_load(cu, cu64, f.lo + 1), T, slot);
+}
 template <int B>
 __device__ __forceinline__ SeqBlock find_block(const void* cu, int cu64, int32_t N, int64_t T, int64_t slot) {
-    const int lane = threadIdx.x & 31;
-    int32_t lo = 0, n = N;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int32_t step = (n + 31) / 32;
-        const int32_t i = lo + lane * step;
-        const bool at_or_before = lane * step < n && cu_load(cu, cu64, i) / B + i <= slot;
-        const unsigned m = __ballot_sync(0xffffffffu, at_or_before);
-        const int k = m ? 31 - __clz(m) : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    SeqBlock b;
-    b.seq = -1;
-    b.start = b.c = b.len = b.first = 0;
-    b.count = 0;
-    const int64_t s0 = cu_load(cu, cu64, lo), s1 = cu_load(cu, cu64, lo + 1);
-    if (s0 < 0 || s1 < s0 || s1 > T) return b;
-    const int64_t c = slot - (s0 / B + lo);
-    if (c < 0 || (c > 0 && c * B >= s1 - s0)) return b;
-    b.seq = lo;
-    b.c = static_cast<int32_t>(c);
-    b.first = static_cast<int32_t>(s0);
-    b.len = static_cast<int32_t>(s1 - s0);
-    b.start = static_cast<int32_t>(s0 + c * B);
-    b.count = min(B, b.first + b.len - b.start);
-    return b;
+    bool same;
+    return find_block<B>(cu, cu64, N, T, slot, slot, same);
 }
 
 // Checks entry i of cu_seqlens (0 <= i < N, with its right neighbour and the two ends).
