@@ -115,13 +115,17 @@ def _status(p, status: torch.Tensor, like: torch.Tensor) -> None:
 
 
 def _on_stream(fn):
-    """Makes a wrapper's `stream` argument the current stream while it runs, so that what it allocates belongs to
-    that stream."""
+    """Makes a wrapper's `stream` argument, which must be on the device of its first operand, the current stream while
+    it runs, so that what it allocates belongs to that stream."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        if kwargs.get("stream") is None:
+        stream = kwargs.get("stream")
+        if stream is None:
             return fn(*args, **kwargs)
-        with torch.cuda.stream(kwargs["stream"]):
+        x = args[0] if args else kwargs.get("x")
+        if isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
+            raise ValueError(f"stream must be on {x.device}, got one on {stream.device}")
+        with torch.cuda.stream(stream):
             return fn(*args, **kwargs)
     return call
 
@@ -130,11 +134,16 @@ _functions = {}
 
 
 def _call(name: str, p, like: torch.Tensor) -> None:
-    """One library call on the current stream of the operands' device."""
+    """One library call on the operands' device, which the library takes from the thread, and its current stream."""
     fn = _functions.get(name)
     if fn is None:
         fn = _functions[name] = getattr(B.load(), name)
-    code = fn(ctypes.byref(p), _raw_stream(like.get_device()))
+    device = like.get_device()
+    if device == _current_device():
+        code = fn(ctypes.byref(p), _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = fn(ctypes.byref(p), _raw_stream(device))
     if code:
         B.check(code, name)
 
@@ -144,6 +153,7 @@ def _raw_stream(device: int) -> int:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)  # the same without a Python Stream object
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 # ------------------------------------------------------------------ gated linear recurrence

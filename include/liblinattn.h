@@ -581,6 +581,8 @@ size_t la_gdn_fwd_split_workspace_bytes(int64_t T, int32_t N, int32_t HV);
  *     (a size of 0 needs none).  Its contents need no initialisation.
  *   - The status word is written only when something is wrong; the caller
  *     zeroes it.
+ *   - A call runs on the thread's current device, which must be the operands'
+ *     and the stream's (the Python wrappers make it current).
  * Sums, states and statistics are fp32; every output is rounded once.
  * ======================================================================== */
 
