@@ -126,7 +126,7 @@ __device__ __forceinline__ float act_fwd(int kind, float p) {
     const float s = sigmoidf(p);
     return kind == LA_ACT_SIGMOID ? s : p * s;
 }
-// The same for two values at once, and act' beside it: silu' = s (1 + p (1 - s)), sigmoid' = s (1 - s).
+// The same for two values at once, and act' beside it, s being the sigmoid: silu' = s (1 + p (1 - s)), sigmoid' = s (1 - s).
 template <int kAct>
 __device__ __forceinline__ float2 act_fwd2(float2 p) {
     if (kAct == LA_ACT_NONE) return p;
@@ -140,11 +140,17 @@ __device__ __forceinline__ float2 act_grad2(float2 p, float2& d) {
         d = both(1.f);
         return p;
     }
-    const float2 s = act_fwd2<LA_ACT_SIGMOID>(p), rest = fma2(s, both(-1.f), both(1.f));
     if (kAct == LA_ACT_SIGMOID) {
-        d = mul2(s, rest);
+        // 1 - s is e^-p s: a difference would lose its bits as s nears 1, and the derivative with them.  Beyond 2^126,
+        // where s is 0, e^-p is held finite, so that the derivative is 0.
+        const float2 t = mul2(p, both(-kLog2e)), e = make_float2(ex2(t.x), ex2(t.y)), q = add2(e, both(1.f));
+        const float2 s = make_float2(rcp_fast(q.x), rcp_fast(q.y));
+        d = mul2(s, mul2(make_float2(fminf(e.x, 0x1p126f), fminf(e.y, 0x1p126f)), s));
         return s;
     }
+    // here the difference, off by 2^-23 at most, stands beside 1: an error of |p| 2^-23, no more than the exponential's
+    // (49344 x 2048 backward through the convolution 133 us; 141 with the product)
+    const float2 s = act_fwd2<LA_ACT_SIGMOID>(p), rest = fma2(s, both(-1.f), both(1.f));
     d = mul2(s, fma2(p, rest, both(1.f)));
     return mul2(p, s);
 }
