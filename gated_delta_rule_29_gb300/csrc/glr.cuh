@@ -77,8 +77,8 @@ __device__ __forceinline__ void exp_both(float2 l, float2& e, float2& rest) {
     e = make_float2(s0 ? p.x : e.x, s1 ? p.y : e.y);
 }
 
-// a, m and dl/dg of two gate values.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g), held below 2^115 so
-// that the product stays finite (s(g) is then 2^-115 instead of less; NaN stays NaN): no cancellation, no branch.
+// a, m and dl/dg of two gate values.  s(g) = 1 / (1 + e) and 1 - s(g) = e s(g) with e = exp(-g): no cancellation.  From
+// e = 2^64 on 1 - s(g) is 1 in 32 bits, and s(g) goes on to 0 while e goes on to infinity (NaN stays NaN).
 struct Gated {
     float2 a, m, slope;
 };
@@ -88,11 +88,9 @@ __device__ __forceinline__ Gated gate(float lb, float2 g) {
     float2 l = g;
     r.slope = both(1.f);
     if (kMode != LA_GATE_LOG) {
-        float2 e = mul2(g, both(-kLog2e));
-        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e.x));  // 115
-        asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(e.y));
-        e = make_float2(ex2(e.x), ex2(e.y));
-        const float2 q = add2(e, both(1.f)), s = make_float2(rcp_fast(q.x), rcp_fast(q.y)), rest = mul2(e, s);
+        const float2 t = mul2(g, both(-kLog2e)), e = make_float2(ex2(t.x), ex2(t.y));
+        const float2 q = add2(e, both(1.f)), s = make_float2(rcp_fast(q.x), rcp_fast(q.y)), es = mul2(e, s);
+        const float2 rest = make_float2(t.x > 64.f ? 1.f : es.x, t.y > 64.f ? 1.f : es.y);
         if (kMode == LA_GATE_LOGSIGMOID) {
             r.a = s;
             r.slope = rest;

@@ -10,6 +10,7 @@ import torch
 
 import gated_delta_rule_29_gb300 as la
 import mixer_reference as R
+import test_gpu_glr as glr
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,17 @@ def test_convolution_gradient_far_from_zero(act, W):
     p = xs * ws[:, -1] + bs
     size = np.abs(xs * ws[:, -1]) + np.abs(bs)
     R.within("dx", dx, ref, F32, (W + 1) * size + act_units(p) + 2, np.abs(ds * ws[:, -1]) * R.act(act, p)[1])
+
+
+@pytest.mark.parametrize("gt", [BF, F32])
+@pytest.mark.parametrize("gate,complement", [("logsigmoid", False), ("logsigmoid", True), ("bound", False)])
+def test_closed_gates(gt, gate, complement):
+    """Logits from where the sigmoid is small to the type's lowest value and minus infinity: a closed gate leaves nothing
+    of the state before it (h is 0 where no input follows), and the gradients through it are the formula's."""
+    logits = [-20.0, -50.0, -80.0, -86.0, -100.0, -1e4, torch.finfo(gt).min, float("-inf")]
+    lens, D = [40, 300], 8 * len(logits)
+    t = glr.draw(lens, D, F32, gt, "logsigmoid", seed=31)
+    for at in (20, 150, 330):
+        t["g"][at] = torch.tensor(logits).repeat_interleave(8).to(gt)
+        t["x"][at:at + 5] = 0.0
+    glr.check(t, lens, gate, complement)
