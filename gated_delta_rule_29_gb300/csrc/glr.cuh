@@ -47,14 +47,17 @@ constexpr uint64_t kWaitNs = 1000000000ull;      // a bounded wait gives up afte
 template <int kWarps>
 constexpr int span() { return kBlock / kWarps / 2; }
 
-// e^l and, for the complement, 1 - e^l, of two values.  kNear: l itself is the input, so that decays near 1 may be
-// the same for many tokens, and an error in them adds up over some 1 / |l| tokens; ex2's is not evenly spread there,
-// and below 1/16 the Taylor series to l^4 (off by 8e-9) takes its place (the bounded gate's l differ from token to
-// token: their errors average out, and the series costs a seventh of its forward's time).  With the complement the
-// series goes to l^7 and 1/2 (2e-7 of 1 - e^l there), as the difference would cancel.
+// e^l and, for the complement, 1 - e^l, of two values.  An error in a decay near 1 adds up over some 1 / |l| tokens, by
+// its mean where decays vary and whole where they stay the same.  ex2.approx is 0.3 units of 2^-24 low on average just
+// below 1 (65536 logits), which its argument makes up for: means are then within 0.2 units, single values within 1.7 for
+// |l| below 1/8, as good as a 32-bit exp's.  kNear: l itself is the input, and below 1/16 the Taylor series to l^4 (off by
+// 8e-9) takes ex2's place, which leaves the rounding alone (0.5 units).  The bounded gate goes without: its l has
+// roundings of its own, and the series takes 7 % of its dense forward's time and 12 % of its backward's.  With the
+// complement the series goes to l^7 and 1/2 (2e-7 of 1 - e^l there), as the difference would cancel.
+constexpr float kEx2Low = 0.3f * 0x1p-24f * kLog2e;
 template <bool kComplement, bool kNear>
 __device__ __forceinline__ void exp_both(float2 l, float2& e, float2& rest) {
-    const float2 t = mul2(l, both(kLog2e));
+    const float2 t = fma2(l, both(kLog2e), both(kEx2Low));
     e = make_float2(ex2(t.x), ex2(t.y));
     rest = both(1.f);
     if (!kComplement && !kNear) return;

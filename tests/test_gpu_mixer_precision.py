@@ -99,3 +99,37 @@ def test_closed_gates(gt, gate, complement):
         t["g"][at] = torch.tensor(logits).repeat_interleave(8).to(gt)
         t["x"][at:at + 5] = 0.0
     glr.check(t, lens, gate, complement)
+
+
+@pytest.mark.parametrize("bound", [-0.5, -5.0])
+def test_slow_bounded_gates(bound):
+    """Decays a = exp(bound s(g)) just below 1, one token against a state of ones: their errors add up over 1 / |log a|
+    tokens, by their mean where gates vary.  A value is off by at most 4 units of 2^-24 (ex2.approx 3, the rest at
+    most |log a| of its own units and the rounding of the argument), and the mean of many by 1/4 (a rounding to nearest
+    has none)."""
+    g = torch.linspace(-11, 8, 1 << 18, device=dev())
+    a = la.glr_decode(torch.zeros(1, g.numel(), device=dev()), g[None].contiguous(),
+                      state := torch.ones(1, g.numel(), device=dev()), gate_lower_bound=bound)
+    assert torch.equal(a, state) and bool((a <= 1).all())
+    log_a = bound * R.sigmoid(R.f64(g))
+    off = (R.f64(a)[0] / np.exp(log_a) - 1) * 2.0 ** 24
+    for lo, hi in ((1e-5, 1e-4), (1e-4, 1e-3), (1e-3, 1e-2), (1e-2, 1 / 16), (1 / 16, 1 / 8), (1 / 8, 1 / 4), (1 / 4, 1 / 2)):
+        at = (-log_a >= lo) & (-log_a < hi)
+        assert at.sum() > 2000 and np.abs(off[at]).max() <= 4 and abs(off[at].mean()) <= 0.25, (lo, off[at].mean())
+
+
+@pytest.mark.parametrize("repeat", [False, True])
+def test_states_of_slow_bounded_gates(repeat):
+    """Final states of 20000 tokens whose gates stay the same, or vary, around decays of 0.99 and 0.999."""
+    T, D = 20000, 64
+    gen = torch.Generator().manual_seed(11)
+    mid = torch.where(torch.arange(D) % 2 == 0, -3.9, -6.2)
+    g = mid + 0.7 * torch.randn(1 if repeat else T, D, generator=gen)
+    g = g.expand(T, D).contiguous().to(dev())
+    x = torch.rand(T, D, generator=gen).to(dev())
+    cu = torch.tensor([0, T], dtype=torch.int32, device=dev())
+    fin = la.glr_fwd(x, g, cu, gate_lower_bound=-0.5)[1]
+    args = (R.f64(x), R.f64(g), [T])
+    ref, scale = R.glr_fwd(*args, lower_bound=-0.5)[1], R.glr_scales(*args, lower_bound=-0.5)[1]
+    # every step within 4 units for its decay, 1 for its sum, and 1 for the joining of spans, warps and blocks
+    R.within("final_state", fin, ref, F32, 6, scale)
