@@ -263,6 +263,20 @@ inline bool good_rows(const void* p, int64_t stride, int64_t rows, int64_t D, in
     if (stride < 0) return false;
     return !out || rows == 1 || stride >= D;
 }
+// Whether the rows of two operands of D channels share memory: for sure where their strides are the same, and where they
+// differ as far as the first rows tell.
+inline bool rows_meet(const void* a, int64_t a_st, const void* b, int64_t b_st, int64_t rows, int64_t D, int32_t dtype) {
+    if (rows == 0) return false;
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)), es = dtype_size(dtype),
+                  row = D * es, st = a_st * es;
+    if (rows == 1 || a_st != b_st || st == 0) return off > -row && off < row;
+    int64_t q = off / st, r = off % st;  // b's first row is r bytes after a's row q
+    if (r < 0) {
+        r += st;
+        --q;
+    }
+    return (r < row && q < rows && q > -rows) || (st - r < row && q + 1 < rows && q + 1 > -rows);
+}
 // An optional contiguous operand.
 inline bool good_optional(const void* p, int32_t dtype) { return !p || aligned_to(p, dtype_size(dtype)); }
 

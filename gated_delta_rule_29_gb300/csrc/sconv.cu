@@ -550,6 +550,7 @@ la_status sconv_fwd(const la_sconv_fwd_params* p, void* stream) {
         return LA_ERR_INVALID_ARG;
     if (p->state_indices && (!aligned_to(p->state_indices, 4) || !p->initial_state || p->final_state || p->state_pool_size <= 0))
         return LA_ERR_INVALID_ARG;
+    if (rows_meet(p->x, p->x_stride_t, p->y, p->y_stride_t, p->T, p->D, p->x_dtype)) return LA_ERR_INVALID_ARG;  // neighbours read x
     Args a = {};
     a.x = p->x; a.x_st = p->x_stride_t; a.w = p->weight; a.b = p->bias; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
     a.cu = p->cu_seqlens; a.cu64 = p->cu_seqlens_bits == 64; a.T = p->T; a.N = p->N; a.D = p->D; a.act = p->activation;
@@ -574,6 +575,9 @@ la_status sconv_bwd(const la_sconv_bwd_params* p, void* stream) {
         return LA_ERR_INVALID_ARG;
     if ((st = check_workspace(p->workspace, p->workspace_bytes, la_sconv_bwd_workspace_bytes(p->T, p->N, p->D, p->W))) != LA_OK)
         return st;
+    if (rows_meet(p->x, p->x_stride_t, p->dx, p->dx_stride_t, p->T, p->D, p->x_dtype) ||
+        rows_meet(p->dy, p->dy_stride_t, p->dx, p->dx_stride_t, p->T, p->D, p->x_dtype))
+        return LA_ERR_INVALID_ARG;  // neighbours read x and dy
     Args a = {};
     a.x = p->x; a.x_st = p->x_stride_t; a.w = p->weight; a.b = p->bias; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
     a.cu = p->cu_seqlens; a.cu64 = p->cu_seqlens_bits == 64; a.T = p->T; a.N = p->N; a.D = p->D; a.act = p->activation;

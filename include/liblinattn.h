@@ -760,7 +760,8 @@ typedef struct la_sconv_fwd_params {
  *
  * tokens before the start being the initial state's rows (zeros without one).  final_state
  * is the last W - 1 inputs (the initial state's rows shifted along for shorter sequences),
- * which with state_indices goes back into the sequence's slot.
+ * which with state_indices goes back into the sequence's slot.  y must not share memory with x, nor sconv_bwd's dx with
+ * x or dy (LA_ERR_INVALID_ARG where their strides are the same or their first rows meet): a token's neighbours read them.
  */
 la_status sconv_fwd(const la_sconv_fwd_params* p, void* stream);
 
