@@ -227,12 +227,24 @@ la_status dispatch(Args& a, cudaStream_t s) {
     return by_row<Launch, X, 1>(a, s);
 }
 
+// Whether the T x H rows of V elements, st and sh elements apart, share no memory.
+inline bool rows_apart(int64_t st, int64_t sh, int64_t T, int64_t H, int64_t V) {
+    if (T == 1 || H == 1) return T * H == 1 || (T == 1 ? sh : st) >= V;
+    const bool by_head = sh <= st;
+    const int64_t a = by_head ? sh : st, na = by_head ? H : T, b = by_head ? st : sh, nb = by_head ? T : H;  // a <= b
+    if (a < V) return false;
+    // row j b lies among the na rows that are a apart, or beyond the last of them
+    for (int64_t j = 1; j < nb && j * b / a < na; ++j) {
+        const int64_t q = j * b / a, r = j * b % a;
+        if (r < V || (a - r < V && q + 1 < na)) return false;
+    }
+    return true;
+}
+
 inline bool good_thd(const void* p, int64_t st, int64_t sh, int64_t T, int H, int V, int32_t dtype, bool out) {
     if (T == 0) return true;
     if (!p || !aligned_to(p, dtype_size(dtype)) || st < 0 || sh < 0) return false;
-    if (!out) return true;
-    if (H > 1 && sh < V) return false;
-    return T == 1 || st >= V;
+    return !out || rows_apart(st, sh, T, H, V);
 }
 
 inline la_status check(int64_t T, int H, int V, int32_t xd, int32_t wd, int32_t act, float eps, const void* w, const void* b) {

@@ -38,6 +38,33 @@ def test_convolution_over_its_inputs(fn, over):
     assert code(fn, **over) == INV
 
 
+# 8 tokens x 2 heads of 64 channels
+ROWS_MEET = [(64, 64), (96, 64), (64, 448), (128, 190), (256, 450), (100, 700), (128, 64 + 2)]
+
+
+@pytest.mark.parametrize("st,sh", ROWS_MEET)
+def test_norm_rows_over_each_other(st, sh):
+    assert code("gn_fwd", y_stride_t=st, y_stride_h=sh) == INV
+    assert code("gn_bwd", dx_stride_t=st, dx_stride_h=sh) == INV
+    z = dict(z=FAKE, z_stride_t=128, z_stride_h=64, dz=FAKE)
+    assert code("gn_bwd", **z, dz_stride_t=st, dz_stride_h=sh) == INV
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("st,sh", [(128, 64), (200, 70), (64, 512), (70, 600), (192, 64), (128, 960), (256, 64 * 3), (128, 192), (256, 448), (64 * 3, 64 * 2)])
+def test_norm_rows_beside_each_other(st, sh):
+    """Results by token or by head, with gaps, and interleaved."""
+    T, H, V = (8, 2, 64) if (st, sh) != (64 * 3, 64 * 2) else (2, 2, 64)
+    gen = torch.Generator().manual_seed(2)
+    x, dy = (torch.randn(T, H, V, generator=gen).to(BF).cuda() for _ in range(2))
+    w = torch.randn(V, generator=gen).cuda()
+    buf = torch.full((T * st + H * sh + V,), 7.0, dtype=BF, device="cuda")
+    out = buf.as_strided((T, H, V), (st, sh, 1))
+    assert torch.equal(la.gn_fwd(x, w, y=out), la.gn_fwd(x, w))
+    assert int((buf != 7).sum()) <= T * H * V
+    assert torch.equal(la.gn_bwd(x, w, dy, dx=out)[0], la.gn_bwd(x, w, dy)[0])
+
+
 @pytest.mark.gpu
 def test_convolution_beside_its_inputs():
     """Interleaved column slices of one buffer, the halves of one buffer, and rows of other strides share no memory."""
