@@ -39,6 +39,7 @@ struct Args {
     float eps;
     void *y, *dz;         // y: the result, or dx in the backward
     float *pw, *pb;       // partial sums [CTAs][V]
+    int64_t ctas;         // of the backward (0 without rows: the sums are then zero)
 };
 
 // Sum over the `lanes` lanes that share a row; kBlock: over the CTA (red has one float per warp).
@@ -176,7 +177,13 @@ __device__ __forceinline__ void with_act(const Args& a, F f) {
     }
 }
 
-// Resident CTAs to compile for: more, with fewer registers each, where a lane holds little.
+// Resident CTAs to compile for: more, with fewer registers each, where a lane holds little.  A launch takes one wave of
+// them: a part of a second one leaves SMs idle, a whole second one starts over for nothing.  Forward, gated 65536 x 32 x
+// 128: bf16 (four an SM) 258 us with 4 x 152 CTAs, 287 with 3, 293 with 6; fp32 a quarter of that (three) 125 with 3,
+// 143 with 4; 16384 x 16 x 512 (two) 211 with 2, 262 with 3.  Backward: bf16 (three) 440 with 3 x 152, 498 with 2, 549 with
+// 4; with a bias (two) 471 with 2, 563 with 3, 479 with 6; 16384 x 16 x 512 (one) 438 with 1, 457 with 6; and the fewer
+// the CTAs, the fewer the partial sums.
+constexpr int kSms = 152;
 constexpr int ctas(int elements, int few, int many) { return elements <= 8 ? many : elements <= 16 ? few : 1; }
 
 // ---------------------------------------------------------------- shapes

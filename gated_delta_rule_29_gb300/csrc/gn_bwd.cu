@@ -5,11 +5,15 @@ namespace la {
 namespace gn {
 namespace {
 
+template <typename X, int kVec, int NV, bool kBias>
+constexpr int resident() { return ctas(NV * kVec, 1, kBias || sizeof(X) == 4 || kVec < 4 ? 2 : 3); }
+constexpr int kMostResident = 3;
+
 // Bound by its bytes where there are many (5 rows with a gate): 65536 x 32 x 128 bf16 in 423 us, 6.3 TB/s (95 % of
 // the measured copy rate); the paired arithmetic took it there from 479.  Small batches are bound by the rounds of a
 // group, each a load, two to four reductions over its lanes and a store: 4099 x 10 x 100, 17 us of a 4 us floor.
 template <typename X, int kVec, int NV, bool kBlock, bool kBias>
-__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 1, kBias || sizeof(X) == 4 || kVec < 4 ? 2 : 3)) gn_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, (resident<X, kVec, NV, kBias>())) gn_bwd_kernel(const Args a) {
     extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
@@ -124,27 +128,23 @@ __global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const flo
     }
 }
 
-// CTAs of the backward: at least kMinRows rows for a group of lanes, and a multiple of the heads where each CTA keeps
-// to one.  The lanes of a row do not depend on its alignment, so the workspace's size follows from the shape.
-constexpr int kSms = 152, kMinRows = 8;
-int64_t bwd_ctas(int64_t T, int H, int V, int per_head) {
+// CTAs of the backward, per_sm an SM at most: at least kMinRows rows for a group of lanes, and a multiple of the heads where
+// each CTA keeps to one.  The lanes of a row do not depend on its alignment, so the most that any form of a shape takes
+// follows from the shape, and with it the workspace's size.
+constexpr int kMinRows = 8;
+int64_t bwd_ctas(int64_t T, int H, int V, int per_head, int per_sm) {
     const int64_t rows = T * H, groups = kThreads / shape(V, 1).lanes;
-    int64_t n = std::max<int64_t>(1, rows / kMinRows / groups);
-    // an SM holds two or three: whole waves of either, or one of two (4099 x 10 x 100, forward and backward: 47.8 us
-    // with 300 CTAs, 49.1 with 320)
-    if (n >= 6 * kSms) n = 6 * kSms;
-    else n = std::min<int64_t>(n, 2 * kSms);
-    if (per_head) n = std::max<int64_t>(H, n / H * H);
-    else n = std::max(n, (H + groups - 1) / groups);
-    return n;
+    const int64_t n = std::min<int64_t>(std::max<int64_t>(1, rows / kMinRows / groups), static_cast<int64_t>(kSms) * per_sm);
+    return per_head ? std::max<int64_t>(H, n / H * H) : std::max(n, (H + groups - 1) / groups);
 }
 
 struct Launch {
     template <typename X, int kVec, int NV, bool kBlock>
-    static la_status run(const Args& a, cudaStream_t s) {
+    static la_status run(Args& a, cudaStream_t s) {
         const int groups = kThreads / a.lanes;
         const size_t smem = static_cast<size_t>(groups) * a.V * sizeof(float);
-        const unsigned grid = static_cast<unsigned>(bwd_ctas(a.T, a.H, a.V, a.per_head));
+        a.ctas = bwd_ctas(a.T, a.H, a.V, a.per_head, a.b ? resident<X, kVec, NV, true>() : resident<X, kVec, NV, false>());
+        const unsigned grid = static_cast<unsigned>(a.ctas);
         if (a.b) gn_bwd_kernel<X, kVec, NV, kBlock, true><<<grid, kThreads, smem, s>>>(a);
         else gn_bwd_kernel<X, kVec, NV, kBlock, false><<<grid, kThreads, smem, s>>>(a);
         return launched();
@@ -163,7 +163,7 @@ extern "C" {
 
 size_t la_gn_bwd_workspace_bytes(int64_t T, int32_t H, int32_t V, int32_t per_head) {
     if (T < 0 || H <= 0 || V <= 0 || V > kMaxV) return 0;
-    return (static_cast<size_t>(bwd_ctas(T, H, V, per_head != 0)) * V * 2 * 4 + 255) & ~size_t(255);
+    return (static_cast<size_t>(bwd_ctas(T, H, V, per_head != 0, kMostResident)) * V * 2 * 4 + 255) & ~size_t(255);
 }
 
 la_status gn_bwd(const la_gn_bwd_params* p, void* stream) {
@@ -191,19 +191,16 @@ la_status gn_bwd(const la_gn_bwd_params* p, void* stream) {
     a.per_head = p->per_head != 0; a.center = p->center != 0; a.act = p->activation; a.eps = p->eps;
     a.y = p->dx; a.y_st = p->dx_stride_t; a.y_sh = p->dx_stride_h;
     a.dz = p->dz; a.dz_st = p->dz_stride_t; a.dz_sh = p->dz_stride_h;
-    int64_t ctas = bwd_ctas(a.T, a.H, a.V, a.per_head);
     a.pw = static_cast<float*>(p->workspace);
-    a.pb = p->bias ? a.pw + ctas * a.V : nullptr;
+    a.pb = p->bias ? a.pw + bwd_ctas(a.T, a.H, a.V, a.per_head, kMostResident) * a.V : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p->T > 0) {
         st = p->x_dtype == LA_DTYPE_BF16 ? dispatch<Launch, bf16>(a, s) : dispatch<Launch, float>(a, s);
         if (st != LA_OK) return st;
-    } else {
-        ctas = 0;  // no rows: the sums are zero
     }
     const int heads = a.per_head ? a.H : 1;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.V) * heads + 31) / 32), a.pb ? 2 : 1);
-    gn_sum_kernel<<<grid, 1024, 0, s>>>(a.pw, a.pb, ctas, a.V, heads, p->d_weight, p->d_bias, a.w_bf16);
+    gn_sum_kernel<<<grid, 1024, 0, s>>>(a.pw, a.pb, a.ctas, a.V, heads, p->d_weight, p->d_bias, a.w_bf16);
     return launched();
 }
 

@@ -5,10 +5,13 @@ namespace la {
 namespace gn {
 namespace {
 
+template <typename X, int kVec, int NV>
+constexpr int resident() { return ctas(NV * kVec, 2, sizeof(X) == 4 || kVec < 4 ? 3 : 4); }
+
 // Bound by its bytes (2 rows, 3 with a gate): 65536 x 32 x 128 bf16, gated, in 258 us, 6.2 TB/s (93 % of the measured
 // copy rate).  A single row a group at a time leaves too little in flight, so short rows are requested one ahead.
 template <typename X, int kVec, int NV, bool kBlock>
-__global__ void __launch_bounds__(kThreads, ctas(NV * kVec, 2, sizeof(X) == 4 || kVec < 4 ? 3 : 4)) gn_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, (resident<X, kVec, NV>())) gn_fwd_kernel(const Args a) {
     __shared__ float red[kThreads / 32];
     const int lane = threadIdx.x % a.lanes;
     const Walk r = walk(a);
@@ -57,7 +60,7 @@ struct Launch {
     template <typename X, int kVec, int NV, bool kBlock>
     static la_status run(const Args& a, cudaStream_t s) {
         const int groups = kThreads / a.lanes;
-        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, 152 * 4);
+        int64_t grid = std::min<int64_t>((a.T * a.H + groups - 1) / groups, kSms * resident<X, kVec, NV>());
         if (a.per_head) grid = (grid + a.H - 1) / a.H * a.H;
         else grid = std::max<int64_t>(grid, (a.H + groups - 1) / groups);
         gn_fwd_kernel<X, kVec, NV, kBlock><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
