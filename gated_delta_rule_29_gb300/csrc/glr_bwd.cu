@@ -6,14 +6,14 @@ namespace glr {
 namespace {
 
 // Warps of a CTA, and CTAs of an SM (as many as the staged rows leave room for).  Short spans: the states before
-// each of its tokens stay in registers, or nearly (8 x 8192 x 4096 bf16: 507 us with 4 CTAs of 64 registers a thread,
-// 536 with 3 of 80).
+// each of its tokens stay in registers, or nearly (8 x 8192 x 4096 bf16: 5 % less time with 4 CTAs of 64 registers a
+// thread than with 3 of 80).
 constexpr int kWarps = 8;
 template <typename X, typename G>
 constexpr int ctas() { return sizeof(X) == 4 ? 2 : sizeof(G) == 4 ? 3 : 4; }
 
-// 8 x 8192 tokens x 4096 channels, bf16 with logits of a complement gate: 490 us, 5.5 TB/s (82 % of the measured copy
-// rate), between its bytes (5 rows) and its issue slots (59 %: the gate evaluated three times).
+// 8 x 8192 tokens x 4096 channels, bf16 with logits of a complement gate: 500 us, 5.4 TB/s (80 % of the measured copy
+// rate), between its bytes (5 rows) and its issue slots (62 %: the gate evaluated three times).
 template <typename X, typename G, int kMode, bool kCompl>
 __global__ void __launch_bounds__(32 * kWarps, (ctas<X, G>())) glr_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
     constexpr int kSpan = span<kWarps>(), kWarpRows = 2 * kSpan;

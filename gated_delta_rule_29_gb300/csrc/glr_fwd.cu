@@ -6,17 +6,17 @@ namespace glr {
 namespace {
 
 // Warps of a CTA and CTAs of an SM (as many as the staged rows leave room for).  With 16-bit inputs longer spans leave
-// less arithmetic between them (8 x 8192 x 4096, fp32 decays: 335 us with 4 warps, 348 with 8; bf16 gates 304 and
-// 339); fp32 rows leave room for three CTAs only, which need the warps (three sequences of 4096 x 2048: 36 and 26 us).
+// less arithmetic between them (8 x 8192 x 4096, fp32 decays: 4 % less time with 4 warps than with 8; bf16 gates 10 %);
+// fp32 rows leave room for three CTAs only, which need the warps (three sequences of 4096 x 2048: 36 and 26 us).
 // The unrolling is short because the code is long: 8 tokens at a time cost one long sequence 9 % in instruction misses.
 template <typename X, typename G>
 constexpr int warps() { return sizeof(X) + sizeof(G) <= 6 ? 4 : 8; }
 template <typename X, typename G>
 constexpr int ctas() { return sizeof(X) + sizeof(G) == 4 ? 6 : sizeof(X) + sizeof(G) == 6 ? 4 : 3; }
 
-// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 342 us, 6.3 TB/s (94 % of the measured copy rate), bound by
-// its bytes; with bf16 logits of a complement gate 301 us, 5.4 TB/s, where the gate evaluated twice (16 of 28
-// instructions an element) takes over half of the issue slots.  One sequence of 131072 x 1000: 195 us, 4.0 TB/s:
+// 8 x 8192 tokens x 4096 channels: bf16 with fp32 decays 340 us, 6.3 TB/s (94 % of the measured copy rate), bound by
+// its bytes; with bf16 logits of a complement gate 298 us, 5.4 TB/s, where the gate evaluated twice (17 of 29
+// instructions an element) takes over half of the issue slots.  One sequence of 131072 x 1000: 198 us, 4.0 TB/s:
 // every block waits for the slowest of the 57 blocks of its channels that are in flight before it.
 template <typename X, typename G, int kMode, bool kCompl>
 __global__ void __launch_bounds__(32 * warps<X, G>(), (ctas<X, G>())) glr_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {

@@ -9,9 +9,9 @@ template <typename X, int kVec, int NV, bool kBias>
 constexpr int resident() { return ctas(NV * kVec, 1, kBias || sizeof(X) == 4 || kVec < 4 ? 2 : 3); }
 constexpr int kMostResident = 3;
 
-// Bound by its bytes where there are many (5 rows with a gate): 65536 x 32 x 128 bf16 in 423 us, 6.3 TB/s (95 % of
-// the measured copy rate); the paired arithmetic took it there from 479.  Small batches are bound by the rounds of a
-// group, each a load, two to four reductions over its lanes and a store: 4099 x 10 x 100, 17 us of a 4 us floor.
+// Bound by its bytes where there are many (5 rows with a gate): 65536 x 32 x 128 bf16 in 430 us, 6.2 TB/s (93 % of
+// the measured copy rate); the paired arithmetic took 50 us off.  Small batches are bound by the rounds of a
+// group, each a load, two to four reductions over its lanes and a store: 4099 x 10 x 100, 16 us of a 4 us floor.
 template <typename X, int kVec, int NV, bool kBlock, bool kBias>
 __global__ void __launch_bounds__(kThreads, (resident<X, kVec, NV, kBias>())) gn_bwd_kernel(const Args a) {
     extern __shared__ float sums[];  // [groups][V]: one weight gradient's sums at a time
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, (resident<X, kVec, NV, kBias>())) gn
     }
 }
 
-// 912 rows of 128 in 7.5 us: a launch and two round trips, not bytes.
+// 456 rows of 128 in 4.6 us: a launch and two round trips, not bytes.
 // out[c] = the sum over the CTAs' partial sums of column c: rows c / V, + heads, + 2 heads, ... (per
 // head), or all rows (shared).  A CTA takes 32 columns; its 32 warps take every 32nd row, in order.
 __global__ void __launch_bounds__(1024) gn_sum_kernel(const float* pw, const float* pb, int64_t rows, int V, int heads,

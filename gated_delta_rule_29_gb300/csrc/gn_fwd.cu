@@ -8,7 +8,7 @@ namespace {
 template <typename X, int kVec, int NV>
 constexpr int resident() { return ctas(NV * kVec, 2, sizeof(X) == 4 || kVec < 4 ? 3 : 4); }
 
-// Bound by its bytes (2 rows, 3 with a gate): 65536 x 32 x 128 bf16, gated, in 258 us, 6.2 TB/s (93 % of the measured
+// Bound by its bytes (2 rows, 3 with a gate): 65536 x 32 x 128 bf16, gated, in 256 us, 6.3 TB/s (94 % of the measured
 // copy rate).  A single row a group at a time leaves too little in flight, so short rows are requested one ahead.
 template <typename X, int kVec, int NV, bool kBlock>
 __global__ void __launch_bounds__(kThreads, (resident<X, kVec, NV>())) gn_fwd_kernel(const Args a) {

@@ -12,9 +12,9 @@
 // backward), each lane two channels with the window in registers.  A CTA keeps to one channel tile: the taps stay in registers, and in the
 // backward (which recomputes p) so do the sums of dw and db over all its blocks, which a second kernel adds
 // over the CTAs in order.  Rows that TMA cannot move go through the same shared memory with plain loads.
-// The forward is bound by its bytes (2 rows): 8 x 8192 x 4096 bf16, W = 4, in 185 us, 5.8 TB/s (87 % of the measured
-// copy rate).  The backward (3 rows, and 20 bytes a channel and CTA of partial sums) takes 125 us for a skewed batch
-// of 49344 x 2048, 4.9 TB/s: its arithmetic (some 20 instructions an element, two of them special functions, a fifth
+// The forward is bound by its bytes (2 rows): 8 x 8192 x 4096 bf16, W = 4, in 184 us, 5.8 TB/s (87 % of the measured
+// copy rate).  The backward (3 rows, and 20 bytes a channel and CTA of partial sums) takes 128 us for a skewed batch
+// of 49344 x 2048, 4.7 TB/s (71 %): its arithmetic (some 20 instructions an element, two of them special functions, a fifth
 // of them repeated at the spans' ends) and the latency of each token's chain share the time with the bytes.
 #include <algorithm>
 #include <type_traits>
@@ -30,7 +30,7 @@ constexpr int kDecodeThreads = 128;
 constexpr int kBlock = 128;  // tokens of a block
 // Warps of a CTA, one span of the block each.  Longer spans repeat less (W - 1 tokens of a span are looked at twice
 // in the backward), more warps hide more: 8 x 8192 x 4096 bf16 forward 184 us with 4 warps, 209 with 8; the skewed
-// batch of 49344 x 2048 backward 160 and 147.
+// batch of 49344 x 2048 backward 8 % less with 8 than with 4.
 template <bool kBackward>
 constexpr int warps() { return kBackward ? 8 : 4; }
 constexpr int kChannels = 64;                          // of a CTA, two a lane
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(1024) sconv_sum_kernel(const float* part, int6
     }
 }
 
-// One token: 512 x 8192 bf16 in 9.5 us from L2, 14 from memory, bound by its bytes (2 W rows) once the taps of a
+// One token: 512 x 8192 bf16 in 9.5 us from L2, 13 from memory, bound by its bytes (2 W rows) once the taps of a
 // thread's channels come in wide loads (19 us one by one).
 template <typename T, int kVec, int W>
 __device__ __forceinline__ void load_run(float (&w)[kVec * W], const void* base, int d) {

@@ -624,6 +624,10 @@ typedef struct la_glr_fwd_params {
  * (rows in between are left alone).
  * Batch invariant: blocks start at each sequence's own first token, and the
  * states combine in a fixed order.
+ * glr_fwd and glr_bwd launch cooperatively, with every CTA that the device holds
+ * at once: beside other work they start when it has left room for all of them,
+ * and they return LA_ERR_CUDA where the process may use fewer SMs than its device
+ * reports.
  */
 la_status glr_fwd(const la_glr_fwd_params* p, void* stream);
 
