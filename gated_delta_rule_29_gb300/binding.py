@@ -30,6 +30,10 @@ LA_GATE_LOGSIGMOID = 3
 LA_ACT_NONE = 0
 LA_ACT_SILU = 1
 LA_ACT_SIGMOID = 2
+LA_QUANT_NONE = 0
+LA_QUANT_ROW = 1
+LA_QUANT_BLOCK = 2
+LA_QUANT_MX = 3
 
 EXPORTED_SYMBOLS = (
     "gdn_fwd",
@@ -69,6 +73,16 @@ EXPORTED_SYMBOLS = (
     "sconv_bwd",
     "sconv_decode",
     "la_sconv_bwd_workspace_bytes",
+    "ssm_fwd",
+    "ssm_bwd",
+    "ssm_decode",
+    "la_ssm_checkpoint_rows",
+    "la_ssm_fwd_workspace_bytes",
+    "la_ssm_bwd_workspace_bytes",
+    "rn_fwd",
+    "rn_bwd",
+    "la_rn_scale_blocks",
+    "la_rn_bwd_workspace_bytes",
 )
 
 _i64 = ctypes.c_int64
@@ -208,15 +222,23 @@ def load(build_if_missing: bool = True):
                                              ctypes.POINTER(_i64)]
         for name, params in (("glr_fwd", GlrFwdParams), ("glr_bwd", GlrBwdParams), ("glr_decode", GlrDecodeParams),
                              ("gn_fwd", GnFwdParams), ("gn_bwd", GnBwdParams), ("sconv_fwd", SconvFwdParams),
-                             ("sconv_bwd", SconvBwdParams), ("sconv_decode", SconvDecodeParams)):
+                             ("sconv_bwd", SconvBwdParams), ("sconv_decode", SconvDecodeParams),
+                             ("ssm_fwd", SsmFwdParams), ("ssm_bwd", SsmBwdParams), ("ssm_decode", SsmDecodeParams),
+                             ("rn_fwd", RnFwdParams), ("rn_bwd", RnBwdParams)):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp]
         for name, args in (("la_glr_checkpoint_rows", [_i64, _i32]),
                            ("la_glr_workspace_bytes", [_i64, _i32, _i32, _i32, _i32]),
                            ("la_gn_bwd_workspace_bytes", [_i64, _i32, _i32, _i32]),
-                           ("la_sconv_bwd_workspace_bytes", [_i64, _i32, _i32, _i32])):
+                           ("la_sconv_bwd_workspace_bytes", [_i64, _i32, _i32, _i32]),
+                           ("la_ssm_checkpoint_rows", [_i64, _i32]),
+                           ("la_ssm_fwd_workspace_bytes", [_i64, _i32, _i32, _i32, _i32, _i32]),
+                           ("la_ssm_bwd_workspace_bytes", [_i64, _i32, _i32, _i32, _i32, _i32]),
+                           ("la_rn_bwd_workspace_bytes", [_i64, _i32])):
             getattr(lib, name).restype = ctypes.c_size_t
             getattr(lib, name).argtypes = args
+        lib.la_rn_scale_blocks.restype = _i32
+        lib.la_rn_scale_blocks.argtypes = [_i32, _i32]
         lib.gdn_fwd_static_workspace.restype = ctypes.c_int
         lib.gdn_fwd_static_workspace.argtypes = [ctypes.POINTER(GdnFwdParams), _vp]
         _lib = lib
@@ -380,6 +402,67 @@ class SconvDecodeParams(ctypes.Structure):
         ("x", _vp), ("x_stride_n", _i64), ("weight", _vp), ("bias", _vp), ("N", _i32), ("D", _i32),
         ("W", _i32), ("x_dtype", _i32), ("weight_dtype", _i32), ("activation", _i32), ("state_pool", _vp),
         ("state_pool_size", _i64), ("state_indices", _vp), ("y", _vp), ("y_stride_n", _i64), ("status", _vp),
+    ]
+
+
+class SsmFwdParams(ctypes.Structure):
+    """Mirror of la_ssm_fwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("dt", _vp), ("dt_stride_t", _i64), ("z", _vp), ("z_stride_t", _i64),
+        ("b", _vp), ("b_stride_t", _i64), ("b_stride_g", _i64), ("c", _vp), ("c_stride_t", _i64),
+        ("c_stride_g", _i64), ("a", _vp), ("skip", _vp), ("dt_bias", _vp), ("dt_softplus", _i32),
+        ("cu_seqlens", _vp), ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("S", _i32), ("G", _i32),
+        ("T", _i64), ("x_dtype", _i32), ("initial_state", _vp), ("initial_state_dtype", _i32),
+        ("state_indices", _vp), ("state_pool_size", _i64), ("time_block", _i32), ("y", _vp), ("y_stride_t", _i64),
+        ("final_state", _vp), ("checkpoints", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+        ("status", _vp),
+    ]
+
+
+class SsmBwdParams(ctypes.Structure):
+    """Mirror of la_ssm_bwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("dt", _vp), ("dt_stride_t", _i64), ("z", _vp), ("z_stride_t", _i64),
+        ("b", _vp), ("b_stride_t", _i64), ("b_stride_g", _i64), ("c", _vp), ("c_stride_t", _i64),
+        ("c_stride_g", _i64), ("a", _vp), ("skip", _vp), ("dt_bias", _vp), ("dt_softplus", _i32),
+        ("cu_seqlens", _vp), ("cu_seqlens_bits", _i32), ("N", _i32), ("D", _i32), ("S", _i32), ("G", _i32),
+        ("T", _i64), ("x_dtype", _i32), ("initial_state", _vp), ("initial_state_dtype", _i32),
+        ("checkpoints", _vp), ("dy", _vp), ("dy_stride_t", _i64), ("d_final_state", _vp), ("dx", _vp),
+        ("dx_stride_t", _i64), ("ddt", _vp), ("ddt_stride_t", _i64), ("dz", _vp), ("dz_stride_t", _i64),
+        ("db", _vp), ("dc", _vp), ("da", _vp), ("d_skip", _vp), ("d_dt_bias", _vp), ("d_initial_state", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("status", _vp),
+    ]
+
+
+class SsmDecodeParams(ctypes.Structure):
+    """Mirror of la_ssm_decode_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_n", _i64), ("dt", _vp), ("dt_stride_n", _i64), ("z", _vp), ("z_stride_n", _i64),
+        ("b", _vp), ("b_stride_n", _i64), ("b_stride_g", _i64), ("c", _vp), ("c_stride_n", _i64),
+        ("c_stride_g", _i64), ("a", _vp), ("skip", _vp), ("dt_bias", _vp), ("dt_softplus", _i32), ("N", _i32),
+        ("D", _i32), ("S", _i32), ("G", _i32), ("x_dtype", _i32), ("state_pool", _vp), ("state_dtype", _i32),
+        ("state_pool_size", _i64), ("state_indices", _vp), ("y", _vp), ("y_stride_n", _i64), ("status", _vp),
+    ]
+
+
+class RnFwdParams(ctypes.Structure):
+    """Mirror of la_rn_fwd_params (same field order and types)."""
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("residual", _vp), ("residual_stride_t", _i64), ("weight", _vp),
+        ("T", _i64), ("V", _i32), ("x_dtype", _i32), ("residual_dtype", _i32), ("weight_dtype", _i32),
+        ("eps", ctypes.c_float), ("quantize", _i32), ("y", _vp), ("y_stride_t", _i64), ("residual_out", _vp),
+        ("residual_out_stride_t", _i64), ("scales", _vp),
+    ]
+
+
+class RnBwdParams(ctypes.Structure):
+    """Mirror of la_rn_bwd_params (same field order and types)."""
+    _fields_ = [
+        ("s", _vp), ("s_stride_t", _i64), ("dy", _vp), ("dy_stride_t", _i64), ("d_residual", _vp),
+        ("d_residual_stride_t", _i64), ("weight", _vp), ("T", _i64), ("V", _i32), ("x_dtype", _i32),
+        ("s_dtype", _i32), ("weight_dtype", _i32), ("eps", ctypes.c_float), ("dx", _vp), ("dx_stride_t", _i64),
+        ("ds", _vp), ("ds_stride_t", _i64), ("d_weight", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 

@@ -1,0 +1,150 @@
+// rn_bwd.cu -- the residual norm's backward (rn.cuh has the method).
+#include "rn.cuh"
+
+namespace la {
+namespace rn {
+namespace {
+
+// The weight gradient is summed in registers over a warp's rows, then over the CTA's groups, then by a second launch over
+// the CTAs, in an order fixed by the shape.
+template <typename X, typename R, int kVec, int NV, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) rn_bwd_kernel(const Args a) {
+    constexpr int E = NV * kVec;
+    __shared__ float2 red[2][32];
+    extern __shared__ float sums[];  // [groups][V]
+    const int warp = threadIdx.x >> 5;
+    const int groups = (blockDim.x >> 5) / a.warps, g = warp / a.warps;
+    const auto pl = place<kVec, NV>(warp % a.warps);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups, rounds = (a.T + step - 1) / step;
+    const float inv_v = 1.f / a.V;
+    float w[E], dw[E];
+    load_weight<kVec, NV>(w, a, pl);
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[e] = 0.f;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+    for (int64_t n = 0; n < rounds; ++n, t += step) {
+        const bool live = t < a.T;
+        Vec<R, kVec> s[NV], dr[NV];
+        Vec<X, kVec> dy[NV];
+        load_row<R, kVec, NV>(s, a.x, t * a.x_st, live, pl, a.V);
+        load_row<X, kVec, NV>(dy, a.dy, t * a.dy_st, live, pl, a.V);
+        if (a.dres) load_row<R, kVec, NV>(dr, a.dres, t * a.dres_st, live, pl, a.V);
+        float sum = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float v = s[e / kVec].get(e % kVec), d = dy[e / kVec].get(e % kVec);
+            sum = fmaf(v, v, sum);
+            dot = fmaf(d * w[e], v, dot);
+        }
+        row_reduce<false>(sum, dot, a.warps, red, static_cast<int>(n));
+        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps)), m = dot * inv_v * rs * rs;  // mean(dn n) r, what s is taken off with
+        if (!live) continue;  // a warp has one row
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float v = s[e / kVec].get(e % kVec), d = dy[e / kVec].get(e % kVec);
+            dw[e] = fmaf(d, v * rs, dw[e]);
+            o[e] = rs * fmaf(-v, m, d * w[e]);
+            if (a.dres) o[e] += dr[e / kVec].get(e % kVec);
+        }
+        if (a.y) store_row<X, kVec, NV>(a.y, t * a.y_st, o, pl, a.V);
+        if (a.ds) store_row<R, kVec, NV>(a.ds, t * a.ds_st, o, pl, a.V);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int c = pl.column(k) + i;
+            if (c < a.V) sums[g * a.V + c] = dw[k * kVec + i];
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.V; c += blockDim.x) {
+        float s = 0.f;
+        for (int q = 0; q < groups; ++q) s += sums[q * a.V + c];
+        a.pw[static_cast<int64_t>(blockIdx.x) * a.V + c] = s;
+    }
+}
+
+// dw[c] = the sum of the CTAs' partial sums.  A CTA takes 32 columns; its 32 warps take every 32nd row, in order.
+__global__ void __launch_bounds__(1024) rn_sum_kernel(const float* pw, int64_t rows, int V, void* dw, int w_bf16) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = c < V ? strided_sum<16>(pw + c, V, w, rows, 32) : 0.f;
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < V) {
+#pragma unroll
+        for (int i = 1; i < 32; ++i) s += part[i][lane];
+        store_any(dw, c, w_bf16, s);
+    }
+}
+
+int64_t bwd_ctas(int64_t T, int V) {
+    const Shape sh = shape(V);
+    const int groups = sh.threads / 32 / sh.warps;
+    return std::max<int64_t>(1, std::min<int64_t>((T + groups - 1) / groups, kSms * 2));
+}
+
+struct Launch {
+    template <typename X, typename R, int kVec, int NV>
+    static la_status run(const Args& a, Shape sh, cudaStream_t s) {
+        const size_t smem = static_cast<size_t>(sh.threads / 32 / sh.warps) * a.V * sizeof(float);
+        const unsigned grid = static_cast<unsigned>(bwd_ctas(a.T, a.V));
+        if (sh.threads == 512) {
+            static const cudaError_t opted =
+                cudaFuncSetAttribute(rn_bwd_kernel<X, R, kVec, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV * 4);
+            if (opted != cudaSuccess) return LA_ERR_CUDA;
+            rn_bwd_kernel<X, R, kVec, NV, 512><<<grid, 512, smem, s>>>(a);
+        } else {
+            rn_bwd_kernel<X, R, kVec, NV, 256><<<grid, 256, smem, s>>>(a);
+        }
+        return launched();
+    }
+};
+
+}  // namespace
+}  // namespace rn
+}  // namespace la
+
+using namespace la;
+using namespace la::mixer;
+using namespace la::rn;
+
+extern "C" {
+
+size_t la_rn_bwd_workspace_bytes(int64_t T, int32_t V) {
+    if (T < 0 || V <= 0 || V > kMaxV) return 0;
+    return (static_cast<size_t>(bwd_ctas(T, V)) * V * 4 + 255) & ~size_t(255);
+}
+
+la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
+    if (!p) return LA_ERR_INVALID_ARG;
+    la_status st = check(p->T, p->V, p->x_dtype, p->s_dtype, p->weight_dtype, p->eps, p->weight);
+    if (st != LA_OK) return st;
+    if (!good_rows(p->s, p->s_stride_t, p->T, p->V, p->s_dtype, false) || !good_rows(p->dy, p->dy_stride_t, p->T, p->V, p->x_dtype, false) ||
+        (p->d_residual && !good_rows(p->d_residual, p->d_residual_stride_t, p->T, p->V, p->s_dtype, false)) ||
+        (p->dx && !good_rows(p->dx, p->dx_stride_t, p->T, p->V, p->x_dtype, true)) ||
+        (p->ds && !good_rows(p->ds, p->ds_stride_t, p->T, p->V, p->s_dtype, true)))
+        return LA_ERR_INVALID_ARG;
+    if ((p->T > 0 && !p->dx && !p->ds) || !p->d_weight || !aligned_to(p->d_weight, dtype_size(p->weight_dtype))) return LA_ERR_INVALID_ARG;
+    if ((st = check_workspace(p->workspace, p->workspace_bytes, la_rn_bwd_workspace_bytes(p->T, p->V))) != LA_OK) return st;
+    Args a = {};
+    a.x = p->s; a.x_st = p->s_stride_t; a.dy = p->dy; a.dy_st = p->dy_stride_t; a.dres = p->d_residual; a.dres_st = p->d_residual_stride_t;
+    a.w = p->weight; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
+    a.T = p->T; a.V = p->V; a.eps = p->eps;
+    a.y = p->dx; a.y_st = p->dx_stride_t; a.ds = p->ds; a.ds_st = p->ds_stride_t;
+    a.pw = static_cast<float*>(p->workspace);
+    const int vec = 16 / dtype_size(p->x_dtype), xs = dtype_size(p->x_dtype), rs = dtype_size(p->s_dtype);
+    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, rs, vec) && wide_rows(a.dy, a.dy_st, a.T, xs, vec) && wide_rows(a.dres, a.dres_st, a.T, rs, vec) &&
+                      wide_rows(a.y, a.y_st, a.T, xs, vec) && wide_rows(a.ds, a.ds_st, a.T, rs, vec);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int64_t rows = 0;
+    if (p->T > 0) {
+        if ((st = dispatch<Launch>(a, p->x_dtype, p->s_dtype, wide, s)) != LA_OK) return st;
+        rows = bwd_ctas(a.T, a.V);
+    }
+    rn_sum_kernel<<<static_cast<unsigned>((a.V + 31) / 32), 1024, 0, s>>>(a.pw, rows, a.V, p->d_weight, a.w_bf16);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,182 @@
+// rn_fwd.cu -- the residual norm's forward (rn.cuh has the method).
+#include "rn.cuh"
+
+namespace la {
+namespace rn {
+namespace {
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <int kVec>
+__device__ __forceinline__ void store_e4m3(uint8_t* to, const float* v) {
+    if (kVec == 1) {
+        *to = static_cast<uint8_t>(e4m3_pair(v[0], 0.f));
+    } else {
+        uint32_t w[kVec / 4 > 0 ? kVec / 4 : 1];
+#pragma unroll
+        for (int i = 0; i + 3 < kVec; i += 4) w[i / 4] = e4m3_pair(v[i], v[i + 1]) | e4m3_pair(v[i + 2], v[i + 3]) << 16;
+        if (kVec == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[kVec > 4 ? 1 : 0]);
+        else *reinterpret_cast<uint32_t*>(to) = w[0];
+    }
+}
+
+constexpr float kTop = 448.f;  // the largest e4m3 value
+
+// A block's scale from its largest |y|, which counts as 2^-100 at least: most / 448, or as a power of two the least with
+// most <= 448 scale: with most = m 2^e, 1 <= m < 2, that is 2^(e - 8), or 2^(e - 7) where m > 1.75.
+struct Scale {
+    float inverse;
+    float scale;
+    uint8_t exponent;  // of the power of two, as e8m0 has it; 255 (NaN) where most is not finite
+};
+__device__ __forceinline__ Scale scale_of(float most, bool power) {
+    most = max_nan(most, 0x1p-100f);
+    Scale s;
+    if (power) {
+        const uint32_t b = __float_as_uint(most), e = (b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);
+        s.exponent = b >= 0x7F800000u ? 255 : static_cast<uint8_t>(e);
+        s.scale = __uint_as_float(b >= 0x7F800000u ? 0x7FC00000u : e << 23);
+        s.inverse = __uint_as_float(b >= 0x7F800000u ? 0x7FC00000u : (254u - e) << 23);
+    } else {
+        s.exponent = 0;
+        s.scale = __fdiv_rn(most, kTop);
+        s.inverse = __fdiv_rn(kTop, most);
+    }
+    return s;
+}
+
+template <typename X, typename R, int kVec, int NV, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) rn_fwd_kernel(const Args a) {
+    constexpr int E = NV * kVec;
+    __shared__ float2 red[2][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = (blockDim.x >> 5) / a.warps, g = warp / a.warps;
+    const auto pl = place<kVec, NV>(warp % a.warps);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups, rounds = (a.T + step - 1) / step;
+    const float inv_v = 1.f / a.V;
+    float w[E];
+    load_weight<kVec, NV>(w, a, pl);
+    int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+    for (int64_t n = 0; n < rounds; ++n, t += step) {
+        const bool live = t < a.T;
+        Vec<X, kVec> x[NV];
+        Vec<R, kVec> r[NV];
+        load_row<X, kVec, NV>(x, a.x, t * a.x_st, live, pl, a.V);
+        if (a.res) load_row<R, kVec, NV>(r, a.res, t * a.res_st, live, pl, a.V);
+        float s[E], sum = 0.f, most = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            s[e] = x[e / kVec].get(e % kVec);
+            if (a.res) s[e] = to_f(from_f<R>(s[e] + r[e / kVec].get(e % kVec)));
+            sum = fmaf(s[e], s[e], sum);
+        }
+        if (a.res && live) store_row<R, kVec, NV>(a.out, t * a.out_st, s, pl, a.V);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            s[e] *= w[e];
+            if (a.quant == LA_QUANT_ROW) most = max_nan(most, fabsf(s[e]));
+        }
+        row_reduce<true>(sum, most, a.warps, red, static_cast<int>(n));
+        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps));
+        if (!live) continue;  // a warp has one row
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] *= rs;
+        if (a.quant == LA_QUANT_NONE) {
+            store_row<X, kVec, NV>(a.y, t * a.y_st, s, pl, a.V);
+            continue;
+        }
+        if (a.quant == LA_QUANT_ROW) {
+            const Scale sc = scale_of(most * rs, false);
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[e] *= sc.inverse;
+            if (warp % a.warps == 0 && lane == 0) static_cast<float*>(a.scales)[t] = sc.scale;
+        } else {
+            // a block is kLanes lanes of kParts vectors
+            auto blocks = [&](auto width) {
+                constexpr int kLanes = width / kVec < 32 ? width / kVec : 32, kParts = width / kVec < 32 ? 1 : width / kVec / 32;
+#pragma unroll
+                for (int k = 0; k < NV; k += kParts) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kParts * kVec; ++i) m = max_nan(m, fabsf(s[k * kVec + i]));
+#pragma unroll
+                    for (int off = 1; off < kLanes; off *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    const Scale sc = scale_of(m, width == 32);
+#pragma unroll
+                    for (int i = 0; i < kParts * kVec; ++i) s[k * kVec + i] *= sc.inverse;
+                    const int c = pl.column(k);
+                    if (c < a.V && lane % kLanes == 0) {
+                        const int64_t at = t * a.blocks + c / width;
+                        if (width == 32) static_cast<uint8_t*>(a.scales)[at] = sc.exponent;
+                        else static_cast<float*>(a.scales)[at] = sc.scale;
+                    }
+                }
+            };
+            if (a.quant == LA_QUANT_MX) blocks(std::integral_constant<int, 32>());
+            else blocks(std::integral_constant<int, 128>());
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = pl.column(k);
+            if (c < a.V) store_e4m3<kVec>(static_cast<uint8_t*>(a.y) + t * a.y_st + c, s + k * kVec);
+        }
+    }
+}
+
+struct Launch {
+    template <typename X, typename R, int kVec, int NV>
+    static la_status run(const Args& a, Shape sh, cudaStream_t s) {
+        const int groups = sh.threads / 32 / sh.warps;
+        const int64_t grid = std::min<int64_t>((a.T + groups - 1) / groups, kSms * 4);
+        if (sh.threads == 512) rn_fwd_kernel<X, R, kVec, NV, 512><<<static_cast<unsigned>(grid), 512, 0, s>>>(a);
+        else rn_fwd_kernel<X, R, kVec, NV, 256><<<static_cast<unsigned>(grid), 256, 0, s>>>(a);
+        return launched();
+    }
+};
+
+}  // namespace
+}  // namespace rn
+}  // namespace la
+
+using namespace la;
+using namespace la::mixer;
+using namespace la::rn;
+
+extern "C" {
+
+int32_t la_rn_scale_blocks(int32_t V, int32_t quantize) {
+    if (V <= 0) return 0;
+    return quantize == LA_QUANT_ROW ? 1 : quantize == LA_QUANT_BLOCK ? (V - 1) / 128 + 1 : quantize == LA_QUANT_MX ? (V - 1) / 32 + 1 : 0;
+}
+
+la_status rn_fwd(const la_rn_fwd_params* p, void* stream) {
+    if (!p) return LA_ERR_INVALID_ARG;
+    const int32_t rd = p->residual ? p->residual_dtype : p->x_dtype;
+    la_status st = check(p->T, p->V, p->x_dtype, rd, p->weight_dtype, p->eps, p->weight);
+    if (st != LA_OK) return st;
+    if (p->quantize < LA_QUANT_NONE || p->quantize > LA_QUANT_MX) return LA_ERR_INVALID_ARG;
+    const bool eight = p->quantize != LA_QUANT_NONE;
+    if (!good_rows(p->x, p->x_stride_t, p->T, p->V, p->x_dtype, false)) return LA_ERR_INVALID_ARG;
+    if (p->residual && (!good_rows(p->residual, p->residual_stride_t, p->T, p->V, rd, false) ||
+                        !good_rows(p->residual_out, p->residual_out_stride_t, p->T, p->V, rd, true)))
+        return LA_ERR_INVALID_ARG;
+    if (p->T > 0 && (!p->y || p->y_stride_t < 0 || (p->T > 1 && p->y_stride_t < p->V) || (!eight && !aligned_to(p->y, dtype_size(p->x_dtype)))))
+        return LA_ERR_INVALID_ARG;
+    if (eight && p->T > 0 && (!p->scales || (p->quantize != LA_QUANT_MX && !aligned_to(p->scales, 4)))) return LA_ERR_INVALID_ARG;
+    if (p->T == 0) return LA_OK;
+    Args a = {};
+    a.x = p->x; a.x_st = p->x_stride_t; a.res = p->residual; a.res_st = p->residual_stride_t;
+    a.w = p->weight; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;
+    a.T = p->T; a.V = p->V; a.eps = p->eps; a.quant = p->quantize; a.blocks = la_rn_scale_blocks(p->V, p->quantize);
+    a.y = p->y; a.y_st = p->y_stride_t; a.out = p->residual ? p->residual_out : nullptr; a.out_st = p->residual_out_stride_t;
+    a.scales = p->scales;
+    const int vec = 16 / dtype_size(p->x_dtype);
+    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, dtype_size(p->x_dtype), vec) && wide_rows(a.res, a.res_st, a.T, dtype_size(rd), vec) &&
+                      wide_rows(a.out, a.out_st, a.T, dtype_size(rd), vec) && wide_rows(a.y, a.y_st, a.T, eight ? 1 : dtype_size(p->x_dtype), vec);
+    return dispatch<Launch>(a, p->x_dtype, rd, wide, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,265 @@
+// ssm.cuh -- the selective state space scan (ssm_fwd, ssm_bwd, ssm_decode): what ssm_fwd.cu, ssm_bwd.cu and ssm.cu share.
+//
+// Channel d of group j, states s, with the step size dt_t (the raw one plus the bias, through softplus where asked for):
+//
+//   a_t = e^(dt_t A[d, s]),  h_t = a_t h_{t-1} + dt_t x_t B_t[j, s],  p_t = sum_s C_t[j, s] h_t + skip[d] x_t,
+//   y_t = p_t  or  p_t silu(z_t);
+//
+// and backwards, dp being the gradient of p and g_t the one that leaves token t towards h_{t-1}:
+//
+//   e_t = C_t dp_t + g_{t+1},  g_t = a_t e_t,  dC_t = sum_d dp h_t,  dB_t = sum_d e_t dt x,  du = sum_s e_t B_t,
+//   w_t = g_t h_{t-1},  dA += w_t dt,  dx = du dt + dp skip,  d dt = du x + sum_s w_t A.
+//
+// A thread holds four states of a few channels in registers and walks the tokens; Q = 1, 2, 4, 8 or 16 lanes share a
+// channel (up to 64 states, the ones beyond S with A = B = C = 0), so one warp has 32 / Q groups of channels beside
+// each other.  B and C are read from shared memory once for all of a thread's channels, the steps once for all its states.
+#pragma once
+#include <algorithm>
+
+#include "mixer.cuh"
+
+namespace la {
+namespace ssm {
+
+using namespace la::mixer;
+
+constexpr int kSave = 32;  // tokens between saved states
+constexpr int kMaxS = 64;
+constexpr int kSms = 152;
+
+// ex2.approx is 0.3 units of 2^-24 low on average just below 1, where an error adds up over 1 / |dt A| tokens: its
+// argument makes up for that (the gated linear recurrence's decays have the measurements).
+constexpr float kEx2Low = 0.3f * 0x1p-24f * kLog2e;
+
+struct Args {
+    const void *x, *dt, *z, *b, *c, *dy;
+    int64_t x_st, dt_st, z_st, dy_st, b_st, b_sg, c_st, c_sg;
+    const float *A, *skip, *bias;
+    int softplus;
+    const void* cu;
+    int cu64, N;
+    int64_t T;
+    int D, S, G, Dg, tiles_pg;  // channels and channel tiles of a group
+    const void* s0;
+    int s0_bf16;
+    const int32_t* idx;
+    int64_t pool;
+    void* y;
+    int64_t y_st;
+    float *fin, *ckpt;
+    const float* dfin;
+    void *dx, *ddt, *dz, *db, *dc;
+    int64_t dx_st, ddt_st, dz_st;
+    float *dA, *dskip, *dbias, *ds0;
+    int32_t* status;
+    int shift;           // a time block is 2^shift tokens
+    float *table, *sums; // [slots][D][S]: what a block leaves from nothing, then what enters it; [slots][D]: its steps' sum
+    float* dbc;          // [tiles of a group][T][G][2][S]: dB and dC of a tile's channels
+    float *pA, *pch;     // [parts][D][S], [parts][2][D]: partial sums of dA, and of d skip and d bias
+    int parts;
+    int vec, svec;       // wide accesses: rows of the operands; of the states
+};
+
+// ---------------------------------------------------------------- time blocks of 2^shift tokens
+LA_HOST_DEVICE int64_t slots_for(int64_t T, int32_t N, int shift) { return (T >> shift) + N; }
+
+// Block c of sequence i is slot (cu[i] >> shift) + i + c (seq_search.h); called by whole warps.
+__device__ __forceinline__ SeqBlock find_time_block(const Args& a, int shift, int64_t slot) {
+    const int lane = threadIdx.x & 31;
+    SlotSearch f = {0, a.N, true};
+    while (f.n > 1) {
+        const int32_t i = f.lo + lane * f.step();
+        const bool live = lane * f.step() < f.n;
+        const int64_t v = live ? (cu_load(a.cu, a.cu64, i) >> shift) + i : 0;
+        const unsigned here = __ballot_sync(0xffffffffu, live && v <= slot);
+        f.narrow(here, here);
+    }
+    SeqBlock b;
+    b.seq = -1;
+    b.start = b.count = b.c = b.len = b.first = 0;
+    const int64_t s0 = cu_load(a.cu, a.cu64, f.lo), s1 = cu_load(a.cu, a.cu64, f.lo + 1);
+    if (s0 < 0 || s1 < s0 || s1 > a.T) return b;
+    const int64_t c = slot - ((s0 >> shift) + f.lo);
+    if (c < 0 || (c > 0 && (c << shift) >= s1 - s0)) return b;
+    b.seq = f.lo;
+    b.c = static_cast<int32_t>(c);
+    b.first = static_cast<int32_t>(s0);
+    b.len = static_cast<int32_t>(s1 - s0);
+    b.start = static_cast<int32_t>(s0 + (c << shift));
+    b.count = static_cast<int32_t>(min(s1 - b.start, int64_t(1) << shift));
+    return b;
+}
+__device__ __forceinline__ int64_t this_slot() { return blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z; }
+
+// Where a sequence's state is in initial_state, or -1 with the status set.
+__device__ __forceinline__ int64_t state_row(const Args& a, int32_t seq) {
+    if (!a.idx) return seq;
+    const int64_t k = a.idx[seq];
+    if (k < 0 || k >= a.pool) {
+        raise_status(a.status, LA_ERR_BAD_STATE_INDEX);
+        return -1;
+    }
+    return k;
+}
+
+// ---------------------------------------------------------------- steps
+__device__ __forceinline__ float step_of(float raw, int softplus) {
+    return !softplus || raw > 20.f ? raw : log1pf(expf(raw));  // above 20 log1p(e^x) is x in 32 bits
+}
+
+// ---------------------------------------------------------------- channels of a tile, lanes of a thread
+struct Tile {
+    int group, ch, n;  // the tile's group, first channel and number of channels
+};
+__device__ __forceinline__ Tile tile_of(const Args& a, int tile, int width) {
+    Tile t;
+    t.group = tile / a.tiles_pg;
+    const int at = (tile - t.group * a.tiles_pg) * width;
+    t.ch = t.group * a.Dg + at;
+    t.n = min(width, a.Dg - at);
+    return t;
+}
+
+// Four consecutive elements of a row, of which n exist (0 for the others).
+template <typename X>
+__device__ __forceinline__ float4 load4(const void* base, int64_t at, int n, int vec) {
+    const X* p = static_cast<const X*>(base) + at;
+    float v[4];
+    if (vec && n >= 4) {
+        Packed<X, 4> w;
+        w.load(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w.get(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename X>
+__device__ __forceinline__ void store4(void* base, int64_t at, int n, int vec, float4 f) {
+    X* p = static_cast<X*>(base) + at;
+    const float v[4] = {f.x, f.y, f.z, f.w};
+    if (vec && n >= 4) store_packed<X, 4>(p, v);
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = from_f<X>(v[i]);
+}
+__device__ __forceinline__ float2 lo(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi(float4 v) { return make_float2(v.z, v.w); }
+
+// Four states of one channel in a [rows, D, S] array; 0 beyond S or where the channel does not exist.
+__device__ __forceinline__ float4 load_states(const void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!live || s >= a.S) return make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t at = (row * a.D + d) * a.S + s;
+    if (a.svec && !is_bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (s + i < a.S) v[i] = load_any(base, at + i, is_bf16);
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_states(void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16, float4 f) {
+    if (!live || s >= a.S) return;
+    const int64_t at = (row * a.D + d) * a.S + s;
+    if (a.svec && !is_bf16) {
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = f;
+        return;
+    }
+    const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (s + i < a.S) store_any(base, at + i, is_bf16, v[i]);
+}
+
+// A thread's kPairs x 2 channels of four states, as pairs of channels: v[p][s] = channels (2p, 2p + 1), state s.
+template <int kPairs>
+__device__ __forceinline__ void load_thread_states(float2 (&v)[kPairs][4], const void* base, int64_t row, const Args& a, int d, int end, int s, int is_bf16) {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+        const float4 x = load_states(base, row, a, d + 2 * p, s, d + 2 * p < end, is_bf16);
+        const float4 y = load_states(base, row, a, d + 2 * p + 1, s, d + 2 * p + 1 < end, is_bf16);
+        v[p][0] = make_float2(x.x, y.x);
+        v[p][1] = make_float2(x.y, y.y);
+        v[p][2] = make_float2(x.z, y.z);
+        v[p][3] = make_float2(x.w, y.w);
+    }
+}
+template <int kPairs>
+__device__ __forceinline__ void store_thread_states(const float2 (&v)[kPairs][4], void* base, int64_t row, const Args& a, int d, int end, int s, int is_bf16) {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+        store_states(base, row, a, d + 2 * p, s, d + 2 * p < end, is_bf16, make_float4(v[p][0].x, v[p][1].x, v[p][2].x, v[p][3].x));
+        store_states(base, row, a, d + 2 * p + 1, s, d + 2 * p + 1 < end, is_bf16, make_float4(v[p][0].y, v[p][1].y, v[p][2].y, v[p][3].y));
+    }
+}
+template <int kPairs>
+__device__ __forceinline__ void zero(float2 (&v)[kPairs][4]) {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[p][s] = both(0.f);
+}
+
+// Sums kValues values over the lanes that differ in the bits from kBit up to kEnd.  While there are several values each
+// step halves them: a lane keeps the upper half where its bit is set.  Returns the number of the first value that is
+// left (of max(1, kValues / lanes)); where one is left before the lanes are done, the lanes beyond hold it too.
+template <int kValues, int kBit, int kEnd>
+__device__ __forceinline__ int spread_sum(float (&v)[kValues]) {
+    if constexpr (kBit >= kEnd) {
+        return 0;
+    } else if constexpr (kValues == 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], kBit);
+        return spread_sum<1, 2 * kBit, kEnd>(v);
+    } else {
+        constexpr int kHalf = kValues / 2;
+        const bool up = threadIdx.x & kBit;
+        float w[kHalf];
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) {
+            const float mine = up ? v[i + kHalf] : v[i], other = up ? v[i] : v[i + kHalf];
+            w[i] = mine + __shfl_xor_sync(0xffffffffu, other, kBit);
+        }
+        const int at = spread_sum<kHalf, 2 * kBit, kEnd>(w);
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) v[i] = w[i];
+        return (up ? kHalf : 0) + at;
+    }
+}
+
+// Lanes of a channel for S states.
+inline int lanes_for(int S) {
+    int q = 1;
+    while (4 * q < S) q *= 2;
+    return q;
+}
+// Calls F::run<X, Q>(args...) for the operands' type and the states.
+template <typename F, typename X, typename... A>
+la_status by_states(int S, A&&... args) {
+    switch (lanes_for(S)) {
+        case 1: return F::template run<X, 1>(args...);
+        case 2: return F::template run<X, 2>(args...);
+        case 4: return F::template run<X, 4>(args...);
+        case 8: return F::template run<X, 8>(args...);
+        default: return F::template run<X, 16>(args...);
+    }
+}
+template <typename F, typename... A>
+la_status by_shape(int32_t dtype, int S, A&&... args) {
+    return dtype == LA_DTYPE_BF16 ? by_states<F, bf16>(S, args...) : by_states<F, float>(S, args...);
+}
+
+inline dim3 slot_grid(int tiles, int64_t slots) {
+    const int64_t y = std::min<int64_t>(slots, 65535);
+    return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(y), static_cast<unsigned>((slots + y - 1) / y));
+}
+// ssm_fwd.cu, ssm_bwd.cu
+int fwd_shift(int64_t T, int D, int S, int G, int time_block);
+la_status run_fwd(Args a, int32_t dtype, cudaStream_t s);
+la_status run_bwd(Args a, int32_t dtype, cudaStream_t s);
+int bwd_width(int S);
+int bwd_parts(int64_t T, int32_t N, int D, int S, int G);
+
+}  // namespace ssm
+}  // namespace la

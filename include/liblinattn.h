@@ -814,6 +814,195 @@ typedef struct la_sconv_decode_params {
 /* sconv_decode -- one sconv_fwd step per sequence against a state pool (as gdn_decode). */
 la_status sconv_decode(const la_sconv_decode_params* p, void* stream);
 
+/* ===========================================================================
+ * Operators of a state-space block: the selective state space scan (ssm_*) and
+ * the root-mean-square norm with the residual's addition (rn_*).  They follow the
+ * conventions of the token-mixer operators above.
+ * ======================================================================== */
+
+/* Parameters of ssm_fwd.  Strides are in elements; x, dt, z, b, c and y have one type. */
+typedef struct la_ssm_fwd_params {
+    const void* x;    int64_t x_stride_t;              /* [T, D] */
+    const void* dt;   int64_t dt_stride_t;             /* [T, D]: step sizes, before dt_bias and dt_softplus */
+    const void* z;    int64_t z_stride_t;              /* [T, D] gate, or NULL */
+    const void* b;    int64_t b_stride_t, b_stride_g;  /* [T, G, S] */
+    const void* c;    int64_t c_stride_t, c_stride_g;  /* [T, G, S] */
+    const float* a;                                    /* [D, S] contiguous: rates, <= 0 for a decaying state */
+    const float* skip;                                 /* [D] or NULL */
+    const float* dt_bias;                              /* [D] or NULL */
+    int32_t dt_softplus;                               /* the step is softplus(dt + dt_bias) */
+    const void* cu_seqlens;                            /* [N + 1] */
+    int32_t cu_seqlens_bits;                           /* 32 or 64 */
+    int32_t N, D, S, G;                                /* S 1 to 64; D a multiple of G */
+    int64_t T;
+    int32_t x_dtype;                                   /* la_dtype */
+    const void* initial_state;                         /* [N, D, S] contiguous, or NULL (zeros) */
+    int32_t initial_state_dtype;                       /* la_dtype */
+    const int32_t* state_indices;                      /* [N] or NULL: initial_state is then a pool, as in gdn_fwd */
+    int64_t state_pool_size;
+    int32_t time_block;                                /* 0, or a power of two >= 64: see ssm_fwd */
+    void* y;          int64_t y_stride_t;              /* [T, D] out */
+    float* final_state;                                /* [N, D, S] out or NULL; NULL with state_indices */
+    float* checkpoints;                                /* [la_ssm_checkpoint_rows(T, N), D, S] out or NULL */
+    void* workspace;  size_t workspace_bytes;          /* >= la_ssm_fwd_workspace_bytes(T, N, D, S, G, time_block) */
+    int32_t* status;
+} la_ssm_fwd_params;
+
+/*
+ * ssm_fwd -- the selective state space scan: S states a channel, whose input and
+ * output vectors and step sizes come with every token.  For a sequence, channel d
+ * of group j = d / (D / G) and state s
+ *
+ *     dt_t = dt + dt_bias[d], or softplus of that,
+ *     h_t  = exp(dt_t a[d][s]) h_{t-1} + dt_t x_t b_t[j][s],
+ *     p_t  = sum_s c_t[j][s] h_t + skip[d] x_t,     y_t = p_t, or p_t silu(z_t) with z.
+ *
+ * An empty sequence's final state is its initial state (or zeros).  checkpoints
+ * receives the fp32 state entering every 32 tokens of every sequence, for ssm_bwd:
+ * chunk c of sequence i is row cu_seqlens[i] / 32 + i + c (rows in between are left
+ * alone).  y may be x, dt or z itself (same address and stride), and must share no
+ * memory with them otherwise (LA_ERR_INVALID_ARG as for sconv_fwd), nor with b or c.
+ *
+ * Sequences longer than time_block tokens are split along time, blocks starting at
+ * each sequence's first token; a split costs up to 3/4 of the arithmetic again, so
+ * with time_block 0 blocks are as long as T and D allow while the GPU is filled
+ * (powers of two from 64 on).  Results are the same bits for the same T, N, D, S, G and
+ * time_block; with a given time_block they are batch invariant too.
+ */
+la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream);
+
+/* Parameters of ssm_bwd.  Strides are in elements. */
+typedef struct la_ssm_bwd_params {
+    const void* x;    int64_t x_stride_t;
+    const void* dt;   int64_t dt_stride_t;
+    const void* z;    int64_t z_stride_t;
+    const void* b;    int64_t b_stride_t, b_stride_g;
+    const void* c;    int64_t c_stride_t, c_stride_g;
+    const float* a;
+    const float* skip;
+    const float* dt_bias;
+    int32_t dt_softplus;
+    const void* cu_seqlens;
+    int32_t cu_seqlens_bits;
+    int32_t N, D, S, G;
+    int64_t T;
+    int32_t x_dtype;                                   /* of x, dt, z, b, c, dy and their gradients */
+    const void* initial_state;                         /* as the forward's, or NULL */
+    int32_t initial_state_dtype;
+    const float* checkpoints;                          /* the forward's, or NULL (recomputed) */
+    const void* dy;   int64_t dy_stride_t;             /* [T, D] */
+    const float* d_final_state;                        /* [N, D, S] contiguous, or NULL (zeros) */
+    void* dx;         int64_t dx_stride_t;             /* [T, D] out */
+    void* ddt;        int64_t ddt_stride_t;            /* [T, D] out: gradient of dt as given */
+    void* dz;         int64_t dz_stride_t;             /* [T, D] out; NULL without z */
+    void* db;                                          /* [T, G, S] contiguous, out */
+    void* dc;                                          /* [T, G, S] contiguous, out */
+    float* da;                                         /* [D, S] out */
+    float* d_skip;                                     /* [D] out; NULL without skip */
+    float* d_dt_bias;                                  /* [D] out; NULL without dt_bias */
+    float* d_initial_state;                            /* [N, D, S] out or NULL */
+    void* workspace;  size_t workspace_bytes;          /* >= la_ssm_bwd_workspace_bytes(T, N, D, S, G, checkpoints != NULL) */
+    int32_t* status;
+} la_ssm_bwd_params;
+
+/*
+ * ssm_bwd -- gradients of L = sum(dy * y) + sum(d_final_state * final_state).  The gradients
+ * of a sequence's own inputs do not depend on the batch around it; sums over channels and
+ * over the batch run in an order fixed by the shape.  dx, ddt and dz must share no
+ * memory with each other or an input.
+ */
+la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream);
+
+/* Parameters of ssm_decode.  Strides are in elements. */
+typedef struct la_ssm_decode_params {
+    const void* x;    int64_t x_stride_n;              /* [N, D] */
+    const void* dt;   int64_t dt_stride_n;             /* [N, D] */
+    const void* z;    int64_t z_stride_n;              /* [N, D] or NULL */
+    const void* b;    int64_t b_stride_n, b_stride_g;  /* [N, G, S] */
+    const void* c;    int64_t c_stride_n, c_stride_g;  /* [N, G, S] */
+    const float* a;
+    const float* skip;
+    const float* dt_bias;
+    int32_t dt_softplus;
+    int32_t N, D, S, G;
+    int32_t x_dtype;
+    void* state_pool;                                  /* [state_pool_size, D, S] contiguous, updated in place */
+    int32_t state_dtype;
+    int64_t state_pool_size;
+    const int32_t* state_indices;                      /* [N] or NULL: sequence i uses slot i */
+    void* y;          int64_t y_stride_n;              /* [N, D] out */
+    int32_t* status;
+} la_ssm_decode_params;
+
+/* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode). */
+la_status ssm_decode(const la_ssm_decode_params* p, void* stream);
+
+/* Rows of ssm_fwd's checkpoints buffer: T / 32 + N (0 for invalid arguments). */
+size_t la_ssm_checkpoint_rows(int64_t T, int32_t N);
+
+/* Bytes of device workspace that ssm_fwd and ssm_bwd need (0 for invalid arguments, and where none is needed). */
+size_t la_ssm_fwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int32_t G, int32_t time_block);
+size_t la_ssm_bwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int32_t G, int32_t checkpoints_given);
+
+/* How rn_fwd writes its result: in the input's type, or as e4m3 values with a scale for each row (fp32), each block
+ * of 128 columns (fp32), or each block of 32 columns (a power of two, as e8m0). */
+typedef enum la_quantize { LA_QUANT_NONE = 0, LA_QUANT_ROW = 1, LA_QUANT_BLOCK = 2, LA_QUANT_MX = 3 } la_quantize;
+
+/* Parameters of rn_fwd.  Strides are in elements; V is contiguous. */
+typedef struct la_rn_fwd_params {
+    const void* x;          int64_t x_stride_t;            /* [T, V] */
+    const void* residual;   int64_t residual_stride_t;     /* [T, V] or NULL */
+    const void* weight;                                    /* [V] */
+    int64_t T;
+    int32_t V;                                             /* at most 16384 */
+    int32_t x_dtype, residual_dtype, weight_dtype;         /* a residual of fp32 x is fp32 */
+    float eps;                                             /* > 0 */
+    int32_t quantize;                                      /* la_quantize */
+    void* y;                int64_t y_stride_t;            /* [T, V] out: x's type, or e4m3 */
+    void* residual_out;     int64_t residual_out_stride_t; /* [T, V] out: x + residual, the residual's type; unused without it */
+    void* scales;                                          /* [T, la_rn_scale_blocks(V, quantize)] contiguous, out; NULL without */
+} la_rn_fwd_params;
+
+/*
+ * rn_fwd -- the norm before a block: adds the last block's output to the residual
+ * stream, and norms its rows,
+ *
+ *     s = x + residual (rounded to the residual's type, which is what is normed; s = x without one),
+ *     y = s / sqrt(mean(s^2) + eps) weight.
+ *
+ * In 8 bits y is e4m3(y / scale) with, m being a block's largest |y| and at least
+ * 2^-100, scale = m / 448, or for LA_QUANT_MX the least power of two with m <= 448
+ * scale.  A block whose largest value is not finite has a scale of NaN.
+ * residual_out may be residual or x itself; no other results share memory with an input.
+ */
+la_status rn_fwd(const la_rn_fwd_params* p, void* stream);
+
+/* Scales of a row of rn_fwd (0 for LA_QUANT_NONE or invalid arguments). */
+int32_t la_rn_scale_blocks(int32_t V, int32_t quantize);
+
+/* Parameters of rn_bwd.  Strides are in elements; V is contiguous. */
+typedef struct la_rn_bwd_params {
+    const void* s;          int64_t s_stride_t;            /* [T, V]: what was normed (residual_out, or x) */
+    const void* dy;         int64_t dy_stride_t;           /* [T, V] */
+    const void* d_residual; int64_t d_residual_stride_t;   /* [T, V]: gradient of residual_out, or NULL */
+    const void* weight;
+    int64_t T;
+    int32_t V;
+    int32_t x_dtype, s_dtype, weight_dtype;                /* of dy, dx; of s, d_residual, ds; of weight, d_weight */
+    float eps;
+    void* dx;               int64_t dx_stride_t;           /* [T, V] out or NULL: gradient of x and of the residual */
+    void* ds;               int64_t ds_stride_t;           /* [T, V] out or NULL: the same in s's type */
+    void* d_weight;                                        /* [V] out */
+    void* workspace;        size_t workspace_bytes;        /* >= la_rn_bwd_workspace_bytes(T, V) */
+} la_rn_bwd_params;
+
+/* rn_bwd -- gradients of L = sum(dy * y) + sum(d_residual * residual_out), of 8-bit results as if they were y itself.
+ * At least one of dx and ds is given; each may be dy, d_residual or s itself.  The sum over tokens runs in an order fixed
+ * by the shape. */
+la_status rn_bwd(const la_rn_bwd_params* p, void* stream);
+
+size_t la_rn_bwd_workspace_bytes(int64_t T, int32_t V);
+
 /*
  * Host helper: total checkpoint rows R = sum_i ceil(L_i / n) for a HOST copy of
  * cu_seqlens (idx_bits 32 or 64).  Returns LA_ERR_INVALID_ARG for n <= 0 or a
