@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kThreads) ssm_decode_kernel(const Args a) {
     const float4 A = load_states(a.A, 0, a, d, s, live, 0);
     const float4 b = load4<X>(a.b, i * a.b_st + j * a.b_sg + s, a.S - s, a.vec), c = load4<X>(a.c, i * a.c_st + j * a.c_sg + s, a.S - s, a.vec);
     const float x = live ? to_f(static_cast<const X*>(a.x)[i * a.x_st + d]) : 0.f;
-    const float dt = live ? step_of(to_f(static_cast<const X*>(a.dt)[i * a.dt_st + d]) + (a.bias ? a.bias[d] : 0.f), a.softplus) : 0.f;
+    const float dt = live ? steps_of(both(to_f(static_cast<const X*>(a.dt)[i * a.dt_st + d]) + (a.bias ? a.bias[d] : 0.f)), a.softplus).x : 0.f;
     const float u = dt * x, l = dt * kLog2e;
     h.x = fmaf(ex2(l * A.x), h.x, u * b.x);
     h.y = fmaf(ex2(l * A.y), h.y, u * b.y);

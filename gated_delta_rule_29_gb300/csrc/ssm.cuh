@@ -53,7 +53,7 @@ struct Args {
     float *dA, *dskip, *dbias, *ds0;
     int32_t* status;
     int shift;           // a time block is 2^shift tokens
-    float *table, *sums; // [slots][D][S]: what a block leaves from nothing, then what enters it; [slots][D]: its steps' sum
+    float *table, *sums; // [blocks][D][S]: what a block leaves from nothing, then what enters it; [blocks][D]: its steps' sum
     float* dbc;          // [tiles of a group][T][G][2][S]: dB and dC of a tile's channels
     float *pA, *pch;     // [parts][D][S], [parts][2][D]: partial sums of dA, and of d skip and d bias
     int parts;
@@ -61,33 +61,52 @@ struct Args {
 };
 
 // ---------------------------------------------------------------- time blocks of 2^shift tokens
+// Blocks start at each sequence's first token.  Two numberings, both of (T >> shift) + N blocks and found without a table:
+// slots, block c of sequence i being (cu[i] >> shift) + i + c (seq_search.h), the rows of the saved states; and launch order,
+// the first blocks of all sequences before all others, block c > 0 of sequence i being N + (cu[i] >> shift) + c - 1 (a
+// sequence of L tokens has (L - 1) >> shift of those, and no more fit between its boundaries' quotients).
 LA_HOST_DEVICE int64_t slots_for(int64_t T, int32_t N, int shift) { return (T >> shift) + N; }
 
-// Block c of sequence i is slot (cu[i] >> shift) + i + c (seq_search.h); called by whole warps.
-__device__ __forceinline__ SeqBlock find_time_block(const Args& a, int shift, int64_t slot) {
-    const int lane = threadIdx.x & 31;
-    SlotSearch f = {0, a.N, true};
-    while (f.n > 1) {
-        const int32_t i = f.lo + lane * f.step();
-        const bool live = lane * f.step() < f.n;
-        const int64_t v = live ? (cu_load(a.cu, a.cu64, i) >> shift) + i : 0;
-        const unsigned here = __ballot_sync(0xffffffffu, live && v <= slot);
-        f.narrow(here, here);
-    }
+__device__ __forceinline__ SeqBlock time_block(const Args& a, int shift, int32_t seq, int64_t s0, int64_t s1, int64_t c) {
     SeqBlock b;
     b.seq = -1;
     b.start = b.count = b.c = b.len = b.first = 0;
-    const int64_t s0 = cu_load(a.cu, a.cu64, f.lo), s1 = cu_load(a.cu, a.cu64, f.lo + 1);
-    if (s0 < 0 || s1 < s0 || s1 > a.T) return b;
-    const int64_t c = slot - ((s0 >> shift) + f.lo);
-    if (c < 0 || (c > 0 && (c << shift) >= s1 - s0)) return b;
-    b.seq = f.lo;
+    if (s0 < 0 || s1 < s0 || s1 > a.T || c < 0 || (c > 0 && (c << shift) >= s1 - s0)) return b;
+    b.seq = seq;
     b.c = static_cast<int32_t>(c);
     b.first = static_cast<int32_t>(s0);
     b.len = static_cast<int32_t>(s1 - s0);
     b.start = static_cast<int32_t>(s0 + (c << shift));
     b.count = static_cast<int32_t>(min(s1 - b.start, int64_t(1) << shift));
     return b;
+}
+// The last sequence i whose number (cu[i] >> shift) + i kOwn is at or before `at`; called by whole warps.
+template <int kOwn>
+__device__ __forceinline__ int32_t find_sequence(const Args& a, int shift, int64_t at) {
+    const int lane = threadIdx.x & 31;
+    SlotSearch f = {0, a.N, true};
+    while (f.n > 1) {
+        const int32_t i = f.lo + lane * f.step();
+        const bool live = lane * f.step() < f.n;
+        const int64_t v = live ? (cu_load(a.cu, a.cu64, i) >> shift) + i * kOwn : 0;
+        const unsigned here = __ballot_sync(0xffffffffu, live && v <= at);
+        f.narrow(here, here);
+    }
+    return f.lo;
+}
+__device__ __forceinline__ SeqBlock find_slot(const Args& a, int shift, int64_t slot) {
+    const int32_t i = find_sequence<1>(a, shift, slot);
+    const int64_t s0 = cu_load(a.cu, a.cu64, i), s1 = cu_load(a.cu, a.cu64, i + 1);
+    return time_block(a, shift, i, s0, s1, slot - ((s0 >> shift) + i));
+}
+__device__ __forceinline__ SeqBlock find_launched(const Args& a, int shift, int64_t n) {
+    const bool first = n < a.N;
+    const int32_t i = first ? static_cast<int32_t>(n) : find_sequence<0>(a, shift, n - a.N);
+    const int64_t s0 = cu_load(a.cu, a.cu64, i), s1 = cu_load(a.cu, a.cu64, i + 1);
+    return time_block(a, shift, i, s0, s1, first ? 0 : n - a.N - (s0 >> shift) + 1);
+}
+__device__ __forceinline__ int64_t launched_row(const Args& a, int shift, int64_t seq, int64_t first, int64_t c) {
+    return c == 0 ? seq : a.N + (first >> shift) + c - 1;
 }
 __device__ __forceinline__ int64_t this_slot() { return blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z; }
 
@@ -103,9 +122,19 @@ __device__ __forceinline__ int64_t state_row(const Args& a, int32_t seq) {
 }
 
 // ---------------------------------------------------------------- steps
-__device__ __forceinline__ float step_of(float raw, int softplus) {
-    return !softplus || raw > 20.f ? raw : log1pf(expf(raw));  // above 20 log1p(e^x) is x in 32 bits
+// softplus(v) = max(v, 0) + log1p(t), t = e^-|v| in (0, 1]; log1p(t) = 2 atanh(s), s = t / (2 + t) up to 1/3, where a
+// polynomial of degree 4 in s^2 (fitted at Chebyshev nodes) is off by 4e-9: no difference of near values anywhere, and two
+// MUFU operations and some ten others where expf and log1pf take forty.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    const float2 l = mul2(make_float2(fabsf(v.x), fabsf(v.y)), both(-kLog2e)), t = make_float2(ex2(l.x), ex2(l.y));
+    const float2 d = add2(t, both(2.f)), s = mul2(t, make_float2(rcp_fast(d.x), rcp_fast(d.y))), w = mul2(s, s);
+    float2 p = fma2(w, both(0.28174657f), both(0.27961419f));
+    p = fma2(w, p, both(0.40024854f));
+    p = fma2(w, p, both(0.66666316f));
+    p = fma2(w, p, both(2.f));
+    return fma2(s, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float2 steps_of(float2 raw, int softplus) { return softplus ? softplus2(raw) : raw; }
 
 // ---------------------------------------------------------------- channels of a tile, lanes of a thread
 struct Tile {
@@ -200,6 +229,23 @@ __device__ __forceinline__ void zero(float2 (&v)[kPairs][4]) {
     for (int p = 0; p < kPairs; ++p)
 #pragma unroll
         for (int s = 0; s < 4; ++s) v[p][s] = both(0.f);
+}
+
+// kS consecutive states of a lane's channel, as pairs.
+template <int kS>
+__device__ __forceinline__ void load_lane_states(float2 (&v)[kS / 2], const void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
+#pragma unroll
+    for (int k = 0; k < kS; k += 4) {
+        const float4 f = load_states(base, row, a, d, s + k, live, is_bf16);
+        v[k / 2] = lo(f);
+        v[k / 2 + 1] = hi(f);
+    }
+}
+template <int kS>
+__device__ __forceinline__ void store_lane_states(const float2 (&v)[kS / 2], void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
+#pragma unroll
+    for (int k = 0; k < kS; k += 4)
+        store_states(base, row, a, d, s + k, live, is_bf16, make_float4(v[k / 2].x, v[k / 2].y, v[k / 2 + 1].x, v[k / 2 + 1].y));
 }
 
 // Sums kValues values over the lanes that differ in the bits from kBit up to kEnd.  While there are several values each

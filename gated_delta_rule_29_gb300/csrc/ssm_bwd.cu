@@ -33,7 +33,8 @@ __device__ __forceinline__ float4 raw_steps(const Args& a, int64_t tok, int ch, 
     return make_float4(r.x + bias[0], r.y + bias[1], r.z + bias[2], r.w + bias[3]);
 }
 __device__ __forceinline__ float4 steps_of(float4 r, int softplus) {
-    return make_float4(step_of(r.x, softplus), step_of(r.y, softplus), step_of(r.z, softplus), step_of(r.w, softplus));
+    const float2 a = ssm::steps_of(lo(r), softplus), b = ssm::steps_of(hi(r), softplus);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ void load_channels(float (&v)[4], const float* p, int ch, int n) {
 #pragma unroll
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(32) ssm_chunk_gradient_kernel(const Args a) {
     const int lane = threadIdx.x, q = lane % Q, cg = lane / Q;
     const int64_t slot = this_slot();
     if (slot >= slots_for(a.T, a.N, kShift)) return;
-    const SeqBlock blk = find_time_block(a, kShift, slot);
+    const SeqBlock blk = find_slot(a, kShift, slot);
     if (blk.seq < 0 || blk.count == 0) return;
     const Tile tile = tile_of(a, blockIdx.x, kW);
     const int d0 = tile.ch + 4 * cg, end = tile.ch + tile.n, s0 = 4 * q;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_chunk_kernel(const Args a) {
 
     const int64_t slots = slots_for(a.T, a.N, kShift);
     for (int64_t slot = part; slot < slots; slot += a.parts) {
-        const SeqBlock blk = find_time_block(a, kShift, slot);
+        const SeqBlock blk = find_slot(a, kShift, slot);
         if (blk.seq < 0 || blk.count == 0) continue;  // the same for the whole CTA
         const int n = blk.count;
         __syncthreads();  // the last chunk's sums have been read

@@ -1,8 +1,10 @@
 // ssm_fwd.cu -- the selective scan's forward (ssm.cuh has the formulas).
 //
-// A warp takes 128 / Q channels of one time block and walks its tokens, some at a time through shared memory: rows by
-// cp.async one stage ahead, then the steps and dt x in 32 bits, then the tokens, whose sums over the states replace
-// dt x, then the skip, the gate and the store.
+// A warp takes 32 / Q channels of one time block and walks its tokens, 32 at a time through shared memory, the next ones
+// on their way meanwhile (cp.async).  A lane has one channel with kS of its states, so that B and C are the same address for
+// 32 or 16 neighbouring lanes (two cycles for 16 bytes a lane, measured, where addresses that alternate between lanes
+// take four), pairs of states come as they lie, and up to 16 states no sum goes over lanes.  What two tokens' scans need
+// beside B and C is formed while the two before are scanned.
 //
 // Time is split where the channels of all sequences are too few to fill the GPU: blocks of 2^shift tokens from each sequence's start.
 // A first launch leaves what each block but the last makes of a zero state, and its steps' sum; a second one goes along
@@ -22,174 +24,209 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-template <typename X, int Q>
+constexpr int kTok = 32;  // tokens of a stage; divides kSave
+
+template <typename X, int kS, int Q>
 struct Stage {
-    static constexpr int kW = 128 / Q;                                       // channels of a warp
-    static constexpr int kTok = Q == 1 ? 8 : Q == 2 || Q == 16 ? 16 : 32;    // tokens of a stage; divides kSave
-    static constexpr int kVec = 16 / static_cast<int>(sizeof(X));
-    static constexpr int kSB = 4 * Q > kVec ? 4 * Q : kVec;                  // states, padded to a wide access
-    X rows[2][3][kTok * kW];    // x, dt, z
-    X states[2][2][kTok * kSB]; // B, C
-    float dt[kTok * kW], u[kTok * kW];
-    float b[kTok * 4 * Q], c[kTok * 4 * Q];
+    static constexpr int kW = 32 / Q, kSP = kS * Q;  // channels of a warp, states of a channel
+    X rows[2][3][kTok * kW];                         // x, dt, z
+    X states[2][2][kTok * kSP];                      // B, C
+    float wide[sizeof(X) == 4 ? 1 : 2][sizeof(X) == 4 ? 4 : kTok * kSP];  // B and C in 32 bits, where they are not so already
 };
 
-// Rows [0, rows) of n elements into shared memory, padded with zeros to kWidth.
+// A lane's part of stages of kTok rows of n elements, padded with zeros to kWidth in shared memory: the same columns of
+// every kRows-th row.
 template <typename X, int kWidth>
-__device__ __forceinline__ void stage_rows(X* s, const void* base, int64_t at, int64_t stride, int rows, int n, int vec) {
-    constexpr int kVec = 16 / static_cast<int>(sizeof(X)), kVecs = kWidth / kVec;
-    const X* g = static_cast<const X*>(base) + at;
-    for (int i = threadIdx.x & 31; i < rows * kVecs; i += 32) {
-        const int r = i / kVecs, c = i % kVecs * kVec;
-        const X* p = g + r * stride + c;
-        if (vec && c + kVec <= n) cp_async16(s + r * kWidth + c, p);
-        else
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) s[r * kWidth + c + e] = c + e < n ? p[e] : from_f<X>(0.f);
+struct Rows {
+    static constexpr int kVec = 16 / static_cast<int>(sizeof(X)), kVecs = kWidth / kVec, kRows = 32 / kVecs;
+    const X* from;  // of the next stage
+    int64_t step;   // kRows rows
+    int n;          // elements from this lane's column on
+    bool wide;
+    __device__ __forceinline__ Rows(const void* base, int64_t at, int64_t stride, int elements, int vec) {
+        const int lane = threadIdx.x & 31, c = lane % kVecs * kVec;
+        n = elements - c;
+        wide = vec && n >= kVec;
+        from = static_cast<const X*>(base) + at + lane / kVecs * stride + c;
+        step = kRows * stride;
     }
-}
+    __device__ __forceinline__ void stage(X* to, int rows) {
+        const int lane = threadIdx.x & 31;
+        to += lane / kVecs * kWidth + lane % kVecs * kVec;
+#pragma unroll
+        for (int j = 0; j < kTok / kRows; ++j, to += kRows * kWidth, from += step) {
+            if (lane / kVecs + j * kRows >= rows) continue;
+            if (wide) cp_async16(to, from);
+            else
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) to[e] = e < n ? from[e] : from_f<X>(0.f);
+        }
+    }
+};
 
-template <typename X, int Q, bool kLocal>
+template <typename X, int kS, int Q, bool kLocal, bool kGate>
 __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
-    typedef Stage<X, Q> Sm;
-    constexpr int kW = Sm::kW, kTok = Sm::kTok, kSP = 4 * Q;
+    typedef Stage<X, kS, Q> Sm;
+    constexpr int kW = Sm::kW, kSP = Sm::kSP, kPairs = kS / 2;
     __shared__ __align__(16) Sm sm;
-    const int lane = threadIdx.x, q = lane % Q, cg = lane / Q;
+    const int lane = threadIdx.x, q = lane / kW, ch = lane % kW;
     const int64_t slot = this_slot();
     if (slot >= slots_for(a.T, a.N, a.shift)) return;
     if (!kLocal && blockIdx.x == 0 && lane == 0 && slot < a.N) check_cu(a.cu, a.cu64, a.N, a.T, slot, a.status);
-    const SeqBlock blk = find_time_block(a, a.shift, slot);
+    const SeqBlock blk = find_launched(a, a.shift, slot);
     if (blk.seq < 0) return;
     const bool last = blk.start + blk.count == blk.first + blk.len;
     if (kLocal && last) return;  // what the last block leaves, nobody takes over
     const Tile tile = tile_of(a, blockIdx.x, kW);
-    const int d0 = tile.ch + 4 * cg, end = tile.ch + tile.n, s0 = 4 * q;
+    const int d = tile.ch + ch, s0 = kS * q;
+    const bool live = ch < tile.n;
 
-    float2 A2[2][4], h[2][4];
-    load_thread_states(A2, a.A, 0, a, d0, end, s0, 0);
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) A2[p][s] = mul2(A2[p][s], both(kLog2e));
-    zero(h);
-    int64_t row0 = -1;
-    if (!kLocal) {
-        const bool split = blk.len > (int64_t(1) << a.shift);
-        if (a.s0) {
-            row0 = state_row(a, blk.seq);
-            if (row0 < 0) return;
-        }
-        if (split) load_thread_states(h, a.table, slot, a, d0, end, s0, 0);
-        else if (a.s0) load_thread_states(h, a.s0, row0, a, d0, end, s0, a.s0_bf16);
-    }
-    // the channels that this lane prepares and finishes: four of them, of every kRows-th row
-    constexpr int kVecs = kW / 4, kRows = 32 / kVecs;
-    const int c4 = lane % kVecs * 4, r4 = lane / kVecs;
-    float bias[4], skip[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool live = c4 + i < tile.n;
-        bias[i] = live && a.bias ? a.bias[tile.ch + c4 + i] : 0.f;
-        skip[i] = !kLocal && live && a.skip ? a.skip[tile.ch + c4 + i] : 0.f;
-    }
-    float2 sum[2] = {both(0.f), both(0.f)};
-
-    auto load = [&](int buf, int t) {
-        const int n = min(kTok, blk.count - t);
-        const int64_t tok = blk.start + t;
-        if (n > 0) {
-            stage_rows<X, kW>(sm.rows[buf][0], a.x, tok * a.x_st + tile.ch, a.x_st, n, tile.n, a.vec);
-            stage_rows<X, kW>(sm.rows[buf][1], a.dt, tok * a.dt_st + tile.ch, a.dt_st, n, tile.n, a.vec);
-            if (!kLocal && a.z) stage_rows<X, kW>(sm.rows[buf][2], a.z, tok * a.z_st + tile.ch, a.z_st, n, tile.n, a.vec);
-            stage_rows<X, Sm::kSB>(sm.states[buf][0], a.b, tok * a.b_st + tile.group * a.b_sg, a.b_st, n, a.S, a.vec);
-            if (!kLocal) stage_rows<X, Sm::kSB>(sm.states[buf][1], a.c, tok * a.c_st + tile.group * a.c_sg, a.c_st, n, a.S, a.vec);
-        }
+    Rows<X, kW> x_rows(a.x, blk.start * a.x_st + tile.ch, a.x_st, tile.n, a.vec), dt_rows(a.dt, blk.start * a.dt_st + tile.ch, a.dt_st, tile.n, a.vec),
+        z_rows(a.z, blk.start * a.z_st + tile.ch, a.z_st, tile.n, a.vec);
+    Rows<X, kSP> b_rows(a.b, blk.start * a.b_st + tile.group * a.b_sg, a.b_st, a.S, a.vec), c_rows(a.c, blk.start * a.c_st + tile.group * a.c_sg, a.c_st, a.S, a.vec);
+    auto load = [&](int buf, int rows) {
+        x_rows.stage(sm.rows[buf][0], rows);
+        dt_rows.stage(sm.rows[buf][1], rows);
+        if (kGate) z_rows.stage(sm.rows[buf][2], rows);
+        b_rows.stage(sm.states[buf][0], rows);
+        if (!kLocal) c_rows.stage(sm.states[buf][1], rows);
         cp_async_commit();
     };
-    load(0, 0);
+    load(0, blk.count);
+
+    float2 A2[kPairs], h[kPairs];
+    load_lane_states<kS>(A2, a.A, 0, a, d, s0, live, 0);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        A2[k] = mul2(A2[k], both(kLog2e));
+        h[k] = both(0.f);
+    }
+    int64_t row0 = -1;
+    if (!kLocal) {
+        if (a.s0) {
+            row0 = state_row(a, blk.seq);
+            if (row0 < 0) {
+                cp_async_wait<0>();
+                return;
+            }
+        }
+        if (blk.len > int64_t(1) << a.shift) load_lane_states<kS>(h, a.table, slot, a, d, s0, live, 0);
+        else if (a.s0) load_lane_states<kS>(h, a.s0, row0, a, d, s0, live, a.s0_bf16);
+    }
+    const float bias = live && a.bias ? a.bias[d] : 0.f, skip = !kLocal && live && a.skip ? a.skip[d] : 0.f;
+    const bool stores = live && q == 0 && a.y;
+    float sum = 0.f;
+    X* out = kLocal ? nullptr : static_cast<X*>(a.y) + blk.start * a.y_st + d;
+
     int buf = 0;
     for (int t0 = 0; t0 < blk.count; t0 += kTok, buf ^= 1) {
-        load(buf ^ 1, t0 + kTok);
+        load(buf ^ 1, blk.count - t0 - kTok);
         cp_async_wait<1>();
         __syncwarp();
         const int n = min(kTok, blk.count - t0);
-        for (int r = r4; r < n; r += kRows) {
-            const float4 x = load4<X>(sm.rows[buf][0], r * kW + c4, 4, 1), raw = load4<X>(sm.rows[buf][1], r * kW + c4, 4, 1);
-            const float4 dt = make_float4(step_of(raw.x + bias[0], a.softplus), step_of(raw.y + bias[1], a.softplus),
-                                          step_of(raw.z + bias[2], a.softplus), step_of(raw.w + bias[3], a.softplus));
-            *reinterpret_cast<float4*>(sm.dt + r * kW + c4) = dt;
-            *reinterpret_cast<float4*>(sm.u + r * kW + c4) = make_float4(dt.x * x.x, dt.y * x.y, dt.z * x.z, dt.w * x.w);
-        }
-        for (int i = lane; i < n * kSP; i += 32) {
-            const int r = i / kSP, s = i % kSP;
-            sm.b[i] = to_f(sm.states[buf][0][r * Sm::kSB + s]);
-            if (!kLocal) sm.c[i] = to_f(sm.states[buf][1][r * Sm::kSB + s]);
-        }
-        __syncwarp();
-        if (!kLocal && a.ckpt && t0 % kSave == 0) {
-            const int64_t at = (static_cast<int64_t>(blk.first) / kSave) + blk.seq + (blk.start - blk.first + t0) / kSave;
-            store_thread_states(h, a.ckpt, at, a, d0, end, s0, 0);
-        }
-#pragma unroll 2
-        for (int r = 0; r < n; ++r) {
-            const float4 dt = *reinterpret_cast<const float4*>(sm.dt + r * kW + 4 * cg), u = *reinterpret_cast<const float4*>(sm.u + r * kW + 4 * cg);
-            const float4 b = *reinterpret_cast<const float4*>(sm.b + r * kSP + s0);
-            const float bs[4] = {b.x, b.y, b.z, b.w};
-            float4 c;
-            if (!kLocal) c = *reinterpret_cast<const float4*>(sm.c + r * kSP + s0);
-            const float cs[4] = {c.x, c.y, c.z, c.w};
-            float v[4];
+        const float *bs, *cs;
+        if constexpr (sizeof(X) == 4) {
+            bs = sm.states[buf][0];
+            cs = sm.states[buf][1];
+        } else {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float2 dp = p ? hi(dt) : lo(dt), up = p ? hi(u) : lo(u);
-                float2 y;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float2 l = fma2(dp, A2[p][s], both(kEx2Low));
-                    h[p][s] = fma2(make_float2(ex2(l.x), ex2(l.y)), h[p][s], mul2(up, both(bs[s])));
-                    if (!kLocal) y = s ? fma2(h[p][s], both(cs[s]), y) : mul2(h[p][s], both(cs[s]));
-                }
-                if (kLocal) sum[p] = add2(sum[p], dp);
-                v[2 * p] = y.x;
-                v[2 * p + 1] = y.y;
-            }
-            if (!kLocal) {
-                // every lane has read its u before it takes part in the sum that one of them writes over it
-                const int at = spread_sum<4, 1, Q>(v);
-                if (Q <= 4 || q < 4) {
-#pragma unroll
-                    for (int i = 0; i < (Q >= 4 ? 1 : 4 / Q); ++i) sm.u[r * kW + 4 * cg + at + i] = v[i];
-                }
-            }
-        }
-        __syncwarp();
-        if (!kLocal && a.y) {
-            for (int r = r4; r < n; r += kRows) {
-                const float4 p = *reinterpret_cast<const float4*>(sm.u + r * kW + c4), x = load4<X>(sm.rows[buf][0], r * kW + c4, 4, 1);
-                float2 y0 = fma2(make_float2(skip[0], skip[1]), lo(x), lo(p)), y1 = fma2(make_float2(skip[2], skip[3]), hi(x), hi(p));
-                if (a.z) {
-                    const float4 z = load4<X>(sm.rows[buf][2], r * kW + c4, 4, 1);
-                    y0 = mul2(y0, act_fwd2<LA_ACT_SILU>(lo(z)));
-                    y1 = mul2(y1, act_fwd2<LA_ACT_SILU>(hi(z)));
-                }
-                store4<X>(a.y, (blk.start + t0 + r) * a.y_st + tile.ch + c4, tile.n - c4, a.vec, make_float4(y0.x, y0.y, y1.x, y1.y));
+            for (int j = 0; j < kTok * kSP / 128; ++j) {  // rows beyond n hold what they held before
+                const int i = 4 * (lane + 32 * j);
+                *reinterpret_cast<float4*>(sm.wide[0] + i) = load4<X>(sm.states[buf][0], i, 4, 1);
+                if (!kLocal) *reinterpret_cast<float4*>(sm.wide[1] + i) = load4<X>(sm.states[buf][1], i, 4, 1);
             }
             __syncwarp();
+            bs = sm.wide[0];
+            cs = sm.wide[1];
         }
+        bs += s0;
+        cs += s0;
+        if (!kLocal && a.ckpt && t0 % kSave == 0)
+            store_lane_states<kS>(h, a.ckpt, static_cast<int64_t>(blk.first) / kSave + blk.seq + (blk.start - blk.first + t0) / kSave, a, d, s0, live, 0);
+
+        const X *xs = sm.rows[buf][0] + ch, *ds = sm.rows[buf][1] + ch, *zs = sm.rows[buf][2] + ch;
+        struct Pair {  // two tokens' steps, dt x, skip x and gates
+            float2 dt, u, rest, gate;
+        };
+        // no branch within, so that the latency of its chain (some 150 cycles) is filled with the scans beside it
+        auto prepare = [&](int r) {
+            Pair t;
+            const float2 x = make_float2(to_f(xs[r * kW]), to_f(xs[r * kW + kW])), raw = add2(make_float2(to_f(ds[r * kW]), to_f(ds[r * kW + kW])), both(bias));
+            const float2 sp = softplus2(raw);
+            t.dt = make_float2(a.softplus ? sp.x : raw.x, a.softplus ? sp.y : raw.y);
+            t.u = mul2(t.dt, x);
+            if (!kLocal) t.rest = mul2(both(skip), x);
+            if (kGate) t.gate = act_fwd2<LA_ACT_SILU>(make_float2(to_f(zs[r * kW]), to_f(zs[r * kW + kW])));
+            return t;
+        };
+        // one token; returns this lane's part of sum_s C h
+        auto token = [&](float dt, float u, int r) {
+            const float2 d2 = both(dt), u2 = both(u);
+            float2 y0 = both(0.f), y1 = both(0.f);
+#pragma unroll
+            for (int k = 0; k < kPairs; k += 2) {
+                const float4 b = *reinterpret_cast<const float4*>(bs + r * kSP + 2 * k);
+                const float2 l0 = fma2(d2, A2[k], both(kEx2Low)), l1 = fma2(d2, A2[k + 1], both(kEx2Low));
+                h[k] = fma2(make_float2(ex2(l0.x), ex2(l0.y)), h[k], mul2(u2, lo(b)));
+                h[k + 1] = fma2(make_float2(ex2(l1.x), ex2(l1.y)), h[k + 1], mul2(u2, hi(b)));
+                if (!kLocal) {
+                    const float4 c = *reinterpret_cast<const float4*>(cs + r * kSP + 2 * k);
+                    y0 = k ? fma2(h[k], lo(c), y0) : mul2(h[k], lo(c));
+                    y1 = k ? fma2(h[k + 1], hi(c), y1) : mul2(h[k + 1], hi(c));
+                }
+            }
+            y0 = add2(y0, y1);
+            return y0.x + y0.y;
+        };
+        auto finish = [&](const Pair& t, float2 p) {
+#pragma unroll
+            for (int off = kW; off < 32; off *= 2) {
+                p.x += __shfl_xor_sync(0xffffffffu, p.x, off);
+                p.y += __shfl_xor_sync(0xffffffffu, p.y, off);
+            }
+            p = add2(p, t.rest);
+            return kGate ? mul2(p, t.gate) : p;
+        };
+        // rows beyond n are prepared too, from whatever lies there, and not used
+        Pair now = prepare(0);
+        int r = 0;
+#pragma unroll 2
+        for (; r + 1 < n; r += 2) {
+            const Pair next = prepare((r + 2) % kTok);
+            float2 p;
+            p.x = token(now.dt.x, now.u.x, r);
+            p.y = token(now.dt.y, now.u.y, r + 1);
+            if (kLocal) {
+                sum += now.dt.x + now.dt.y;
+            } else {
+                p = finish(now, p);
+                if (stores) {
+                    out[0] = from_f<X>(p.x);
+                    out[a.y_st] = from_f<X>(p.y);
+                }
+                out += 2 * a.y_st;
+            }
+            now = next;
+        }
+        if (r < n) {
+            const float p = token(now.dt.x, now.u.x, r);
+            if (kLocal) {
+                sum += now.dt.x;
+            } else {
+                const float2 y = finish(now, both(p));
+                if (stores) out[0] = from_f<X>(y.x);
+            }
+        }
+        __syncwarp();
     }
     if (kLocal) {
-        store_thread_states(h, a.table, slot, a, d0, end, s0, 0);
-        if (q == 0) {
-            const float v[4] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (d0 + i < end) a.sums[slot * a.D + d0 + i] = v[i];
-        }
+        store_lane_states<kS>(h, a.table, slot, a, d, s0, live, 0);
+        if (live && q == 0) a.sums[slot * a.D + d] = sum;
         return;
     }
     if (!last) return;
-    if (a.idx) store_thread_states(h, const_cast<void*>(a.s0), row0, a, d0, end, s0, a.s0_bf16);
-    else if (a.fin) store_thread_states(h, a.fin, blk.seq, a, d0, end, s0, 0);
+    if (a.idx) store_lane_states<kS>(h, const_cast<void*>(a.s0), row0, a, d, s0, live, a.s0_bf16);
+    else if (a.fin) store_lane_states<kS>(h, a.fin, blk.seq, a, d, s0, live, 0);
 }
 
 // Along each split sequence: what its blocks make of nothing becomes what enters them.
@@ -199,7 +236,7 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(const Args a) {
     if (i >= a.N || e >= DS) return;
     const int64_t t0 = cu_load(a.cu, a.cu64, i), t1 = cu_load(a.cu, a.cu64, i + 1);
     if (t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 <= (int64_t(1) << a.shift)) return;
-    const int64_t blocks = (t1 - t0 - 1 >> a.shift) + 1, slot = (t0 >> a.shift) + i;
+    const int64_t blocks = (t1 - t0 - 1 >> a.shift) + 1;
     float st = 0.f;
     if (a.s0) {
         const int64_t row = state_row(a, static_cast<int32_t>(i));
@@ -214,38 +251,46 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(const Args a) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const bool live = c + k + 1 < blocks;  // the last block has left nothing
-            loc[k] = live ? a.table[(slot + c + k) * DS + e] : 0.f;
-            sum[k] = live ? a.sums[(slot + c + k) * a.D + d] : 0.f;
+            const int64_t row = launched_row(a, a.shift, i, t0, c + k);
+            loc[k] = live ? a.table[row * DS + e] : 0.f;
+            sum[k] = live ? a.sums[row * a.D + d] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (c + k < blocks) {
-                a.table[(slot + c + k) * DS + e] = st;
+                a.table[launched_row(a, a.shift, i, t0, c + k) * DS + e] = st;
                 st = fmaf(ex2(A2 * sum[k]), st, loc[k]);
             }
     }
 }
 
-struct Scan {
-    template <typename X, int Q>
-    static la_status run(Args& a, cudaStream_t s) {
-        constexpr int kW = Stage<X, Q>::kW;
-        a.tiles_pg = (a.Dg + kW - 1) / kW;
-        const int64_t slots = slots_for(a.T, a.N, a.shift);
-        const dim3 grid = slot_grid(a.tiles_pg * a.G, slots);
-        if (a.T > (int64_t(1) << a.shift)) {
-            ssm_scan_kernel<X, Q, true><<<grid, 32, 0, s>>>(a);
-            const unsigned bx = static_cast<unsigned>((static_cast<int64_t>(a.D) * a.S + 127) / 128);
-            ssm_join_kernel<<<slot_grid(static_cast<int>(bx), a.N), 128, 0, s>>>(a);
-        }
-        ssm_scan_kernel<X, Q, false><<<grid, 32, 0, s>>>(a);
-        return launched();
+template <typename X, int kS, int Q>
+la_status scan(Args& a, cudaStream_t s) {
+    constexpr int kW = Stage<X, kS, Q>::kW;
+    a.tiles_pg = (a.Dg + kW - 1) / kW;
+    const dim3 grid = slot_grid(a.tiles_pg * a.G, slots_for(a.T, a.N, a.shift));
+    if (a.T > (int64_t(1) << a.shift)) {
+        ssm_scan_kernel<X, kS, Q, true, false><<<grid, 32, 0, s>>>(a);
+        const unsigned bx = static_cast<unsigned>((static_cast<int64_t>(a.D) * a.S + 127) / 128);
+        ssm_join_kernel<<<slot_grid(static_cast<int>(bx), a.N), 128, 0, s>>>(a);
     }
-};
+    if (a.z) ssm_scan_kernel<X, kS, Q, false, true><<<grid, 32, 0, s>>>(a);
+    else ssm_scan_kernel<X, kS, Q, false, false><<<grid, 32, 0, s>>>(a);
+    return launched();
+}
+// Channels of a warp.
+int scan_width(int S) { return S <= 16 ? 32 : S <= 32 ? 16 : 8; }
+template <typename X>
+la_status by_scan(Args& a, cudaStream_t s) {
+    if (a.S <= 8) return scan<X, 8, 1>(a, s);
+    if (a.S <= 16) return scan<X, 16, 1>(a, s);
+    if (a.S <= 32) return scan<X, 16, 2>(a, s);
+    return scan<X, 16, 4>(a, s);
+}
 
 }  // namespace
 
-// Tokens of a time block: one warp takes a block of 128 / Q channels, and kFill of them fill an SM.
+// Tokens of a time block: a warp takes a block of scan_width channels, and kFill of them fill an SM.
 int fwd_shift(int64_t T, int D, int S, int G, int time_block) {
     int shift = 6;
     if (time_block > 0) {
@@ -253,12 +298,12 @@ int fwd_shift(int64_t T, int D, int S, int G, int time_block) {
         return shift;
     }
     constexpr int kFill = 8;
-    const int64_t width = 128 / lanes_for(S), tiles = (D / G + width - 1) / width * G;
+    const int64_t width = scan_width(S), tiles = (D / G + width - 1) / width * G;
     while (shift < 30 && (T * tiles >> shift) > kSms * kFill) ++shift;
     return shift;
 }
 
-la_status run_fwd(Args a, int32_t dtype, cudaStream_t s) { return by_shape<Scan>(dtype, a.S, a, s); }
+la_status run_fwd(Args a, int32_t dtype, cudaStream_t s) { return dtype == LA_DTYPE_BF16 ? by_scan<bf16>(a, s) : by_scan<float>(a, s); }
 
 }  // namespace ssm
 }  // namespace la
