@@ -86,9 +86,9 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     (rates, <= 0 for states that decay), skip, dt_bias [D] are fp32.  dt_t is dt + dt_bias, or softplus of that with
     dt_softplus.
 
-    output_checkpoints keeps the fp32 state entering every 32 tokens for ssm_bwd.  state_indices ([N] int32):
+    output_checkpoints keeps the fp32 state entering every 16 tokens for ssm_bwd.  state_indices ([N] int32):
     initial_state is then a pool [P, D, S] and each sequence's end state is written back to its slot.  time_block (0, or a
-    power of two from 64 on): sequences longer than this are split along time; 0 chooses by T, D, S and the groups, a
+    power of two from 64 on): sequences longer than two such blocks are split along time; 0 chooses by T, D, S and the groups, a
     given one makes a sequence's bits independent of the batch around it."""
     p = B.SsmFwdParams()
     T, D, S = _ssm_inputs(p, x, dt, a, b, c, skip, z, dt_bias, dt_softplus, "_t")
@@ -323,7 +323,7 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.
                    initial_state: Optional[torch.Tensor] = None, save_checkpoints: bool = True
                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable ssm_fwd: returns (y, final_state); gradients flow to x, dt, a, b, c, skip, z, dt_bias and
-    initial_state.  save_checkpoints keeps the state entering every 32 tokens (D * S * 4 bytes each) for the backward;
+    initial_state.  save_checkpoints keeps the state entering every 16 tokens (D * S * 4 bytes each) for the backward;
     without them it recomputes them."""
     return _SelectiveScan.apply(x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints)
 

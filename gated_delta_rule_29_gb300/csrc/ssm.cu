@@ -50,6 +50,15 @@ struct Decode {
     }
 };
 
+template <typename X>
+la_status by_states(Args& a, cudaStream_t s) {
+    if (a.S <= 4) return Decode::run<X, 1>(a, s);
+    if (a.S <= 8) return Decode::run<X, 2>(a, s);
+    if (a.S <= 16) return Decode::run<X, 4>(a, s);
+    if (a.S <= 32) return Decode::run<X, 8>(a, s);
+    return Decode::run<X, 16>(a, s);
+}
+
 size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
 
 bool good_shape(int32_t D, int32_t S, int32_t G) { return D > 0 && S > 0 && G > 0 && D % G == 0; }
@@ -108,7 +117,7 @@ bool good_time_block(int32_t b) { return b == 0 || (b >= 64 && (b & (b - 1)) == 
 
 // The forward's workspace: what enters each time block, and the steps' sums; nothing where no sequence can have two.
 size_t table_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int shift) {
-    if (T <= (int64_t(1) << shift)) return 0;
+    if (!split(T, shift)) return 0;
     const size_t slots = static_cast<size_t>(slots_for(T, N, shift));
     return round_up(slots * D * S * 4) + round_up(slots * D * 4);
 }
@@ -132,9 +141,9 @@ size_t la_ssm_fwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, in
 
 size_t la_ssm_bwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int32_t G, int32_t checkpoints_given) {
     if (T < 0 || N < 0 || !good_shape(D, S, G) || S > kMaxS) return 0;
-    const size_t DS = static_cast<size_t>(D) * S, rows = la_ssm_checkpoint_rows(T, N), parts = bwd_parts(T, N, D, S, G);
+    const size_t DS = static_cast<size_t>(D) * S, rows = la_ssm_checkpoint_rows(T, N), parts = bwd_parts(T, N, D, S, G), blocks = bwd_blocks(T, N);
     const size_t tiles = (D / G + bwd_width(S) - 1) / bwd_width(S);
-    size_t n = round_up(rows * DS * 4) + round_up(rows * D * 4) + round_up(tiles * T * G * 2 * S * 4) + round_up(parts * DS * 4) +
+    size_t n = round_up(blocks * DS * 4) + round_up(blocks * D * 4) + round_up(tiles * T * G * 2 * S * 4) + round_up(parts * DS * 4) +
                round_up(parts * 2 * D * 4);
     if (!checkpoints_given) n += round_up(rows * DS * 4) + la_ssm_fwd_workspace_bytes(T, N, D, S, G, 0);
     return n;
@@ -197,7 +206,7 @@ la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream) {
             wide_rows(a, a.dz, a.dz_st, xd);
     a.svec = a.svec && aligned_to(p->checkpoints, 16);
     a.parts = bwd_parts(a.T, a.N, a.D, a.S, a.G);
-    const size_t DS = static_cast<size_t>(a.D) * a.S, rows = la_ssm_checkpoint_rows(a.T, a.N);
+    const size_t DS = static_cast<size_t>(a.D) * a.S, rows = la_ssm_checkpoint_rows(a.T, a.N), blocks = bwd_blocks(a.T, a.N);
     const size_t tiles = (a.Dg + bwd_width(a.S) - 1) / bwd_width(a.S);
     uint8_t* ws = static_cast<uint8_t*>(p->workspace);
     auto take = [&](size_t bytes) {
@@ -205,8 +214,8 @@ la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream) {
         ws += round_up(bytes);
         return q;
     };
-    float* table = take(rows * DS * 4);
-    float* sums = take(rows * a.D * 4);
+    float* table = take(blocks * DS * 4);
+    float* sums = take(blocks * a.D * 4);
     a.dbc = take(tiles * a.T * a.G * 2 * a.S * 4);
     a.pA = take(static_cast<size_t>(a.parts) * DS * 4);
     a.pch = take(static_cast<size_t>(a.parts) * 2 * a.D * 4);
@@ -240,7 +249,8 @@ la_status ssm_decode(const la_ssm_decode_params* p, void* stream) {
     a.idx = p->state_indices; a.pool = p->state_pool_size;
     a.y = p->y; a.y_st = p->y_stride_n;
     if (a.N == 0) return LA_OK;
-    return by_shape<Decode>(p->x_dtype, a.S, a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return p->x_dtype == LA_DTYPE_BF16 ? by_states<bf16>(a, s) : by_states<float>(a, s);
 }
 
 }  // extern "C"

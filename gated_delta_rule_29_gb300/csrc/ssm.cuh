@@ -23,7 +23,7 @@ namespace ssm {
 
 using namespace la::mixer;
 
-constexpr int kSave = 32;  // tokens between saved states
+constexpr int kSave = 16;  // tokens between saved states
 constexpr int kMaxS = 64;
 constexpr int kSms = 152;
 
@@ -99,11 +99,18 @@ __device__ __forceinline__ SeqBlock find_slot(const Args& a, int shift, int64_t 
     const int64_t s0 = cu_load(a.cu, a.cu64, i), s1 = cu_load(a.cu, a.cu64, i + 1);
     return time_block(a, shift, i, s0, s1, slot - ((s0 >> shift) + i));
 }
+// Sequences of up to two blocks stay whole.
+LA_HOST_DEVICE bool split(int64_t len, int shift) { return len > int64_t(2) << shift; }
 __device__ __forceinline__ SeqBlock find_launched(const Args& a, int shift, int64_t n) {
     const bool first = n < a.N;
     const int32_t i = first ? static_cast<int32_t>(n) : find_sequence<0>(a, shift, n - a.N);
     const int64_t s0 = cu_load(a.cu, a.cu64, i), s1 = cu_load(a.cu, a.cu64, i + 1);
-    return time_block(a, shift, i, s0, s1, first ? 0 : n - a.N - (s0 >> shift) + 1);
+    SeqBlock b = time_block(a, shift, i, s0, s1, first ? 0 : n - a.N - (s0 >> shift) + 1);
+    if (b.seq >= 0 && !split(b.len, shift)) {
+        if (first) b.count = b.len;
+        else b.seq = -1;
+    }
+    return b;
 }
 __device__ __forceinline__ int64_t launched_row(const Args& a, int shift, int64_t seq, int64_t first, int64_t c) {
     return c == 0 ? seq : a.N + (first >> shift) + c - 1;
@@ -177,6 +184,47 @@ __device__ __forceinline__ void store4(void* base, int64_t at, int n, int vec, f
 }
 __device__ __forceinline__ float2 lo(float4 v) { return make_float2(v.x, v.y); }
 __device__ __forceinline__ float2 hi(float4 v) { return make_float2(v.z, v.w); }
+
+// ---------------------------------------------------------------- rows into shared memory
+__device__ __forceinline__ void cp_async16(void* s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(g) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// A thread's part of stages of kTokens rows of n elements, kPitch apart and padded with zeros to kWidth in shared memory: the
+// same columns of every kRows-th row.
+template <typename X, int kWidth, int kThreads, int kTokens, int kPitch = kWidth>
+struct Rows {
+    static constexpr int kVec = 16 / static_cast<int>(sizeof(X)), kVecs = kWidth / kVec, kRows = kThreads / kVecs;
+    const X* from;  // this thread's column of its first row
+    int64_t stride;
+    int n;          // elements from this thread's column on
+    bool wide;
+    __device__ __forceinline__ Rows(const void* base, int64_t at, int64_t stride_, int elements, int vec) : stride(stride_) {
+        const int c = threadIdx.x % kThreads % kVecs * kVec;
+        n = elements - c;
+        wide = vec && n >= kVec;
+        from = static_cast<const X*>(base) + at + threadIdx.x % kThreads / kVecs * stride + c;
+    }
+    // Rows from t on, of which `rows` are left.
+    __device__ __forceinline__ void stage(X* to, int t, int rows) const {
+        const int i = threadIdx.x % kThreads, r = i / kVecs;
+        to += r * kPitch + i % kVecs * kVec;
+        const X* p = from + t * stride;
+#pragma unroll
+        for (int j = 0; j < (kTokens + kRows - 1) / kRows; ++j, to += kRows * kPitch, p += kRows * stride) {
+            if (r + j * kRows >= min(rows, kTokens)) continue;
+            if (wide) cp_async16(to, p);
+            else
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) to[e] = e < n ? p[e] : from_f<X>(0.f);
+        }
+    }
+};
 
 // Four states of one channel in a [rows, D, S] array; 0 beyond S or where the channel does not exist.
 __device__ __forceinline__ float4 load_states(const void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
@@ -274,28 +322,6 @@ __device__ __forceinline__ int spread_sum(float (&v)[kValues]) {
     }
 }
 
-// Lanes of a channel for S states.
-inline int lanes_for(int S) {
-    int q = 1;
-    while (4 * q < S) q *= 2;
-    return q;
-}
-// Calls F::run<X, Q>(args...) for the operands' type and the states.
-template <typename F, typename X, typename... A>
-la_status by_states(int S, A&&... args) {
-    switch (lanes_for(S)) {
-        case 1: return F::template run<X, 1>(args...);
-        case 2: return F::template run<X, 2>(args...);
-        case 4: return F::template run<X, 4>(args...);
-        case 8: return F::template run<X, 8>(args...);
-        default: return F::template run<X, 16>(args...);
-    }
-}
-template <typename F, typename... A>
-la_status by_shape(int32_t dtype, int S, A&&... args) {
-    return dtype == LA_DTYPE_BF16 ? by_states<F, bf16>(S, args...) : by_states<F, float>(S, args...);
-}
-
 inline dim3 slot_grid(int tiles, int64_t slots) {
     const int64_t y = std::min<int64_t>(slots, 65535);
     return dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(y), static_cast<unsigned>((slots + y - 1) / y));
@@ -305,6 +331,7 @@ int fwd_shift(int64_t T, int D, int S, int G, int time_block);
 la_status run_fwd(Args a, int32_t dtype, cudaStream_t s);
 la_status run_bwd(Args a, int32_t dtype, cudaStream_t s);
 int bwd_width(int S);
+int64_t bwd_blocks(int64_t T, int32_t N);
 int bwd_parts(int64_t T, int32_t N, int D, int S, int G);
 
 }  // namespace ssm

@@ -15,16 +15,7 @@ namespace la {
 namespace ssm {
 namespace {
 
-__device__ __forceinline__ void cp_async16(void* s, const void* g) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(g) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-constexpr int kTok = 32;  // tokens of a stage; divides kSave
+constexpr int kTok = 32;  // tokens of a stage; a multiple of kSave
 
 template <typename X, int kS, int Q>
 struct Stage {
@@ -32,36 +23,6 @@ struct Stage {
     X rows[2][3][kTok * kW];                         // x, dt, z
     X states[2][2][kTok * kSP];                      // B, C
     float wide[sizeof(X) == 4 ? 1 : 2][sizeof(X) == 4 ? 4 : kTok * kSP];  // B and C in 32 bits, where they are not so already
-};
-
-// A lane's part of stages of kTok rows of n elements, padded with zeros to kWidth in shared memory: the same columns of
-// every kRows-th row.
-template <typename X, int kWidth>
-struct Rows {
-    static constexpr int kVec = 16 / static_cast<int>(sizeof(X)), kVecs = kWidth / kVec, kRows = 32 / kVecs;
-    const X* from;  // of the next stage
-    int64_t step;   // kRows rows
-    int n;          // elements from this lane's column on
-    bool wide;
-    __device__ __forceinline__ Rows(const void* base, int64_t at, int64_t stride, int elements, int vec) {
-        const int lane = threadIdx.x & 31, c = lane % kVecs * kVec;
-        n = elements - c;
-        wide = vec && n >= kVec;
-        from = static_cast<const X*>(base) + at + lane / kVecs * stride + c;
-        step = kRows * stride;
-    }
-    __device__ __forceinline__ void stage(X* to, int rows) {
-        const int lane = threadIdx.x & 31;
-        to += lane / kVecs * kWidth + lane % kVecs * kVec;
-#pragma unroll
-        for (int j = 0; j < kTok / kRows; ++j, to += kRows * kWidth, from += step) {
-            if (lane / kVecs + j * kRows >= rows) continue;
-            if (wide) cp_async16(to, from);
-            else
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) to[e] = e < n ? from[e] : from_f<X>(0.f);
-        }
-    }
 };
 
 template <typename X, int kS, int Q, bool kLocal, bool kGate>
@@ -81,18 +42,21 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
     const int d = tile.ch + ch, s0 = kS * q;
     const bool live = ch < tile.n;
 
-    Rows<X, kW> x_rows(a.x, blk.start * a.x_st + tile.ch, a.x_st, tile.n, a.vec), dt_rows(a.dt, blk.start * a.dt_st + tile.ch, a.dt_st, tile.n, a.vec),
+    typedef Rows<X, kW, 32, kTok> RowsOf;
+    typedef Rows<X, kSP, 32, kTok> StatesOf;
+    const RowsOf x_rows(a.x, blk.start * a.x_st + tile.ch, a.x_st, tile.n, a.vec), dt_rows(a.dt, blk.start * a.dt_st + tile.ch, a.dt_st, tile.n, a.vec),
         z_rows(a.z, blk.start * a.z_st + tile.ch, a.z_st, tile.n, a.vec);
-    Rows<X, kSP> b_rows(a.b, blk.start * a.b_st + tile.group * a.b_sg, a.b_st, a.S, a.vec), c_rows(a.c, blk.start * a.c_st + tile.group * a.c_sg, a.c_st, a.S, a.vec);
-    auto load = [&](int buf, int rows) {
-        x_rows.stage(sm.rows[buf][0], rows);
-        dt_rows.stage(sm.rows[buf][1], rows);
-        if (kGate) z_rows.stage(sm.rows[buf][2], rows);
-        b_rows.stage(sm.states[buf][0], rows);
-        if (!kLocal) c_rows.stage(sm.states[buf][1], rows);
+    const StatesOf b_rows(a.b, blk.start * a.b_st + tile.group * a.b_sg, a.b_st, a.S, a.vec), c_rows(a.c, blk.start * a.c_st + tile.group * a.c_sg, a.c_st, a.S, a.vec);
+    auto load = [&](int buf, int t) {
+        const int rows = blk.count - t;
+        x_rows.stage(sm.rows[buf][0], t, rows);
+        dt_rows.stage(sm.rows[buf][1], t, rows);
+        if (kGate) z_rows.stage(sm.rows[buf][2], t, rows);
+        b_rows.stage(sm.states[buf][0], t, rows);
+        if (!kLocal) c_rows.stage(sm.states[buf][1], t, rows);
         cp_async_commit();
     };
-    load(0, blk.count);
+    load(0, 0);
 
     float2 A2[kPairs], h[kPairs];
     load_lane_states<kS>(A2, a.A, 0, a, d, s0, live, 0);
@@ -110,7 +74,7 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
                 return;
             }
         }
-        if (blk.len > int64_t(1) << a.shift) load_lane_states<kS>(h, a.table, slot, a, d, s0, live, 0);
+        if (split(blk.len, a.shift)) load_lane_states<kS>(h, a.table, slot, a, d, s0, live, 0);
         else if (a.s0) load_lane_states<kS>(h, a.s0, row0, a, d, s0, live, a.s0_bf16);
     }
     const float bias = live && a.bias ? a.bias[d] : 0.f, skip = !kLocal && live && a.skip ? a.skip[d] : 0.f;
@@ -120,7 +84,7 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
 
     int buf = 0;
     for (int t0 = 0; t0 < blk.count; t0 += kTok, buf ^= 1) {
-        load(buf ^ 1, blk.count - t0 - kTok);
+        load(buf ^ 1, t0 + kTok);
         cp_async_wait<1>();
         __syncwarp();
         const int n = min(kTok, blk.count - t0);
@@ -141,9 +105,6 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
         }
         bs += s0;
         cs += s0;
-        if (!kLocal && a.ckpt && t0 % kSave == 0)
-            store_lane_states<kS>(h, a.ckpt, static_cast<int64_t>(blk.first) / kSave + blk.seq + (blk.start - blk.first + t0) / kSave, a, d, s0, live, 0);
-
         const X *xs = sm.rows[buf][0] + ch, *ds = sm.rows[buf][1] + ch, *zs = sm.rows[buf][2] + ch;
         struct Pair {  // two tokens' steps, dt x, skip x and gates
             float2 dt, u, rest, gate;
@@ -190,23 +151,27 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
         // rows beyond n are prepared too, from whatever lies there, and not used
         Pair now = prepare(0);
         int r = 0;
+        for (int r0 = 0; r0 < n; r0 += kSave) {
+            if (!kLocal && a.ckpt)
+                store_lane_states<kS>(h, a.ckpt, static_cast<int64_t>(blk.first) / kSave + blk.seq + (blk.start - blk.first + t0 + r0) / kSave, a, d, s0, live, 0);
 #pragma unroll 2
-        for (; r + 1 < n; r += 2) {
-            const Pair next = prepare((r + 2) % kTok);
-            float2 p;
-            p.x = token(now.dt.x, now.u.x, r);
-            p.y = token(now.dt.y, now.u.y, r + 1);
-            if (kLocal) {
-                sum += now.dt.x + now.dt.y;
-            } else {
-                p = finish(now, p);
-                if (stores) {
-                    out[0] = from_f<X>(p.x);
-                    out[a.y_st] = from_f<X>(p.y);
+            for (; r + 1 < min(n, r0 + kSave); r += 2) {
+                const Pair next = prepare((r + 2) % kTok);
+                float2 p;
+                p.x = token(now.dt.x, now.u.x, r);
+                p.y = token(now.dt.y, now.u.y, r + 1);
+                if (kLocal) {
+                    sum += now.dt.x + now.dt.y;
+                } else {
+                    p = finish(now, p);
+                    if (stores) {
+                        out[0] = from_f<X>(p.x);
+                        out[a.y_st] = from_f<X>(p.y);
+                    }
+                    out += 2 * a.y_st;
                 }
-                out += 2 * a.y_st;
+                now = next;
             }
-            now = next;
         }
         if (r < n) {
             const float p = token(now.dt.x, now.u.x, r);
@@ -235,7 +200,7 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(const Args a) {
     const int64_t i = this_slot();
     if (i >= a.N || e >= DS) return;
     const int64_t t0 = cu_load(a.cu, a.cu64, i), t1 = cu_load(a.cu, a.cu64, i + 1);
-    if (t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 <= (int64_t(1) << a.shift)) return;
+    if (t0 < 0 || t1 < t0 || t1 > a.T || !split(t1 - t0, a.shift)) return;
     const int64_t blocks = (t1 - t0 - 1 >> a.shift) + 1;
     float st = 0.f;
     if (a.s0) {
@@ -269,7 +234,7 @@ la_status scan(Args& a, cudaStream_t s) {
     constexpr int kW = Stage<X, kS, Q>::kW;
     a.tiles_pg = (a.Dg + kW - 1) / kW;
     const dim3 grid = slot_grid(a.tiles_pg * a.G, slots_for(a.T, a.N, a.shift));
-    if (a.T > (int64_t(1) << a.shift)) {
+    if (split(a.T, a.shift)) {
         ssm_scan_kernel<X, kS, Q, true, false><<<grid, 32, 0, s>>>(a);
         const unsigned bx = static_cast<unsigned>((static_cast<int64_t>(a.D) * a.S + 127) / 128);
         ssm_join_kernel<<<slot_grid(static_cast<int>(bx), a.N), 128, 0, s>>>(a);

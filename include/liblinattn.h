@@ -858,15 +858,15 @@ typedef struct la_ssm_fwd_params {
  *     p_t  = sum_s c_t[j][s] h_t + skip[d] x_t,     y_t = p_t, or p_t silu(z_t) with z.
  *
  * An empty sequence's final state is its initial state (or zeros).  checkpoints
- * receives the fp32 state entering every 32 tokens of every sequence, for ssm_bwd:
- * chunk c of sequence i is row cu_seqlens[i] / 32 + i + c (rows in between are left
+ * receives the fp32 state entering every 16 tokens of every sequence, for ssm_bwd:
+ * part c of sequence i is row cu_seqlens[i] / 16 + i + c (rows in between are left
  * alone).  y may be x, dt or z itself (same address and stride), and must share no
  * memory with them otherwise (LA_ERR_INVALID_ARG as for sconv_fwd), nor with b or c.
  *
- * Sequences longer than time_block tokens are split along time, blocks starting at
- * each sequence's first token; a split costs up to 3/4 of the arithmetic again, so
- * with time_block 0 blocks are as long as T and D allow while the GPU is filled
- * (powers of two from 64 on).  Results are the same bits for the same T, N, D, S, G and
+ * Sequences longer than two blocks of time_block tokens are split along time, blocks
+ * starting at each sequence's first token; a split costs up to 3/4 of the arithmetic
+ * again, so with time_block 0 blocks are as long as T and D allow while the GPU is
+ * filled (powers of two from 64 on).  Results are the same bits for the same T, N, D, S, G and
  * time_block; with a given time_block they are batch invariant too.
  */
 la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream);
@@ -937,7 +937,7 @@ typedef struct la_ssm_decode_params {
 /* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode). */
 la_status ssm_decode(const la_ssm_decode_params* p, void* stream);
 
-/* Rows of ssm_fwd's checkpoints buffer: T / 32 + N (0 for invalid arguments). */
+/* Rows of ssm_fwd's checkpoints buffer: T / 16 + N (0 for invalid arguments). */
 size_t la_ssm_checkpoint_rows(int64_t T, int32_t N);
 
 /* Bytes of device workspace that ssm_fwd and ssm_bwd need (0 for invalid arguments, and where none is needed). */

@@ -85,14 +85,14 @@ def test_refusals(fn, over, code):
 
 def test_sizes():
     lib = B.load()
-    assert la.ssm_checkpoint_rows(0, 3) == 3 and la.ssm_checkpoint_rows(1000, 3) == 34
+    assert la.ssm_checkpoint_rows(0, 3) == 3 and la.ssm_checkpoint_rows(1000, 3) == 65
     assert lib.la_ssm_checkpoint_rows(-1, 3) == 0
-    assert lib.la_ssm_fwd_workspace_bytes(64, 3, 70, 16, 1, 64) == 0
-    assert lib.la_ssm_fwd_workspace_bytes(65, 3, 70, 16, 1, 64) >= 4 * 70 * 17 * 4
+    assert lib.la_ssm_fwd_workspace_bytes(128, 3, 70, 16, 1, 64) == 0
+    assert lib.la_ssm_fwd_workspace_bytes(129, 3, 70, 16, 1, 64) >= 5 * 70 * 17 * 4
     assert lib.la_ssm_fwd_workspace_bytes(1000, 3, 70, 16, 1, 0) >= lib.la_ssm_fwd_workspace_bytes(1000, 3, 70, 16, 1, 512)
     for bad in ((-1, 3, 70, 16, 1), (10, 3, 70, 65, 1), (10, 3, 70, 16, 3)):
         assert lib.la_ssm_fwd_workspace_bytes(*bad, 64) == 0 and lib.la_ssm_bwd_workspace_bytes(*bad, 0) == 0
-    assert lib.la_ssm_bwd_workspace_bytes(1000, 3, 70, 16, 1, 0) >= lib.la_ssm_bwd_workspace_bytes(1000, 3, 70, 16, 1, 1) + 34 * 70 * 16 * 4
+    assert lib.la_ssm_bwd_workspace_bytes(1000, 3, 70, 16, 1, 0) >= lib.la_ssm_bwd_workspace_bytes(1000, 3, 70, 16, 1, 1) + 65 * 70 * 16 * 4
     assert [lib.la_rn_scale_blocks(V, q) for V, q in ((4096, 0), (4096, 1), (4096, 2), (4097, 2), (33, 3), (0, 3), (5, 9))] == [0, 1, 32, 33, 2, 0, 0]
     assert lib.la_rn_bwd_workspace_bytes(10, 64) > 0 and lib.la_rn_bwd_workspace_bytes(10, 16385) == 0
 
