@@ -1,6 +1,6 @@
 // ssm_fwd.cu -- the selective scan's forward (ssm.cuh has the formulas).
 //
-// A warp takes 32 / Q channels of one time block and walks its tokens, 32 at a time through shared memory, the next ones
+// A warp takes 32 / Q channels of one time block and walks its tokens, 16 at a time through shared memory, the next ones
 // on their way meanwhile (cp.async).  A lane has one channel with kS of its states, so that B and C are the same address for
 // 32 or 16 neighbouring lanes (two cycles for 16 bytes a lane, measured, where addresses that alternate between lanes
 // take four), pairs of states come as they lie, and up to 16 states no sum goes over lanes.  What two tokens' scans need
@@ -15,7 +15,8 @@ namespace la {
 namespace ssm {
 namespace {
 
-constexpr int kTok = 32;  // tokens of a stage; a multiple of kSave
+constexpr int kTok = 16;  // tokens of a stage; saved states lie between stages
+static_assert(kTok == kSave, "");
 
 template <typename X, int kS, int Q>
 struct Stage {
@@ -26,7 +27,7 @@ struct Stage {
 };
 
 template <typename X, int kS, int Q, bool kLocal, bool kGate>
-__global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
+__global__ void __launch_bounds__(32, 14) ssm_scan_kernel(const Args a) {
     typedef Stage<X, kS, Q> Sm;
     constexpr int kW = Sm::kW, kSP = Sm::kSP, kPairs = kS / 2;
     __shared__ __align__(16) Sm sm;
@@ -105,6 +106,8 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
         }
         bs += s0;
         cs += s0;
+        if (!kLocal && a.ckpt)
+            store_lane_states<kS>(h, a.ckpt, static_cast<int64_t>(blk.first) / kSave + blk.seq + (blk.start - blk.first + t0) / kSave, a, d, s0, live, 0);
         const X *xs = sm.rows[buf][0] + ch, *ds = sm.rows[buf][1] + ch, *zs = sm.rows[buf][2] + ch;
         struct Pair {  // two tokens' steps, dt x, skip x and gates
             float2 dt, u, rest, gate;
@@ -151,27 +154,23 @@ __global__ void __launch_bounds__(32) ssm_scan_kernel(const Args a) {
         // rows beyond n are prepared too, from whatever lies there, and not used
         Pair now = prepare(0);
         int r = 0;
-        for (int r0 = 0; r0 < n; r0 += kSave) {
-            if (!kLocal && a.ckpt)
-                store_lane_states<kS>(h, a.ckpt, static_cast<int64_t>(blk.first) / kSave + blk.seq + (blk.start - blk.first + t0 + r0) / kSave, a, d, s0, live, 0);
 #pragma unroll 2
-            for (; r + 1 < min(n, r0 + kSave); r += 2) {
-                const Pair next = prepare((r + 2) % kTok);
-                float2 p;
-                p.x = token(now.dt.x, now.u.x, r);
-                p.y = token(now.dt.y, now.u.y, r + 1);
-                if (kLocal) {
-                    sum += now.dt.x + now.dt.y;
-                } else {
-                    p = finish(now, p);
-                    if (stores) {
-                        out[0] = from_f<X>(p.x);
-                        out[a.y_st] = from_f<X>(p.y);
-                    }
-                    out += 2 * a.y_st;
+        for (; r + 1 < n; r += 2) {
+            const Pair next = prepare((r + 2) % kTok);
+            float2 p;
+            p.x = token(now.dt.x, now.u.x, r);
+            p.y = token(now.dt.y, now.u.y, r + 1);
+            if (kLocal) {
+                sum += now.dt.x + now.dt.y;
+            } else {
+                p = finish(now, p);
+                if (stores) {
+                    out[0] = from_f<X>(p.x);
+                    out[a.y_st] = from_f<X>(p.y);
                 }
-                now = next;
+                out += 2 * a.y_st;
             }
+            now = next;
         }
         if (r < n) {
             const float p = token(now.dt.x, now.u.x, r);
@@ -262,7 +261,7 @@ int fwd_shift(int64_t T, int D, int S, int G, int time_block) {
         while ((1 << shift) < time_block) ++shift;
         return shift;
     }
-    constexpr int kFill = 8;
+    constexpr int kFill = 24;
     const int64_t width = scan_width(S), tiles = (D / G + width - 1) / width * G;
     while (shift < 30 && (T * tiles >> shift) > kSms * kFill) ++shift;
     return shift;
