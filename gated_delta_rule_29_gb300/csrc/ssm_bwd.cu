@@ -238,10 +238,15 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
             __syncthreads();  // these tokens have come, and the last ones have been finished
             if (kBufs == 2) load(buf ^ 1, t0 - kSub);
             const X *xs = sm.rows[buf][0], *ds = sm.rows[buf][1], *ys = sm.rows[buf][2], *zs = sm.rows[buf][3];
+            // tokens are worked on in fours: the ones beyond the last have steps, inputs and gradients of 0, which change nothing
+            const int n4 = (n + 3) & ~3;
 #pragma unroll
             for (int r = r4; r < kSub; r += kRows) {
-                if (r >= n) break;
                 const int at = r * kTile + c4;
+                if (r >= n) {
+                    if (r < n4) *reinterpret_cast<float4*>(&sm.dt[r][c4]) = *reinterpret_cast<float4*>(&sm.u[r][c4]) = *reinterpret_cast<float4*>(&sm.dp[r][c4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    continue;
+                }
                 const float4 x = load4<X>(xs, at, 4, 1), v = load4<X>(ds, at, 4, 1), dy = load4<X>(ys, at, 4, 1);
                 const float2 t0 = steps_of(add2(lo(v), bias[0]), a.softplus), t1 = steps_of(add2(hi(v), bias[1]), a.softplus);
                 const float2 u0 = mul2(t0, lo(x)), u1 = mul2(t1, hi(x));
@@ -255,9 +260,11 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                 *reinterpret_cast<float4*>(&sm.u[r][c4]) = make_float4(u0.x, u0.y, u1.x, u1.y);
                 *reinterpret_cast<float4*>(&sm.dp[r][c4]) = make_float4(p0.x, p0.y, p1.x, p1.y);
             }
-            for (int i = tid; i < n * Q; i += kThreads) {
-                *reinterpret_cast<float4*>(&sm.b[0][0] + 4 * i) = load4<X>(sm.states[buf][0], 4 * i, 4, 1);
-                *reinterpret_cast<float4*>(&sm.c[0][0] + 4 * i) = load4<X>(sm.states[buf][1], 4 * i, 4, 1);
+            for (int i = tid; i < n4 * Q; i += kThreads) {
+                const bool there = i < n * Q;
+                const float4 zeros = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4*>(&sm.b[0][0] + 4 * i) = there ? load4<X>(sm.states[buf][0], 4 * i, 4, 1) : zeros;
+                *reinterpret_cast<float4*>(&sm.c[0][0] + 4 * i) = there ? load4<X>(sm.states[buf][1], 4 * i, 4, 1) : zeros;
             }
             __syncthreads();
 
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                 float y[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = min(4 * k + i, n - 1);
+                    const int r = 4 * k + i;
                     const float4 dt = *reinterpret_cast<const float4*>(&sm.dt[r][cl]), u = *reinterpret_cast<const float4*>(&sm.u[r][cl]);
                     const float4 b = *reinterpret_cast<const float4*>(&sm.b[r][s0]), c = *reinterpret_cast<const float4*>(&sm.c[r][s0]);
                     const float bs[4] = {b.x, b.y, b.z, b.w}, cs[4] = {c.x, c.y, c.z, c.w};
@@ -295,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = spread_sum<4, 1, Q>(y[i]);
-                        if (4 * k + i < n && q < 4) sm.r[4 * k + i][cl + at] = y[i][0];
+                        if (q < 4) sm.r[4 * k + i][cl + at] = y[i][0];
                     }
                 }
             }
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = min(4 * k + i, n - 1);
+                    const int r = 4 * k + i;
                     const float4 dt = *reinterpret_cast<const float4*>(&sm.dt[r][cl]), u = *reinterpret_cast<const float4*>(&sm.u[r][cl]);
                     const float4 b = *reinterpret_cast<const float4*>(&sm.b[r][s0]);
                     const float bs[4] = {b.x, b.y, b.z, b.w};
@@ -346,13 +353,20 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                         }
                     }
                 }
+                // what a token takes from shared memory: requested before the sums of the one after it go over the lanes
+                // (what is written between would hold the reads back)
+                float4 dt, u, dp, b, c;
+                auto fetch = [&](int r) {
+                    dt = *reinterpret_cast<const float4*>(&sm.dt[r][cl]);
+                    u = *reinterpret_cast<const float4*>(&sm.u[r][cl]);
+                    dp = *reinterpret_cast<const float4*>(&sm.dp[r][cl]);
+                    b = *reinterpret_cast<const float4*>(&sm.b[r][s0]);
+                    c = *reinterpret_cast<const float4*>(&sm.c[r][s0]);
+                };
+                fetch(4 * k + 3);
 #pragma unroll
                 for (int i = 3; i >= 0; --i) {
                     const int r = 4 * k + i;
-                    if (r >= n) continue;  // the same for the whole CTA
-                    const float4 dt = *reinterpret_cast<const float4*>(&sm.dt[r][cl]), u = *reinterpret_cast<const float4*>(&sm.u[r][cl]);
-                    const float4 dp = *reinterpret_cast<const float4*>(&sm.dp[r][cl]);
-                    const float4 b = *reinterpret_cast<const float4*>(&sm.b[r][s0]), c = *reinterpret_cast<const float4*>(&sm.c[r][s0]);
                     const float bs[4] = {b.x, b.y, b.z, b.w}, cs[4] = {c.x, c.y, c.z, c.w};
                     float2 db[4], dc[4];
                     float t[8];
@@ -376,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                         t[4 + 2 * p] = wa.x;
                         t[5 + 2 * p] = wa.y;
                     }
+                    if (i > 0) fetch(r - 1);
                     float v[8];
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
