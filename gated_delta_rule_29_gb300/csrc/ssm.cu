@@ -10,53 +10,191 @@ using namespace la::ssm;
 
 constexpr int kThreads = 128;
 
-// One thread four states of one channel of one sequence.
-template <typename X, int Q>
+// A lane has kS states of one channel of one sequence: as few steps are formed as there are channels, but its 16-byte
+// accesses lie kS * 4 bytes from its neighbours' (512 x 8192 x 16 in fp32: 124 us, all of it L1 wavefronts).
+template <typename X, int kS, int Q>
 __global__ void __launch_bounds__(kThreads) ssm_decode_kernel(const Args a) {
+    constexpr int kW = 32 / Q, kPairs = kS / 2;  // channels of a warp
+    const int lane = threadIdx.x & 31, q = lane / kW, s0 = kS * q;
+    const int d = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kW + lane % kW;
     const int64_t i = this_slot();
     if (i >= a.N) return;
-    const int q = threadIdx.x % Q, s = 4 * q;
-    const int d = blockIdx.x * (kThreads / Q) + threadIdx.x / Q;
+    const bool live = d < a.D;
     const int64_t row = state_row(a, static_cast<int32_t>(i));
     if (row < 0) return;
-    const bool live = d < a.D;
-    const int j = live ? d / a.Dg : 0;
-    float4 h = load_states(a.s0, row, a, d, s, live, a.s0_bf16);
-    const float4 A = load_states(a.A, 0, a, d, s, live, 0);
-    const float4 b = load4<X>(a.b, i * a.b_st + j * a.b_sg + s, a.S - s, a.vec), c = load4<X>(a.c, i * a.c_st + j * a.c_sg + s, a.S - s, a.vec);
-    const float x = live ? to_f(static_cast<const X*>(a.x)[i * a.x_st + d]) : 0.f;
-    const float dt = live ? steps_of(both(to_f(static_cast<const X*>(a.dt)[i * a.dt_st + d]) + (a.bias ? a.bias[d] : 0.f)), a.softplus).x : 0.f;
-    const float u = dt * x, l = dt * kLog2e;
-    h.x = fmaf(ex2(l * A.x), h.x, u * b.x);
-    h.y = fmaf(ex2(l * A.y), h.y, u * b.y);
-    h.z = fmaf(ex2(l * A.z), h.z, u * b.z);
-    h.w = fmaf(ex2(l * A.w), h.w, u * b.w);
-    store_states(const_cast<void*>(a.s0), row, a, d, s, live, a.s0_bf16, h);
-    float p = fmaf(h.x, c.x, h.y * c.y) + fmaf(h.z, c.z, h.w * c.w);
+    float2 h[kPairs], A[kPairs];
+    load_lane_states<kS>(h, a.s0, row, a, d, s0, live, a.s0_bf16);
+    const float x = live ? to_f(static_cast<const X*>(a.x)[i * a.x_st + d]) : 0.f, raw = live ? to_f(static_cast<const X*>(a.dt)[i * a.dt_st + d]) : 0.f;
+    const float z = live && a.z ? to_f(static_cast<const X*>(a.z)[i * a.z_st + d]) : 0.f;
+    load_lane_states<kS>(A, a.A, 0, a, d, s0, live, 0);
+    const float bias = live && a.bias ? a.bias[d] : 0.f, skip = live && a.skip ? a.skip[d] : 0.f;
+    const int64_t j = live ? d / a.Dg : 0, b_at = i * a.b_st + j * a.b_sg + s0, c_at = i * a.c_st + j * a.c_sg + s0;
+    const float step = steps_of(both(raw + bias), a.softplus).x;
+    const float2 u = both(step * x), l = both(step * kLog2e);
+    float2 y = both(0.f);
 #pragma unroll
-    for (int off = 1; off < Q; off *= 2) p += __shfl_xor_sync(0xffffffffu, p, off);
-    if (!live || q) return;
-    if (a.skip) p = fmaf(a.skip[d], x, p);
-    if (a.z) p *= act_fwd(LA_ACT_SILU, to_f(static_cast<const X*>(a.z)[i * a.z_st + d]));
-    static_cast<X*>(a.y)[i * a.y_st + d] = from_f<X>(p);
+    for (int k = 0; k < kPairs; k += 2) {
+        const float4 b = load4<X>(a.b, b_at + 2 * k, a.S - s0 - 2 * k, a.vec), c = load4<X>(a.c, c_at + 2 * k, a.S - s0 - 2 * k, a.vec);
+        const float2 l0 = mul2(l, A[k]), l1 = mul2(l, A[k + 1]);
+        h[k] = fma2(make_float2(ex2(l0.x), ex2(l0.y)), h[k], mul2(u, lo(b)));
+        h[k + 1] = fma2(make_float2(ex2(l1.x), ex2(l1.y)), h[k + 1], mul2(u, hi(b)));
+        y = fma2(h[k], lo(c), y);
+        y = fma2(h[k + 1], hi(c), y);
+    }
+    store_lane_states<kS>(h, const_cast<void*>(a.s0), row, a, d, s0, live, a.s0_bf16);
+    float p = y.x + y.y;
+#pragma unroll
+    for (int off = kW; off < 32; off *= 2) p += __shfl_xor_sync(0xffffffffu, p, off);
+    p = fmaf(skip, x, p);
+    if (a.z) p *= act_fwd(LA_ACT_SILU, z);
+    if (live && q == 0) static_cast<X*>(a.y)[i * a.y_st + d] = from_f<X>(p);
 }
 
-struct Decode {
-    template <typename X, int Q>
-    static la_status run(Args& a, cudaStream_t s) {
-        constexpr int kChannels = kThreads / Q;
-        ssm_decode_kernel<X, Q><<<slot_grid((a.D + kChannels - 1) / kChannels, a.N), kThreads, 0, s>>>(a);
-        return launched();
-    }
-};
+// For many fp32 states: Q neighbouring lanes share a channel, four states each, so that accesses are contiguous, and a CTA
+// keeps its channels and goes over the sequences, four at a time, with the states of the next groups on their way into shared
+// memory (each thread's own 16 bytes, so that nothing waits but the thread).  The lanes of a channel share the four
+// sequences' steps and results.  512 x 8192 x 16 in 112 us (4.8 TB/s), 512 x 4096 x 64 in 219 (375 the way above).
+constexpr int kSeqs = 4, kDepth = 4;
 
+template <typename X, int Q>
+__global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args a, int groups) {
+    __shared__ __align__(16) float4 ring[kDepth][kSeqs][kThreads];
+    constexpr int kShare = Q < kSeqs ? Q : kSeqs, kOwn = kSeqs / kShare;  // lanes that share the sequences; sequences of a lane
+    const int q = threadIdx.x % Q, s = 4 * q, mine = q % kShare;          // this lane's: mine, mine + kShare, ...
+    const int d = blockIdx.x * (kThreads / Q) + threadIdx.x / Q;
+    const bool live = d < a.D && s < a.S;
+    const int dl = min(d, a.D - 1), j = dl / a.Dg;
+    const int64_t within = static_cast<int64_t>(dl) * a.S + s, pitch = static_cast<int64_t>(a.D) * a.S;
+    float* const pool = static_cast<float*>(const_cast<void*>(a.s0));
+    const float bias = a.bias ? a.bias[dl] : 0.f, skip = a.skip ? a.skip[dl] : 0.f;
+    const float4 A = load_states(a.A, 0, a, d, s, live, 0);
+
+    // the slots of a group's sequences as they are given; which of them are there is seen when they are used
+    auto slots_of = [&](int (&slot)[kSeqs], int group) {
+#pragma unroll
+        for (int i = 0; i < kSeqs; ++i) {
+            const int n = group * kSeqs + i;
+            slot[i] = n < a.N ? (a.idx ? a.idx[n] : n) : -1;
+        }
+    };
+    auto request = [&](int stage, const int (&slot)[kSeqs]) {
+#pragma unroll
+        for (int i = 0; i < kSeqs; ++i)
+            if (live && slot[i] >= 0 && slot[i] < a.pool) cp_async16(&ring[stage][i][threadIdx.x], pool + slot[i] * pitch + within);
+        cp_async_commit();
+    };
+    struct Inputs {
+        Packed<X, 4> b[kSeqs], c[kSeqs];
+        X x[kOwn], dt[kOwn], z[kOwn];
+    };
+    auto inputs_of = [&](int group) {
+        Inputs t;
+#pragma unroll
+        for (int i = 0; i < kSeqs; ++i) {
+            const int64_t n = min(group * kSeqs + i, a.N - 1);
+            t.b[i].load(static_cast<const X*>(a.b) + n * a.b_st + j * a.b_sg + min(s, a.S - 4));
+            t.c[i].load(static_cast<const X*>(a.c) + n * a.c_st + j * a.c_sg + min(s, a.S - 4));
+        }
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const int64_t n = min(group * kSeqs + mine + k * kShare, a.N - 1);
+            t.x[k] = static_cast<const X*>(a.x)[n * a.x_st + dl];
+            t.dt[k] = static_cast<const X*>(a.dt)[n * a.dt_st + dl];
+            t.z[k] = a.z ? static_cast<const X*>(a.z)[n * a.z_st + dl] : from_f<X>(0.f);
+        }
+        return t;
+    };
+    const int step = gridDim.y;
+    int group = blockIdx.y, slot[kDepth][kSeqs];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) slots_of(slot[k], group + k * step);
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) request(k, slot[k]);
+    Inputs in = inputs_of(group);
+    for (int n = 0; group < groups; ++n, group += step) {
+        request((n + kDepth - 1) % kDepth, slot[kDepth - 1]);
+        int here[kSeqs];
+#pragma unroll
+        for (int i = 0; i < kSeqs; ++i) {
+            here[i] = slot[0][i];
+#pragma unroll
+            for (int k = 0; k + 1 < kDepth; ++k) slot[k][i] = slot[k + 1][i];
+        }
+        slots_of(slot[kDepth - 1], group + kDepth * step);
+        const Inputs now = in;
+        in = inputs_of(group + step);
+        float x[kOwn], dt[kOwn];
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            x[k] = to_f(now.x[k]);
+            dt[k] = steps_of(both(to_f(now.dt[k]) + bias), a.softplus).x;
+        }
+        cp_async_wait<kDepth - 1>();
+        float p[kSeqs];
+#pragma unroll
+        for (int i = 0; i < kSeqs; ++i) {
+            const int from = (threadIdx.x & 31) / Q * Q + i % kShare;
+            const float t = kShare == 1 ? dt[i / kShare] : __shfl_sync(0xffffffffu, dt[i / kShare], from);
+            const float v = kShare == 1 ? x[i / kShare] : __shfl_sync(0xffffffffu, x[i / kShare], from);
+            const bool there = here[i] >= 0 && here[i] < a.pool;
+            const float u = t * v, l = t * kLog2e;
+            float4 h = ring[n % kDepth][i][threadIdx.x];
+            h.x = fmaf(ex2(l * A.x), h.x, u * now.b[i].get(0));
+            h.y = fmaf(ex2(l * A.y), h.y, u * now.b[i].get(1));
+            h.z = fmaf(ex2(l * A.z), h.z, u * now.b[i].get(2));
+            h.w = fmaf(ex2(l * A.w), h.w, u * now.b[i].get(3));
+            if (live && there) *reinterpret_cast<float4*>(pool + here[i] * pitch + within) = h;
+            p[i] = live ? fmaf(h.x, now.c[i].get(0), h.y * now.c[i].get(1)) + fmaf(h.z, now.c[i].get(2), h.w * now.c[i].get(3)) : 0.f;
+#pragma unroll
+            for (int off = 1; off < Q; off *= 2) p[i] += __shfl_xor_sync(0xffffffffu, p[i], off);
+            if (!there && group * kSeqs + i < a.N) raise_status(a.status, LA_ERR_BAD_STATE_INDEX);
+        }
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            float y = 0.f;
+            bool there = false;
+#pragma unroll
+            for (int i = 0; i < kShare; ++i)
+                if (mine == i) {
+                    y = p[i + k * kShare];
+                    there = here[i + k * kShare] >= 0 && here[i + k * kShare] < a.pool;
+                }
+            y = fmaf(skip, x[k], y);
+            if (a.z) y *= act_fwd(LA_ACT_SILU, to_f(now.z[k]));
+            if (there && d < a.D && q < kShare) static_cast<X*>(a.y)[(static_cast<int64_t>(group) * kSeqs + mine + k * kShare) * a.y_st + d] = from_f<X>(y);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+template <typename X, int kS, int Q>
+la_status decode(const Args& a, cudaStream_t s) {
+    constexpr int kChannels = kThreads / Q;
+    ssm_decode_kernel<X, kS, Q><<<slot_grid((a.D + kChannels - 1) / kChannels, a.N), kThreads, 0, s>>>(a);
+    return launched();
+}
+template <typename X, int Q>
+la_status decode_many(const Args& a, cudaStream_t s) {
+    const int tiles = (a.D + kThreads / Q - 1) / (kThreads / Q), groups = (a.N + kSeqs - 1) / kSeqs;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(std::max(1, groups / 8)));
+    ssm_decode_many_kernel<X, Q><<<grid, kThreads, 0, s>>>(a, groups);
+    return launched();
+}
 template <typename X>
-la_status by_states(Args& a, cudaStream_t s) {
-    if (a.S <= 4) return Decode::run<X, 1>(a, s);
-    if (a.S <= 8) return Decode::run<X, 2>(a, s);
-    if (a.S <= 16) return Decode::run<X, 4>(a, s);
-    if (a.S <= 32) return Decode::run<X, 8>(a, s);
-    return Decode::run<X, 16>(a, s);
+la_status by_states(const Args& a, cudaStream_t s) {
+    // rows in 16-byte accesses throughout, and states enough for CTAs of eight groups: 64 x 8192 x 16 takes 21 us this way and
+    // 25 the other, 64 x 4096 x 16 18 and 16
+    if (a.vec && a.svec && !a.s0_bf16 && a.S >= 4 && static_cast<int64_t>(a.N) * a.D * a.S >= int64_t(1) << 23) {
+        if (a.S <= 4) return decode_many<X, 1>(a, s);
+        if (a.S <= 8) return decode_many<X, 2>(a, s);
+        if (a.S <= 16) return decode_many<X, 4>(a, s);
+        if (a.S <= 32) return decode_many<X, 8>(a, s);
+        return decode_many<X, 16>(a, s);
+    }
+    if (a.S <= 8) return decode<X, 8, 1>(a, s);
+    if (a.S <= 16) return decode<X, 16, 1>(a, s);
+    if (a.S <= 32) return decode<X, 16, 2>(a, s);
+    return decode<X, 16, 4>(a, s);
 }
 
 size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
