@@ -20,52 +20,48 @@ def ssm_checkpoint_rows(T: int, N: int) -> int:
     return int(B.load().la_ssm_checkpoint_rows(int(T), int(N)))
 
 
+def _like(name: str, v, like: torch.Tensor) -> int:
+    """Row stride of an operand of the shape, type and device of `like`, rank 2."""
+    if isinstance(v, torch.Tensor) and v.dtype is like.dtype and v.shape == like.shape and v.get_device() == like.get_device():
+        row, last = v.stride()
+        if last == 1:
+            return row
+    row = _rows(name, v, 2, like)[0]
+    if v.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {v.dtype}")
+    return row
+
+
 def _vectors(name: str, v, rows: int, like: torch.Tensor) -> tuple:
     """Strides (row, group) and shape (G, S) of [rows, S] or [rows, G, S] vectors of the type of `like`."""
-    strides = _rows(name, v, 2 if isinstance(v, torch.Tensor) and v.dim() == 2 else 3)
+    shape = getattr(v, "shape", ())
+    strides = _rows(name, v, 2 if len(shape) == 2 else 3)
     if v.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {v.dtype}")
-    if v.shape[0] != rows or v.get_device() != like.get_device():
-        raise ValueError(f"{name} must have {rows} rows on {like.device}, got {tuple(v.shape)} on {v.device}")
-    return (strides[0], 0 if len(strides) == 2 else strides[1]), (v.shape[1] if v.dim() == 3 else 1, v.shape[-1])
+    if shape[0] != rows or v.get_device() != like.get_device():
+        raise ValueError(f"{name} must have {rows} rows on {like.device}, got {tuple(shape)} on {v.device}")
+    return (strides[0], 0, 1, shape[1]) if len(shape) == 2 else (strides[0], strides[1], shape[1], shape[2])
 
 
-def _like(name: str, v, like: torch.Tensor) -> int:
-    """Row stride of an operand of the shape and type of `like`."""
-    strides = _rows(name, v, 2, like)
-    if v.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {v.dtype}")
-    return strides[0]
-
-
-def _ssm_inputs(p, x, dt, a, b, c, skip, z, dt_bias, dt_softplus, suffix: str) -> tuple:
-    """Fills in the operands; `suffix` of the strides' names.  Returns (rows, D, S)."""
-    setattr(p, "x_stride" + suffix, _rows("x", x, 2)[0])
-    p.x, p.x_dtype = x.data_ptr(), _dtype("x", x)
+def _ssm_inputs(cls, x, dt, a, b, c, skip, z, dt_bias, dt_softplus) -> tuple:
+    """The call's parameters with the operands, which are the first fields of every ssm_* struct in the same order, filled
+    in; and (rows, D, S, G)."""
+    x_row = _rows("x", x, 2)[0]
+    _dtype("x", x)
     rows, D = x.shape
-    setattr(p, "dt_stride" + suffix, _like("dt", dt, x))
-    p.dt = dt.data_ptr()
-    if z is not None:
-        setattr(p, "z_stride" + suffix, _like("z", z, x))
-        p.z = z.data_ptr()
-    (row, p.b_stride_g), shape = _vectors("b", b, rows, x)
-    setattr(p, "b_stride" + suffix, row)
-    (row, p.c_stride_g), other = _vectors("c", c, rows, x)
-    setattr(p, "c_stride" + suffix, row)
-    if shape != other:
+    dt_row = _like("dt", dt, x)
+    z_row, z_at = (0, None) if z is None else (_like("z", z, x), z.data_ptr())
+    b_row, b_group, G, S = _vectors("b", b, rows, x)
+    c_row, c_group, c_G, c_S = _vectors("c", c, rows, x)
+    if (c_G, c_S) != (G, S):
         raise ValueError(f"b and c must have the same shape, got {tuple(b.shape)} and {tuple(c.shape)}")
-    p.b, p.c = b.data_ptr(), c.data_ptr()
-    p.G, p.S = G, S = shape
     if G < 1 or D % G:
         raise ValueError(f"the {D} channels must be a multiple of the {G} groups of b and c")
-    p.D = D
-    p.a = _packed("a", a, (D, S), _FP32, x)
-    if skip is not None:
-        p.skip = _packed("skip", skip, (D,), _FP32, x)
-    if dt_bias is not None:
-        p.dt_bias = _packed("dt_bias", dt_bias, (D,), _FP32, x)
-    p.dt_softplus = bool(dt_softplus)
-    return rows, D, S
+    p = cls(x.data_ptr(), x_row, dt.data_ptr(), dt_row, z_at, z_row, b.data_ptr(), b_row, b_group, c.data_ptr(), c_row, c_group,
+            _packed("a", a, (D, S), _FP32, x), None if skip is None else _packed("skip", skip, (D,), _FP32, x),
+            None if dt_bias is None else _packed("dt_bias", dt_bias, (D,), _FP32, x), bool(dt_softplus))
+    p.D, p.S, p.G, p.x_dtype = D, S, G, _DTYPES[x.dtype]
+    return p, rows, D, S, G
 
 
 @_on_stream
@@ -90,8 +86,7 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     initial_state is then a pool [P, D, S] and each sequence's end state is written back to its slot.  time_block (0, or a
     power of two from 64 on): sequences longer than two such blocks are split along time; 0 chooses by T, D, S and the groups, a
     given one makes a sequence's bits independent of the batch around it."""
-    p = B.SsmFwdParams()
-    T, D, S = _ssm_inputs(p, x, dt, a, b, c, skip, z, dt_bias, dt_softplus, "_t")
+    p, T, D, S, G = _ssm_inputs(B.SsmFwdParams, x, dt, a, b, c, skip, z, dt_bias, dt_softplus)
     p.T = T
     N = _sequences(p, cu_seqlens, x)
     if time_block < 0 or time_block & (time_block - 1) or 0 < time_block < 64 or time_block > 1 << 30:
@@ -118,7 +113,7 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if output_checkpoints or checkpoints is not None:
         checkpoints, p.checkpoints = _state_dest("checkpoints", checkpoints, (ssm_checkpoint_rows(T, N), D, S),
                                                  torch.float32, x)
-    need = B.load().la_ssm_fwd_workspace_bytes(T, N, D, S, p.G, time_block)
+    need = B.load().la_ssm_fwd_workspace_bytes(T, N, D, S, G, time_block)
     ws = _workspace(p, workspace, need, x)  # noqa: F841
     if status is not None:
         _status(p, status, x)
@@ -138,8 +133,7 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     """Gradients of sum(dy * y) + sum(d_final_state * final_state) for ssm_fwd with the same inputs: (dx, ddt, da, db,
     dc, d_skip or None, dz or None, d_dt_bias or None, d_initial_state [N, D, S] fp32), each in its input's dtype.
     checkpoints: the forward's; without them the states are recomputed (one more forward pass)."""
-    p = B.SsmBwdParams()
-    T, D, S = _ssm_inputs(p, x, dt, a, b, c, skip, z, dt_bias, dt_softplus, "_t")
+    p, T, D, S, G = _ssm_inputs(B.SsmBwdParams, x, dt, a, b, c, skip, z, dt_bias, dt_softplus)
     p.T = T
     N = _sequences(p, cu_seqlens, x)
     p.dy, p.dy_stride_t = dy.data_ptr() if isinstance(dy, torch.Tensor) else None, _like("dy", dy, x)
@@ -169,7 +163,7 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         d_bias = torch.empty_like(dt_bias)
         p.d_dt_bias = d_bias.data_ptr()
     d_initial, p.d_initial_state = _state_dest("d_initial_state", None, (N, D, S), torch.float32, x)
-    need = B.load().la_ssm_bwd_workspace_bytes(T, N, D, S, p.G, checkpoints is not None)
+    need = B.load().la_ssm_bwd_workspace_bytes(T, N, D, S, G, checkpoints is not None)
     ws = _workspace(p, workspace, need, x)  # noqa: F841
     if status is not None:
         _status(p, status, x)
@@ -186,8 +180,7 @@ def ssm_decode(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tens
     """One scan step for each of N sequences: x, dt, z [N, D], b, c [N, S] or [N, G, S]; sequence i steps
     pool[state_indices[i]] (pool[i] without indices) of state_pool [P, D, S] (fp32 or bf16) in place.  Returns y [N, D]
     in x's dtype."""
-    p = B.SsmDecodeParams()
-    N, D, S = _ssm_inputs(p, x, dt, a, b, c, skip, z, dt_bias, dt_softplus, "_n")
+    p, N, D, S, _ = _ssm_inputs(B.SsmDecodeParams, x, dt, a, b, c, skip, z, dt_bias, dt_softplus)
     p.N = N
     if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 3:
         raise ValueError("state_pool must be a contiguous [P, D, S] tensor")
@@ -341,7 +334,7 @@ class _ResidualNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, d_s=None):
         s, weight = ctx.saved_tensors
-        dy = torch.zeros_like(s, dtype=ctx.dtype) if dy is None else _cotangent(dy, torch.empty(0, dtype=ctx.dtype))
+        dy = torch.zeros_like(s, dtype=ctx.dtype) if dy is None else _cotangent(dy, dy)  # the type of y, which is x's
         dx, dw, ds = rn_bwd(s, weight, dy, d_residual=None if d_s is None else _cotangent(d_s, s), eps=ctx.eps)
         return dx, dw, (ds if ctx.added else None), None
 

@@ -30,11 +30,12 @@ struct Args {
     float eps;
     void *y, *out, *scales, *ds;   // y: the result, or dx in the backward; out: the sum
     float* pw;                     // partial sums [CTAs][V] of dw
+    int64_t ctas;                  // of the backward (0 without rows: the sums are then zero)
 };
 
-// A lane's elements: kVec consecutive ones NV times.
+// kVec consecutive elements in accesses of up to 16 bytes.
 template <typename X, int kVec>
-struct Vec {  // kVec elements in accesses of up to 16 bytes
+struct Vec {
     static constexpr int kPer = kVec * static_cast<int>(sizeof(X)) > 16 ? 16 / static_cast<int>(sizeof(X)) : kVec, kParts = kVec / kPer;
     Packed<X, kPer> p[kParts];
     __device__ __forceinline__ void load(const X* from) {
@@ -46,16 +47,42 @@ struct Vec {  // kVec elements in accesses of up to 16 bytes
         for (int i = 0; i < kParts; ++i) p[i].zero();
     }
     __device__ __forceinline__ float get(int i) const { return p[i / kPer].get(i % kPer); }
-    __device__ __forceinline__ static void store(X* to, const float* v) {
+    __device__ __forceinline__ void store(X* to) const {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            float t[kPer];
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) t[j] = v[i * kPer + j];
-            store_packed<X, kPer>(to + i * kPer, t);
+            uint32_t* t = reinterpret_cast<uint32_t*>(to + i * kPer);
+            const uint32_t* w = p[i].w;
+            constexpr int kBytes = kPer * static_cast<int>(sizeof(X));
+            if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(t) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(t) = make_uint2(w[0], w[1]);
+            else if constexpr (kBytes == 4) *t = w[0];
+            else *reinterpret_cast<uint16_t*>(t) = static_cast<uint16_t>(w[0]);
         }
     }
 };
+// Elements 2j and 2j + 1 of a lane's NV vectors, and the same rounded to X.
+template <typename X, int kVec, int NV>
+__device__ __forceinline__ float2 pair_of(const Vec<X, kVec> (&v)[NV], int j) {
+    return make_float2(v[2 * j / kVec].get(2 * j % kVec), v[(2 * j + 1) / kVec].get((2 * j + 1) % kVec));
+}
+template <typename X, int kVec, int NV>
+__device__ __forceinline__ void set_pair(Vec<X, kVec> (&v)[NV], int j, float2 f) {
+    constexpr int kPer = Vec<X, kVec>::kPer;
+    const int a = 2 * j % kVec, b = (2 * j + 1) % kVec;
+    if constexpr (sizeof(X) == 4) {
+        v[2 * j / kVec].p[a / kPer].w[a % kPer] = __float_as_uint(f.x);
+        v[(2 * j + 1) / kVec].p[b / kPer].w[b % kPer] = __float_as_uint(f.y);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+        if constexpr (kVec == 1) {
+            v[2 * j].p[0].w[0] = u & 0xFFFFu;
+            v[2 * j + 1].p[0].w[0] = u >> 16;
+        } else {
+            v[2 * j / kVec].p[a / kPer].w[a % kPer / 2] = u;
+        }
+    }
+}
 
 template <int kVec, int NV>
 struct Place {
@@ -78,22 +105,17 @@ __device__ __forceinline__ void load_row(Vec<X, kVec> (&v)[NV], const void* base
     }
 }
 template <typename X, int kVec, int NV>
-__device__ __forceinline__ void store_row(void* base, int64_t at, const float (&v)[NV * kVec], Place<kVec, NV> pl, int V) {
+__device__ __forceinline__ void store_row(void* base, int64_t at, const Vec<X, kVec> (&v)[NV], Place<kVec, NV> pl, int V) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = pl.column(k);
-        if (c < V) Vec<X, kVec>::store(static_cast<X*>(base) + at + c, v + k * kVec);
+        if (c < V) v[k].store(static_cast<X*>(base) + at + c);
     }
 }
 template <int kVec, int NV>
-__device__ __forceinline__ void load_weight(float (&w)[NV * kVec], const Args& a, Place<kVec, NV> pl) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = pl.column(k) + i;
-            w[k * kVec + i] = c < a.V ? load_any(a.w, c, a.w_bf16) : 0.f;
-        }
+__device__ __forceinline__ float2 weight_pair(const Args& a, Place<kVec, NV> pl, int j) {
+    const int c0 = pl.column(2 * j / kVec) + 2 * j % kVec, c1 = pl.column((2 * j + 1) / kVec) + (2 * j + 1) % kVec;
+    return make_float2(c0 < a.V ? load_any(a.w, c0, a.w_bf16) : 0.f, c1 < a.V ? load_any(a.w, c1, a.w_bf16) : 0.f);
 }
 
 // The larger value, NaN where one is.

@@ -5,11 +5,17 @@ namespace la {
 namespace rn {
 namespace {
 
+// CTAs of 256 threads that an SM holds, with room for the next row: 65536 x 4096 with an fp32 stream takes 671 us with one, 696
+// with two (and spills), 692 with three and no row ahead; a floor of 641.
+template <typename R, int kVec, int kElements>
+constexpr int resident() { return kElements > 16 ? 1 : kVec == 1 ? (kElements > 8 ? 2 : 3) : kElements > 8 ? (sizeof(R) == 4 ? 1 : 2) : sizeof(R) == 4 ? 2 : 3; }
+constexpr int kMostResident = 3;
+
 // The weight gradient is summed in registers over a warp's rows, then over the CTA's groups, then by a second launch over
 // the CTAs, in an order fixed by the shape.
 template <typename X, typename R, int kVec, int NV, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) rn_bwd_kernel(const Args a) {
-    constexpr int E = NV * kVec;
+__global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>())) rn_bwd_kernel(const Args a) {
+    constexpr int P = NV * kVec / 2;
     __shared__ float2 red[2][32];
     extern __shared__ float sums[];  // [groups][V]
     const int warp = threadIdx.x >> 5;
@@ -17,45 +23,67 @@ __global__ void __launch_bounds__(kMaxThreads) rn_bwd_kernel(const Args a) {
     const auto pl = place<kVec, NV>(warp % a.warps);
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups, rounds = (a.T + step - 1) / step;
     const float inv_v = 1.f / a.V;
-    float w[E], dw[E];
-    load_weight<kVec, NV>(w, a, pl);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dw[e] = 0.f;
+    Vec<R, kVec> s[NV], dr[NV], next_s[NV], next_dr[NV];
+    Vec<X, kVec> dy[NV], next_dy[NV];
+    auto load = [&](Vec<R, kVec> (&to_s)[NV], Vec<X, kVec> (&to_dy)[NV], Vec<R, kVec> (&to_dr)[NV], int64_t t) {
+        load_row<R, kVec, NV>(to_s, a.x, t * a.x_st, t < a.T, pl, a.V);
+        load_row<X, kVec, NV>(to_dy, a.dy, t * a.dy_st, t < a.T, pl, a.V);
+        if (a.dres) load_row<R, kVec, NV>(to_dr, a.dres, t * a.dres_st, t < a.T, pl, a.V);
+    };
+    constexpr bool kAhead = kVec > 1 && NV * kVec <= 16;
     int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+    if (kAhead) load(next_s, next_dy, next_dr, t);
+    constexpr bool kKeep = NV * kVec <= 16;
+    float2 w[kKeep ? P : 1], dw[P];  // the weights are kept where a lane holds few elements
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        if (kKeep) w[j] = weight_pair<kVec, NV>(a, pl, j);
+        dw[j] = both(0.f);
+    }
+    auto weight = [&](int j) { return kKeep ? w[j] : weight_pair<kVec, NV>(a, pl, j); };
     for (int64_t n = 0; n < rounds; ++n, t += step) {
         const bool live = t < a.T;
-        Vec<R, kVec> s[NV], dr[NV];
-        Vec<X, kVec> dy[NV];
-        load_row<R, kVec, NV>(s, a.x, t * a.x_st, live, pl, a.V);
-        load_row<X, kVec, NV>(dy, a.dy, t * a.dy_st, live, pl, a.V);
-        if (a.dres) load_row<R, kVec, NV>(dr, a.dres, t * a.dres_st, live, pl, a.V);
-        float sum = 0.f, dot = 0.f;
+        if (kAhead) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float v = s[e / kVec].get(e % kVec), d = dy[e / kVec].get(e % kVec);
-            sum = fmaf(v, v, sum);
-            dot = fmaf(d * w[e], v, dot);
+            for (int k = 0; k < NV; ++k) {
+                s[k] = next_s[k];
+                dy[k] = next_dy[k];
+                dr[k] = next_dr[k];
+            }
+            load(next_s, next_dy, next_dr, t + step);
+        } else {
+            load(s, dy, dr, t);
         }
+        float2 sq = both(0.f), sd = both(0.f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float2 v = pair_of<R, kVec, NV>(s, j);
+            sq = fma2(v, v, sq);
+            sd = fma2(mul2(pair_of<X, kVec, NV>(dy, j), weight(j)), v, sd);
+        }
+        float sum = sq.x + sq.y, dot = sd.x + sd.y;
         row_reduce<false>(sum, dot, a.warps, red, static_cast<int>(n));
-        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps)), m = dot * inv_v * rs * rs;  // mean(dn n) r, what s is taken off with
+        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps)), m = -(dot * inv_v * rs * rs);  // mean(dn n) r, what s is taken off with
         if (!live) continue;  // a warp has one row
-        float o[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float v = s[e / kVec].get(e % kVec), d = dy[e / kVec].get(e % kVec);
-            dw[e] = fmaf(d, v * rs, dw[e]);
-            o[e] = rs * fmaf(-v, m, d * w[e]);
-            if (a.dres) o[e] += dr[e / kVec].get(e % kVec);
+        for (int j = 0; j < P; ++j) {
+            const float2 v = pair_of<R, kVec, NV>(s, j), d = pair_of<X, kVec, NV>(dy, j);
+            dw[j] = fma2(d, mul2(v, both(rs)), dw[j]);
+            float2 o = mul2(both(rs), fma2(v, both(m), mul2(d, weight(j))));
+            if (a.dres) o = add2(o, pair_of<R, kVec, NV>(dr, j));
+            set_pair<X, kVec, NV>(dy, j, o);
+            set_pair<R, kVec, NV>(s, j, o);
         }
-        if (a.y) store_row<X, kVec, NV>(a.y, t * a.y_st, o, pl, a.V);
-        if (a.ds) store_row<R, kVec, NV>(a.ds, t * a.ds_st, o, pl, a.V);
+        if (a.y) store_row<X, kVec, NV>(a.y, t * a.y_st, dy, pl, a.V);
+        if (a.ds) store_row<R, kVec, NV>(a.ds, t * a.ds_st, s, pl, a.V);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = pl.column(k) + i;
-            if (c < a.V) sums[g * a.V + c] = dw[k * kVec + i];
+            const int e = k * kVec + i;
+            if (c < a.V) sums[g * a.V + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
         }
     __syncthreads();
     for (int c = threadIdx.x; c < a.V; c += blockDim.x) {
@@ -79,25 +107,28 @@ __global__ void __launch_bounds__(1024) rn_sum_kernel(const float* pw, int64_t r
     }
 }
 
-int64_t bwd_ctas(int64_t T, int V) {
+int64_t bwd_ctas(int64_t T, int V, int per_sm) {
     const Shape sh = shape(V);
     const int groups = sh.threads / 32 / sh.warps;
-    return std::max<int64_t>(1, std::min<int64_t>((T + groups - 1) / groups, kSms * 2));
+    return std::max<int64_t>(1, std::min<int64_t>((T + groups - 1) / groups, kSms * per_sm));
 }
 
 struct Launch {
     template <typename X, typename R, int kVec, int NV>
-    static la_status run(const Args& a, Shape sh, cudaStream_t s) {
+    static la_status run(Args& a, Shape sh, cudaStream_t s) {
         const size_t smem = static_cast<size_t>(sh.threads / 32 / sh.warps) * a.V * sizeof(float);
-        const unsigned grid = static_cast<unsigned>(bwd_ctas(a.T, a.V));
-        if (sh.threads == 512) {
-            static const cudaError_t opted =
-                cudaFuncSetAttribute(rn_bwd_kernel<X, R, kVec, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV * 4);
-            if (opted != cudaSuccess) return LA_ERR_CUDA;
-            rn_bwd_kernel<X, R, kVec, NV, 512><<<grid, 512, smem, s>>>(a);
-        } else {
-            rn_bwd_kernel<X, R, kVec, NV, 256><<<grid, 256, smem, s>>>(a);
+        a.ctas = bwd_ctas(a.T, a.V, resident<R, kVec, NV * kVec>());
+        const unsigned grid = static_cast<unsigned>(a.ctas);
+        if constexpr (NV * kVec == 32) {
+            if (sh.threads == 512) {
+                static const cudaError_t opted =
+                    cudaFuncSetAttribute(rn_bwd_kernel<X, R, kVec, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV * 4);
+                if (opted != cudaSuccess) return LA_ERR_CUDA;
+                rn_bwd_kernel<X, R, kVec, NV, 512><<<grid, 512, smem, s>>>(a);
+                return launched();
+            }
         }
+        rn_bwd_kernel<X, R, kVec, NV, 256><<<grid, 256, smem, s>>>(a);
         return launched();
     }
 };
@@ -114,7 +145,7 @@ extern "C" {
 
 size_t la_rn_bwd_workspace_bytes(int64_t T, int32_t V) {
     if (T < 0 || V <= 0 || V > kMaxV) return 0;
-    return (static_cast<size_t>(bwd_ctas(T, V)) * V * 4 + 255) & ~size_t(255);
+    return (static_cast<size_t>(bwd_ctas(T, V, kMostResident)) * V * 4 + 255) & ~size_t(255);
 }
 
 la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
@@ -138,12 +169,8 @@ la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
     const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, rs, vec) && wide_rows(a.dy, a.dy_st, a.T, xs, vec) && wide_rows(a.dres, a.dres_st, a.T, rs, vec) &&
                       wide_rows(a.y, a.y_st, a.T, xs, vec) && wide_rows(a.ds, a.ds_st, a.T, rs, vec);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int64_t rows = 0;
-    if (p->T > 0) {
-        if ((st = dispatch<Launch>(a, p->x_dtype, p->s_dtype, wide, s)) != LA_OK) return st;
-        rows = bwd_ctas(a.T, a.V);
-    }
-    rn_sum_kernel<<<static_cast<unsigned>((a.V + 31) / 32), 1024, 0, s>>>(a.pw, rows, a.V, p->d_weight, a.w_bf16);
+    if (p->T > 0 && (st = dispatch<Launch>(a, p->x_dtype, p->s_dtype, wide, s)) != LA_OK) return st;
+    rn_sum_kernel<<<static_cast<unsigned>((a.V + 31) / 32), 1024, 0, s>>>(a.pw, a.ctas, a.V, p->d_weight, a.w_bf16);
     return launched();
 }
 

@@ -11,14 +11,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     return r;
 }
 template <int kVec>
-__device__ __forceinline__ void store_e4m3(uint8_t* to, const float* v) {
-    if (kVec == 1) {
-        *to = static_cast<uint8_t>(e4m3_pair(v[0], 0.f));
+__device__ __forceinline__ void store_e4m3(uint8_t* to, const float2* v, int k) {
+    if constexpr (kVec == 1) {
+        *to = static_cast<uint8_t>(e4m3_pair(k % 2 ? v->y : v->x, 0.f));
     } else {
-        uint32_t w[kVec / 4 > 0 ? kVec / 4 : 1];
+        uint32_t w[kVec / 4];
 #pragma unroll
-        for (int i = 0; i + 3 < kVec; i += 4) w[i / 4] = e4m3_pair(v[i], v[i + 1]) | e4m3_pair(v[i + 2], v[i + 3]) << 16;
-        if (kVec == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[kVec > 4 ? 1 : 0]);
+        for (int i = 0; i < kVec / 4; ++i) w[i] = e4m3_pair(v[2 * i].x, v[2 * i].y) | e4m3_pair(v[2 * i + 1].x, v[2 * i + 1].y) << 16;
+        if constexpr (kVec == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t*>(to) = w[0];
     }
 }
@@ -48,50 +48,80 @@ __device__ __forceinline__ Scale scale_of(float most, bool power) {
     return s;
 }
 
+// CTAs of 256 threads that an SM holds.
+template <typename R, int kVec, int kElements>
+constexpr int resident() { return kElements > 16 ? 1 : kVec == 1 ? 4 : kElements > 8 ? (sizeof(R) == 4 ? 2 : 3) : sizeof(R) == 4 ? 3 : 4; }
+
 template <typename X, typename R, int kVec, int NV, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) rn_fwd_kernel(const Args a) {
-    constexpr int E = NV * kVec;
+__global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>())) rn_fwd_kernel(const Args a) {
+    constexpr int P = NV * kVec / 2;
     __shared__ float2 red[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (blockDim.x >> 5) / a.warps, g = warp / a.warps;
     const auto pl = place<kVec, NV>(warp % a.warps);
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups, rounds = (a.T + step - 1) / step;
     const float inv_v = 1.f / a.V;
-    float w[E];
-    load_weight<kVec, NV>(w, a, pl);
+    Vec<X, kVec> x[NV], next_x[NV];
+    Vec<R, kVec> r[NV], next_r[NV];
+    auto load = [&](Vec<X, kVec> (&to_x)[NV], Vec<R, kVec> (&to_r)[NV], int64_t t) {
+        load_row<X, kVec, NV>(to_x, a.x, t * a.x_st, t < a.T, pl, a.V);
+        if (a.res) load_row<R, kVec, NV>(to_r, a.res, t * a.res_st, t < a.T, pl, a.V);
+    };
+    // the next row is on its way while this one is worked on, where a lane holds few elements (65536 x 4096 to 8 bits: 342 us,
+    // 446 without; a floor of 281)
+    constexpr bool kAhead = kVec > 1 && NV * kVec <= 16;
     int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+    if (kAhead) load(next_x, next_r, t);
+    constexpr bool kKeep = NV * kVec <= 16;
+    float2 w[kKeep ? P : 1];  // kept where a lane holds few elements
+#pragma unroll
+    for (int j = 0; j < (kKeep ? P : 0); ++j) w[j] = weight_pair<kVec, NV>(a, pl, j);
     for (int64_t n = 0; n < rounds; ++n, t += step) {
         const bool live = t < a.T;
-        Vec<X, kVec> x[NV];
-        Vec<R, kVec> r[NV];
-        load_row<X, kVec, NV>(x, a.x, t * a.x_st, live, pl, a.V);
-        if (a.res) load_row<R, kVec, NV>(r, a.res, t * a.res_st, live, pl, a.V);
-        float s[E], sum = 0.f, most = 0.f;
+        if (kAhead) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            s[e] = x[e / kVec].get(e % kVec);
-            if (a.res) s[e] = to_f(from_f<R>(s[e] + r[e / kVec].get(e % kVec)));
-            sum = fmaf(s[e], s[e], sum);
+            for (int k = 0; k < NV; ++k) {
+                x[k] = next_x[k];
+                r[k] = next_r[k];
+            }
+            load(next_x, next_r, t + step);
+        } else {
+            load(x, r, t);
         }
-        if (a.res && live) store_row<R, kVec, NV>(a.out, t * a.out_st, s, pl, a.V);
+        float2 s[P], sq = both(0.f);
+        if (a.res) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            s[e] *= w[e];
-            if (a.quant == LA_QUANT_ROW) most = max_nan(most, fabsf(s[e]));
+            for (int j = 0; j < P; ++j) {
+                set_pair<R, kVec, NV>(r, j, add2(pair_of<X, kVec, NV>(x, j), pair_of<R, kVec, NV>(r, j)));
+                s[j] = pair_of<R, kVec, NV>(r, j);
+            }
+            if (live) store_row<R, kVec, NV>(a.out, t * a.out_st, r, pl, a.V);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) s[j] = pair_of<X, kVec, NV>(x, j);
         }
+        float most = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            sq = fma2(s[j], s[j], sq);
+            s[j] = mul2(s[j], kKeep ? w[j] : weight_pair<kVec, NV>(a, pl, j));
+            if (a.quant == LA_QUANT_ROW) most = max_nan(most, max_nan(fabsf(s[j].x), fabsf(s[j].y)));
+        }
+        float sum = sq.x + sq.y;
         row_reduce<true>(sum, most, a.warps, red, static_cast<int>(n));
         const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps));
         if (!live) continue;  // a warp has one row
-#pragma unroll
-        for (int e = 0; e < E; ++e) s[e] *= rs;
         if (a.quant == LA_QUANT_NONE) {
-            store_row<X, kVec, NV>(a.y, t * a.y_st, s, pl, a.V);
+#pragma unroll
+            for (int j = 0; j < P; ++j) set_pair<X, kVec, NV>(x, j, mul2(s[j], both(rs)));
+            store_row<X, kVec, NV>(a.y, t * a.y_st, x, pl, a.V);
             continue;
         }
+        // y / scale as s w times (r / scale): a block's largest |y| is its largest |s w| times r
         if (a.quant == LA_QUANT_ROW) {
             const Scale sc = scale_of(most * rs, false);
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[e] *= sc.inverse;
+            for (int j = 0; j < P; ++j) s[j] = mul2(s[j], both(rs * sc.inverse));
             if (warp % a.warps == 0 && lane == 0) static_cast<float*>(a.scales)[t] = sc.scale;
         } else {
             // a block is kLanes lanes of kParts vectors
@@ -101,12 +131,13 @@ __global__ void __launch_bounds__(kMaxThreads) rn_fwd_kernel(const Args a) {
                 for (int k = 0; k < NV; k += kParts) {
                     float m = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kParts * kVec; ++i) m = max_nan(m, fabsf(s[k * kVec + i]));
+                    for (int e = k * kVec; e < (k + kParts) * kVec; ++e) m = max_nan(m, fabsf(e % 2 ? s[e / 2].y : s[e / 2].x));
 #pragma unroll
                     for (int off = 1; off < kLanes; off *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    const Scale sc = scale_of(m, width == 32);
+                    const Scale sc = scale_of(m * rs, width == 32);
+                    const float f = rs * sc.inverse;
 #pragma unroll
-                    for (int i = 0; i < kParts * kVec; ++i) s[k * kVec + i] *= sc.inverse;
+                    for (int e = k * kVec; e < (k + kParts) * kVec; ++e) (e % 2 ? s[e / 2].y : s[e / 2].x) *= f;
                     const int c = pl.column(k);
                     if (c < a.V && lane % kLanes == 0) {
                         const int64_t at = t * a.blocks + c / width;
@@ -121,7 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads) rn_fwd_kernel(const Args a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = pl.column(k);
-            if (c < a.V) store_e4m3<kVec>(static_cast<uint8_t*>(a.y) + t * a.y_st + c, s + k * kVec);
+            if (c < a.V) store_e4m3<kVec>(static_cast<uint8_t*>(a.y) + t * a.y_st + c, s + k * kVec / 2, k);
         }
     }
 }
@@ -130,9 +161,14 @@ struct Launch {
     template <typename X, typename R, int kVec, int NV>
     static la_status run(const Args& a, Shape sh, cudaStream_t s) {
         const int groups = sh.threads / 32 / sh.warps;
-        const int64_t grid = std::min<int64_t>((a.T + groups - 1) / groups, kSms * 4);
-        if (sh.threads == 512) rn_fwd_kernel<X, R, kVec, NV, 512><<<static_cast<unsigned>(grid), 512, 0, s>>>(a);
-        else rn_fwd_kernel<X, R, kVec, NV, 256><<<static_cast<unsigned>(grid), 256, 0, s>>>(a);
+        const int64_t grid = std::min<int64_t>((a.T + groups - 1) / groups, kSms * resident<R, kVec, NV * kVec>());
+        if constexpr (NV * kVec == 32) {
+            if (sh.threads == 512) {
+                rn_fwd_kernel<X, R, kVec, NV, 512><<<static_cast<unsigned>(grid), 512, 0, s>>>(a);
+                return launched();
+            }
+        }
+        rn_fwd_kernel<X, R, kVec, NV, 256><<<static_cast<unsigned>(grid), 256, 0, s>>>(a);
         return launched();
     }
 };
