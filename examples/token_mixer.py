@@ -1,6 +1,14 @@
-"""A token mixer from the library's operators: short convolution, recurrence, gated group norm.
+"""Token mixers from the library's operators: short convolution, recurrence, gated group norm,
 
     h -> projection -> short_conv -> gdn_attention | gated_linear_recurrence -> group_norm (gate z) -> projection
+
+or short convolution and selective scan,
+
+    h -> projection -> short_conv -> projections of steps, inputs and outputs -> selective_scan (gate z) -> projection
+
+and stacks of them on a residual stream,
+
+    y, stream = residual_norm(h, weight, stream);  h = mixer(y)
 
 over packed variable-length sequences for training, and with state pools for serving (a prefill that leaves every
 sequence's state in its slot, then one token a step).  Run as a program it trains a small mixer for a few steps and
@@ -96,6 +104,90 @@ class TokenMixer(torch.nn.Module):
         return self._norm(o, h)
 
 
+class SelectiveMixer(torch.nn.Module):
+    """The selective scan with its convolution, `states` states a channel; the steps' projection is of low rank."""
+
+    def __init__(self, dim: int, inner: int, states: int = 16, taps: int = 4, device="cuda"):
+        super().__init__()
+        self.inner, self.states, self.taps, self.rank = inner, states, taps, max(1, dim // 16)
+        kw = dict(bias=False, device=device, dtype=torch.bfloat16)
+        self.proj_in = torch.nn.Linear(dim, 2 * inner, **kw)
+        self.proj_x = torch.nn.Linear(inner, self.rank + 2 * states, **kw)
+        self.proj_dt = torch.nn.Linear(self.rank, inner, **kw)
+        self.proj_out = torch.nn.Linear(inner, dim, **kw)
+        self.conv = torch.nn.Parameter(torch.randn(inner, taps, device=device) * taps ** -0.5)
+        self.a_log = torch.nn.Parameter(torch.arange(1, states + 1, device=device).float().log().repeat(inner, 1))
+        self.skip = torch.nn.Parameter(torch.ones(inner, device=device))
+        self.dt_bias = torch.nn.Parameter(torch.full((inner,), -3.0, device=device))
+
+    def _scan_inputs(self, x):
+        low, b, c = self.proj_x(x).split([self.rank, self.states, self.states], 1)
+        return x, self.proj_dt(low), -torch.exp(self.a_log), b, c
+
+    def forward(self, h, cu_seqlens):
+        """h [T, dim] over packed sequences."""
+        x, z = self.proj_in(h).split(self.inner, 1)
+        x, _ = la.short_conv(x, self.conv, cu_seqlens)
+        y, _ = la.selective_scan(*self._scan_inputs(x), cu_seqlens, skip=self.skip, z=z, dt_bias=self.dt_bias, dt_softplus=True)
+        return self.proj_out(y)
+
+    def pools(self, slots: int) -> dict:
+        dev = self.conv.device
+        return {"conv": torch.zeros(slots, self.taps - 1, self.inner, dtype=torch.bfloat16, device=dev),
+                "state": torch.zeros(slots, self.inner, self.states, device=dev)}
+
+    @torch.no_grad()
+    def prefill(self, h, cu_seqlens, pools, slots):
+        x, z = self.proj_in(h).split(self.inner, 1)
+        x, _ = la.sconv_fwd(x, self.conv, cu_seqlens, initial_state=pools["conv"], state_indices=slots)
+        y, _, _ = la.ssm_fwd(*self._scan_inputs(x), cu_seqlens, skip=self.skip, z=z, dt_bias=self.dt_bias, dt_softplus=True,
+                             initial_state=pools["state"], state_indices=slots)
+        return self.proj_out(y)
+
+    @torch.no_grad()
+    def step(self, h, pools, slots):
+        x, z = self.proj_in(h).split(self.inner, 1)
+        x = la.sconv_decode(x, self.conv, pools["conv"], state_indices=slots)
+        y = la.ssm_decode(*self._scan_inputs(x), pools["state"], state_indices=slots, skip=self.skip, z=z, dt_bias=self.dt_bias,
+                          dt_softplus=True)
+        return self.proj_out(y)
+
+
+class Stack(torch.nn.Module):
+    """Mixers one after the other on a residual stream in 32 bits, each behind a norm of the stream, with one at the end."""
+
+    def __init__(self, mixers, dim: int, device="cuda"):
+        super().__init__()
+        self.mixers = torch.nn.ModuleList(mixers)
+        self.norms = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(dim, device=device)) for _ in range(len(mixers) + 1)])
+
+    def forward(self, h, cu_seqlens):
+        stream = torch.zeros_like(h, dtype=torch.float32)
+        for mixer, norm in zip(self.mixers, self.norms):
+            y, stream = la.residual_norm(h, norm, stream)
+            h = mixer(y, cu_seqlens)
+        return la.residual_norm(h, self.norms[-1], stream)[0]
+
+    def pools(self, slots: int) -> list:
+        return [m.pools(slots) for m in self.mixers]
+
+    def _serve(self, h, each):
+        stream = torch.zeros_like(h, dtype=torch.float32)
+        for i, norm in enumerate(self.norms):
+            h, stream, _ = la.rn_fwd(h, norm, stream, residual_out=stream)
+            if i < len(self.mixers):
+                h = each(i, h)
+        return h
+
+    @torch.no_grad()
+    def prefill(self, h, cu_seqlens, pools, slots):
+        return self._serve(h, lambda i, y: self.mixers[i].prefill(y, cu_seqlens, pools[i], slots))
+
+    @torch.no_grad()
+    def step(self, h, pools, slots):
+        return self._serve(h, lambda i, y: self.mixers[i].step(y, pools[i], slots))
+
+
 def train(mixer, h, target, cu_seqlens, steps: int = 20, lr: float = 3e-3):
     """Least squares towards `target`; returns the loss before every step."""
     opt = torch.optim.Adam(mixer.parameters(), lr=lr)
@@ -131,8 +223,9 @@ def main():
     lengths = [300, 17, 129, 64]
     cu = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
     h = torch.randn(sum(lengths), 256, device="cuda").to(torch.bfloat16)
-    for kind in ("delta", "diagonal"):
-        mixer = TokenMixer(256, 4, 64, kind)
+    for kind in ("delta", "diagonal", "selective", "stack"):
+        mixer = TokenMixer(256, 4, 64, kind) if kind in ("delta", "diagonal") else SelectiveMixer(256, 512) if kind == "selective" \
+            else Stack([TokenMixer(256, 4, 64), SelectiveMixer(256, 512)], 256)
         target = 0.5 * torch.roll(h, 1, 0).float()
         losses = train(mixer, h, target, cu)
         print(f"{kind}: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps, "

@@ -121,9 +121,10 @@ struct Launch {
         const unsigned grid = static_cast<unsigned>(a.ctas);
         if constexpr (NV * kVec == 32) {
             if (sh.threads == 512) {
-                static const cudaError_t opted =
-                    cudaFuncSetAttribute(rn_bwd_kernel<X, R, kVec, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV * 4);
-                if (opted != cudaSuccess) return LA_ERR_CUDA;
+                if (cudaFuncSetAttribute(rn_bwd_kernel<X, R, kVec, NV, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV * 4) != cudaSuccess) {
+                    (void)cudaGetLastError();
+                    return LA_ERR_CUDA;
+                }
                 rn_bwd_kernel<X, R, kVec, NV, 512><<<grid, 512, smem, s>>>(a);
                 return launched();
             }

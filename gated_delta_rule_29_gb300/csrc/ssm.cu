@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) ssm_decode_kernel(const Args a) {
 constexpr int kSeqs = 4, kDepth = 4;
 
 template <typename X, int Q>
-__global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args a, int groups) {
+__global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args a, int64_t groups) {
     __shared__ __align__(16) float4 ring[kDepth][kSeqs][kThreads];
     constexpr int kShare = Q < kSeqs ? Q : kSeqs, kOwn = kSeqs / kShare;  // lanes that share the sequences; sequences of a lane
     const int q = threadIdx.x % Q, s = 4 * q, mine = q % kShare;          // this lane's: mine, mine + kShare, ...
@@ -70,11 +70,11 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
     const float4 A = load_states(a.A, 0, a, d, s, live, 0);
 
     // the slots of a group's sequences as they are given; which of them are there is seen when they are used
-    auto slots_of = [&](int (&slot)[kSeqs], int group) {
+    auto slots_of = [&](int (&slot)[kSeqs], int64_t group) {
 #pragma unroll
         for (int i = 0; i < kSeqs; ++i) {
-            const int n = group * kSeqs + i;
-            slot[i] = n < a.N ? (a.idx ? a.idx[n] : n) : -1;
+            const int64_t n = group * kSeqs + i;
+            slot[i] = n < a.N ? (a.idx ? a.idx[n] : static_cast<int>(n)) : -1;
         }
     };
     auto request = [&](int stage, const int (&slot)[kSeqs]) {
@@ -87,32 +87,33 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
         Packed<X, 4> b[kSeqs], c[kSeqs];
         X x[kOwn], dt[kOwn], z[kOwn];
     };
-    auto inputs_of = [&](int group) {
+    auto inputs_of = [&](int64_t group) {
         Inputs t;
 #pragma unroll
         for (int i = 0; i < kSeqs; ++i) {
-            const int64_t n = min(group * kSeqs + i, a.N - 1);
+            const int64_t n = min(group * kSeqs + i, int64_t(a.N) - 1);
             t.b[i].load(static_cast<const X*>(a.b) + n * a.b_st + j * a.b_sg + min(s, a.S - 4));
             t.c[i].load(static_cast<const X*>(a.c) + n * a.c_st + j * a.c_sg + min(s, a.S - 4));
         }
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
-            const int64_t n = min(group * kSeqs + mine + k * kShare, a.N - 1);
+            const int64_t n = min(group * kSeqs + mine + k * kShare, int64_t(a.N) - 1);
             t.x[k] = static_cast<const X*>(a.x)[n * a.x_st + dl];
             t.dt[k] = static_cast<const X*>(a.dt)[n * a.dt_st + dl];
             t.z[k] = a.z ? static_cast<const X*>(a.z)[n * a.z_st + dl] : from_f<X>(0.f);
         }
         return t;
     };
-    const int step = gridDim.y;
-    int group = blockIdx.y, slot[kDepth][kSeqs];
+    const int64_t step = gridDim.y;
+    int64_t group = blockIdx.y;
+    int slot[kDepth][kSeqs];
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) slots_of(slot[k], group + k * step);
 #pragma unroll
     for (int k = 0; k < kDepth - 1; ++k) request(k, slot[k]);
     Inputs in = inputs_of(group);
-    for (int n = 0; group < groups; ++n, group += step) {
-        request((n + kDepth - 1) % kDepth, slot[kDepth - 1]);
+    for (int64_t n = 0; group < groups; ++n, group += step) {
+        request(static_cast<int>((n + kDepth - 1) % kDepth), slot[kDepth - 1]);
         int here[kSeqs];
 #pragma unroll
         for (int i = 0; i < kSeqs; ++i) {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
                 }
             y = fmaf(skip, x[k], y);
             if (a.z) y *= act_fwd(LA_ACT_SILU, to_f(now.z[k]));
-            if (there && d < a.D && q < kShare) static_cast<X*>(a.y)[(static_cast<int64_t>(group) * kSeqs + mine + k * kShare) * a.y_st + d] = from_f<X>(y);
+            if (there && d < a.D && q < kShare) static_cast<X*>(a.y)[(group * kSeqs + mine + k * kShare) * a.y_st + d] = from_f<X>(y);
         }
     }
     cp_async_wait<0>();
@@ -175,8 +176,9 @@ la_status decode(const Args& a, cudaStream_t s) {
 }
 template <typename X, int Q>
 la_status decode_many(const Args& a, cudaStream_t s) {
-    const int tiles = (a.D + kThreads / Q - 1) / (kThreads / Q), groups = (a.N + kSeqs - 1) / kSeqs;
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(std::max(1, groups / 8)));
+    const int tiles = (a.D + kThreads / Q - 1) / (kThreads / Q);
+    const int64_t groups = (int64_t(a.N) + kSeqs - 1) / kSeqs;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(std::min<int64_t>(65535, std::max<int64_t>(1, groups / 8))));
     ssm_decode_many_kernel<X, Q><<<grid, kThreads, 0, s>>>(a, groups);
     return launched();
 }

@@ -503,9 +503,10 @@ template <typename X, int Q, bool kGate>
 la_status blocks(Args& a, cudaStream_t s) {
     constexpr int kTile = Work<X, Q>::kTile, kSmem = sizeof(Work<X, Q>);
     a.tiles_pg = (a.Dg + kTile - 1) / kTile;
-    static const cudaError_t opted =
-        cudaFuncSetAttribute(ssm_block_kernel<X, Q, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (opted != cudaSuccess) return LA_ERR_CUDA;
+    if (cudaFuncSetAttribute(ssm_block_kernel<X, Q, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LA_ERR_CUDA;
+    }
     ssm_block_kernel<X, Q, kGate><<<static_cast<unsigned>(a.parts * a.tiles_pg * a.G), kThreads, kSmem, s>>>(a);
     return LA_OK;
 }
