@@ -290,9 +290,9 @@ def rn_bwd(s: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, *, d_residua
 # ------------------------------------------------------------------ autograd
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints):
+    def forward(ctx, x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints, time_block):
         y, fin, ck = ssm_fwd(x, dt, a, b, c, cu_seqlens, skip=skip, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus,
-                             initial_state=initial_state, output_checkpoints=save_checkpoints)
+                             initial_state=initial_state, output_checkpoints=save_checkpoints, time_block=time_block)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, ck)
         ctx.dt_softplus = dt_softplus
@@ -307,18 +307,19 @@ class _SelectiveScan(torch.autograd.Function):
         dx, ddt, da, db, dc, d_skip, dz, d_bias, ds0 = ssm_bwd(
             x, dt, a, b, c, cu, _cotangent(dy, x), skip=skip, z=z, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
             initial_state=s0, d_final_state=d_fin, checkpoints=ck)
-        return dx, ddt, da, db, dc, None, d_skip, dz, d_bias, None if s0 is None else ds0.to(s0.dtype), None, None
+        return dx, ddt, da, db, dc, None, d_skip, dz, d_bias, None if s0 is None else ds0.to(s0.dtype), None, None, None
 
 
 def selective_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
                    cu_seqlens: torch.Tensor, *, skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
                    dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
-                   initial_state: Optional[torch.Tensor] = None, save_checkpoints: bool = True
+                   initial_state: Optional[torch.Tensor] = None, save_checkpoints: bool = True, time_block: int = 0
                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable ssm_fwd: returns (y, final_state); gradients flow to x, dt, a, b, c, skip, z, dt_bias and
     initial_state.  save_checkpoints keeps the state entering every 16 tokens (D * S * 4 bytes each) for the backward;
-    without them it recomputes them."""
-    return _SelectiveScan.apply(x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints)
+    without them it recomputes them (in the blocks of time_block 0)."""
+    return _SelectiveScan.apply(x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints,
+                                time_block)
 
 
 class _ResidualNorm(torch.autograd.Function):

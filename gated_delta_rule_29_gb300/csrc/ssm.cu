@@ -311,7 +311,6 @@ la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream) {
     set_table(a, p->workspace, a.shift);
     a.idx = p->state_indices; a.pool = p->state_pool_size;
     a.y = p->y; a.y_st = p->y_stride_t; a.fin = p->final_state; a.ckpt = p->checkpoints;
-    a.vec = a.vec && wide_rows(a, a.y, a.y_st, p->x_dtype);
     a.svec = a.svec && aligned_to(a.fin, 16) && aligned_to(a.ckpt, 16);
     if (a.N == 0) return LA_OK;
     return run_fwd(a, p->x_dtype, static_cast<cudaStream_t>(stream));

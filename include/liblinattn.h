@@ -817,7 +817,8 @@ la_status sconv_decode(const la_sconv_decode_params* p, void* stream);
 /* ===========================================================================
  * Operators of a state-space block: the selective state space scan (ssm_*) and
  * the root-mean-square norm with the residual's addition (rn_*).  They follow the
- * conventions of the token-mixer operators above.
+ * conventions of the token-mixer operators above; batch invariance of the scan needs
+ * a given time_block.
  * ======================================================================== */
 
 /* Parameters of ssm_fwd.  Strides are in elements; x, dt, z, b, c and y have one type. */
@@ -907,8 +908,9 @@ typedef struct la_ssm_bwd_params {
 
 /*
  * ssm_bwd -- gradients of L = sum(dy * y) + sum(d_final_state * final_state).  The gradients
- * of a sequence's own inputs do not depend on the batch around it; sums over channels and
- * over the batch run in an order fixed by the shape.  dx, ddt and dz must share no
+ * of a sequence's own inputs do not depend on the batch around it where its checkpoints do
+ * not (recomputed ones are those of time_block 0); sums over channels and over the batch run
+ * in an order fixed by the shape.  dx, ddt and dz must share no
  * memory with each other or an input.
  */
 la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream);

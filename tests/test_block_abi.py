@@ -104,3 +104,13 @@ def test_wrappers_refuse_cpu_tensors():
                  lambda: la.rn_fwd(x, x[0]), lambda: la.rn_bwd(x, x[0], x)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_a_stream_of_another_device_is_refused_by_keyword():
+    """Also where the first operand is not called x."""
+    import types
+
+    from test_mixer_device import CudaOperand
+    s = torch.zeros(4, 8).as_subclass(CudaOperand)
+    with pytest.raises(ValueError, match="stream must be on cuda:0"):
+        la.rn_bwd(s=s, weight=s[0], dy=s, stream=types.SimpleNamespace(device=torch.device("cuda", 1)))

@@ -118,7 +118,7 @@ def test_autograd_forms():
     for save in (True, False):
         v = {k: t[k].clone().requires_grad_() for k in names}
         y, fin = la.selective_scan(v["x"], v["dt"], v["a"], v["b"], v["c"], cu, skip=v["skip"], z=v["z"], dt_bias=v["bias"],
-                                   dt_softplus=True, initial_state=v["s0"], save_checkpoints=save)
+                                   dt_softplus=True, initial_state=v["s0"], save_checkpoints=save, time_block=64)
         (y.float() * t["dy"].float()).sum().backward(retain_graph=True)
         want = la.ssm_bwd(t["x"], t["dt"], t["a"], t["b"], t["c"], cu, t["dy"], skip=t["skip"], z=t["z"], dt_bias=t["bias"],
                           dt_softplus=True, initial_state=t["s0"])
