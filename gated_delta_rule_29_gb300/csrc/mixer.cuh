@@ -263,19 +263,29 @@ inline bool good_rows(const void* p, int64_t stride, int64_t rows, int64_t D, in
     if (stride < 0) return false;
     return !out || rows == 1 || stride >= D;
 }
-// Whether the rows of two operands of D channels share memory: for sure where their strides are the same, and where they
-// differ as far as the first rows tell.
-inline bool rows_meet(const void* a, int64_t a_st, const void* b, int64_t b_st, int64_t rows, int64_t D, int32_t dtype) {
+// Whether `rows` rows of a_row bytes, a_st bytes apart, share memory with rows of b_row bytes: for sure where the strides are
+// the same, and where they differ as far as the first rows tell.
+inline bool bytes_meet(const void* a, int64_t a_st, int64_t a_row, const void* b, int64_t b_st, int64_t b_row, int64_t rows) {
     if (rows == 0) return false;
-    const int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)), es = dtype_size(dtype),
-                  row = D * es, st = a_st * es;
-    if (rows == 1 || a_st != b_st || st == 0) return off > -row && off < row;
-    int64_t q = off / st, r = off % st;  // b's first row is r bytes after a's row q
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+    if (rows == 1 || a_st != b_st || a_st == 0) return off > -b_row && off < a_row;
+    int64_t q = off / a_st, r = off % a_st;  // b's first row is r bytes after a's row q
     if (r < 0) {
-        r += st;
+        r += a_st;
         --q;
     }
-    return (r < row && q < rows && q > -rows) || (st - r < row && q + 1 < rows && q + 1 > -rows);
+    return (r < a_row && q < rows && q > -rows) || (a_st - r < b_row && q + 1 < rows && q + 1 > -rows);
+}
+// The same of two operands of D channels.
+inline bool rows_meet(const void* a, int64_t a_st, const void* b, int64_t b_st, int64_t rows, int64_t D, int32_t dtype) {
+    const int64_t es = dtype_size(dtype);
+    return bytes_meet(a, a_st * es, D * es, b, b_st * es, D * es, rows);
+}
+// Whether a result of rows of D channels shares memory with an optional operand other than by lying exactly over it, element by
+// element.  out_size, in_size: bytes of an element.
+inline bool clashes(const void* out, int64_t out_st, int64_t out_size, const void* in, int64_t in_st, int64_t in_size, int64_t rows, int64_t D) {
+    if (!in || (out == in && out_size == in_size && (out_st == in_st || rows == 1))) return false;
+    return bytes_meet(out, out_st * out_size, D * out_size, in, in_st * in_size, D * in_size, rows);
 }
 // An optional contiguous operand.
 inline bool good_optional(const void* p, int32_t dtype) { return !p || aligned_to(p, dtype_size(dtype)); }

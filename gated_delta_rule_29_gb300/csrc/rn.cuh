@@ -194,8 +194,8 @@ la_status dispatch(Args& a, int32_t xd, int32_t rd, bool wide, cudaStream_t s) {
 }
 
 // Whether rows of V elements of `size` bytes take accesses of kVec elements, of at most 16 bytes each.
-inline bool wide_rows(const void* p, int64_t st, int64_t T, int size, int vec) {
-    const int bytes = std::min(16, vec * size);
+inline bool wide_rows(const void* p, int64_t st, int64_t T, int64_t size, int vec) {
+    const int64_t bytes = std::min<int64_t>(16, vec * size);
     return !p || (aligned_to(p, bytes) && (T <= 1 || st * size % bytes == 0));
 }
 

@@ -159,6 +159,14 @@ la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
         (p->ds && !good_rows(p->ds, p->ds_stride_t, p->T, p->V, p->s_dtype, true)))
         return LA_ERR_INVALID_ARG;
     if ((p->T > 0 && !p->dx && !p->ds) || !p->d_weight || !aligned_to(p->d_weight, dtype_size(p->weight_dtype))) return LA_ERR_INVALID_ARG;
+    const int xs = dtype_size(p->x_dtype), rs = dtype_size(p->s_dtype);
+    auto over = [&](const void* out, int64_t st, int size) {
+        return out && (clashes(out, st, size, p->s, p->s_stride_t, rs, p->T, p->V) || clashes(out, st, size, p->dy, p->dy_stride_t, xs, p->T, p->V) ||
+                       clashes(out, st, size, p->d_residual, p->d_residual_stride_t, rs, p->T, p->V));
+    };
+    if (over(p->dx, p->dx_stride_t, xs) || over(p->ds, p->ds_stride_t, rs) ||
+        (p->dx && p->ds && bytes_meet(p->dx, p->dx_stride_t * xs, int64_t(p->V) * xs, p->ds, p->ds_stride_t * rs, int64_t(p->V) * rs, p->T)))
+        return LA_ERR_INVALID_ARG;
     if ((st = check_workspace(p->workspace, p->workspace_bytes, la_rn_bwd_workspace_bytes(p->T, p->V))) != LA_OK) return st;
     Args a = {};
     a.x = p->s; a.x_st = p->s_stride_t; a.dy = p->dy; a.dy_st = p->dy_stride_t; a.dres = p->d_residual; a.dres_st = p->d_residual_stride_t;
@@ -166,7 +174,7 @@ la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
     a.T = p->T; a.V = p->V; a.eps = p->eps;
     a.y = p->dx; a.y_st = p->dx_stride_t; a.ds = p->ds; a.ds_st = p->ds_stride_t;
     a.pw = static_cast<float*>(p->workspace);
-    const int vec = 16 / dtype_size(p->x_dtype), xs = dtype_size(p->x_dtype), rs = dtype_size(p->s_dtype);
+    const int vec = 16 / xs;
     const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, rs, vec) && wide_rows(a.dy, a.dy_st, a.T, xs, vec) && wide_rows(a.dres, a.dres_st, a.T, rs, vec) &&
                       wide_rows(a.y, a.y_st, a.T, xs, vec) && wide_rows(a.ds, a.ds_st, a.T, rs, vec);
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -202,6 +202,13 @@ la_status rn_fwd(const la_rn_fwd_params* p, void* stream) {
     if (p->T > 0 && (!p->y || p->y_stride_t < 0 || (p->T > 1 && p->y_stride_t < p->V) || (!eight && !aligned_to(p->y, dtype_size(p->x_dtype)))))
         return LA_ERR_INVALID_ARG;
     if (eight && p->T > 0 && (!p->scales || (p->quantize != LA_QUANT_MX && !aligned_to(p->scales, 4)))) return LA_ERR_INVALID_ARG;
+    const int64_t xs = dtype_size(p->x_dtype), ss = dtype_size(rd), ys = eight ? 1 : xs;
+    if (clashes(p->y, p->y_stride_t, ys, p->x, p->x_stride_t, xs, p->T, p->V)) return LA_ERR_INVALID_ARG;
+    if (p->residual && (clashes(p->y, p->y_stride_t, ys, p->residual, p->residual_stride_t, ss, p->T, p->V) ||
+                        clashes(p->residual_out, p->residual_out_stride_t, ss, p->x, p->x_stride_t, xs, p->T, p->V) ||
+                        clashes(p->residual_out, p->residual_out_stride_t, ss, p->residual, p->residual_stride_t, ss, p->T, p->V) ||
+                        bytes_meet(p->y, p->y_stride_t * ys, p->V * ys, p->residual_out, p->residual_out_stride_t * ss, p->V * ss, p->T)))
+        return LA_ERR_INVALID_ARG;
     if (p->T == 0) return LA_OK;
     Args a = {};
     a.x = p->x; a.x_st = p->x_stride_t; a.res = p->residual; a.res_st = p->residual_stride_t;
@@ -209,9 +216,9 @@ la_status rn_fwd(const la_rn_fwd_params* p, void* stream) {
     a.T = p->T; a.V = p->V; a.eps = p->eps; a.quant = p->quantize; a.blocks = la_rn_scale_blocks(p->V, p->quantize);
     a.y = p->y; a.y_st = p->y_stride_t; a.out = p->residual ? p->residual_out : nullptr; a.out_st = p->residual_out_stride_t;
     a.scales = p->scales;
-    const int vec = 16 / dtype_size(p->x_dtype);
-    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, dtype_size(p->x_dtype), vec) && wide_rows(a.res, a.res_st, a.T, dtype_size(rd), vec) &&
-                      wide_rows(a.out, a.out_st, a.T, dtype_size(rd), vec) && wide_rows(a.y, a.y_st, a.T, eight ? 1 : dtype_size(p->x_dtype), vec);
+    const int vec = 16 / static_cast<int>(xs);
+    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, xs, vec) && wide_rows(a.res, a.res_st, a.T, ss, vec) &&
+                      wide_rows(a.out, a.out_st, a.T, ss, vec) && wide_rows(a.y, a.y_st, a.T, ys, vec);
     return dispatch<Launch>(a, p->x_dtype, rd, wide, static_cast<cudaStream_t>(stream));
 }
 

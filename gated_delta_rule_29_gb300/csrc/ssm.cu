@@ -208,10 +208,12 @@ bool good_states(const void* p, int64_t st, int64_t sg, int64_t rows, int32_t dt
     return rows == 0 || (p && aligned_to(p, dtype_size(dtype)) && st >= 0 && sg >= 0);
 }
 
-// Whether a result's rows lie over an operand's other than exactly over it, element by element.
-bool clashes(const void* out, int64_t out_st, const void* in, int64_t in_st, int64_t rows, int64_t D, int32_t dtype) {
-    if (!in || (out == in && (out_st == in_st || rows == 1))) return false;
-    return rows_meet(out, out_st, in, in_st, rows, D, dtype);
+// Whether y shares memory with x, dt or z other than by lying exactly over one of them.
+template <typename P>
+bool result_clashes(const P* p, int64_t rows, int64_t y_st, int64_t x_st, int64_t dt_st, int64_t z_st) {
+    const int64_t es = dtype_size(p->x_dtype);
+    auto over = [&](const void* in, int64_t st) { return clashes(p->y, y_st, es, in, st, es, rows, p->D); };
+    return over(p->x, x_st) || over(p->dt, dt_st) || over(p->z, z_st);
 }
 
 template <typename P>
@@ -298,9 +300,7 @@ la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream) {
     if (!good_rows(p->y, p->y_stride_t, p->T, p->D, p->x_dtype, true) || !good_optional(p->initial_state, p->initial_state_dtype) ||
         !good_optional(p->final_state, LA_DTYPE_F32) || !good_optional(p->checkpoints, LA_DTYPE_F32) || !good_time_block(p->time_block))
         return LA_ERR_INVALID_ARG;
-    if (clashes(p->y, p->y_stride_t, p->x, p->x_stride_t, p->T, p->D, p->x_dtype) || clashes(p->y, p->y_stride_t, p->dt, p->dt_stride_t, p->T, p->D, p->x_dtype) ||
-        clashes(p->y, p->y_stride_t, p->z, p->z_stride_t, p->T, p->D, p->x_dtype))
-        return LA_ERR_INVALID_ARG;
+    if (result_clashes(p, p->T, p->y_stride_t, p->x_stride_t, p->dt_stride_t, p->z_stride_t)) return LA_ERR_INVALID_ARG;
     if (p->state_indices && (!aligned_to(p->state_indices, 4) || !p->initial_state || p->final_state || p->state_pool_size <= 0))
         return LA_ERR_INVALID_ARG;
     Args a = {};
@@ -332,6 +332,16 @@ la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream) {
         !good_optional(p->checkpoints, LA_DTYPE_F32) || !good_optional(p->d_final_state, LA_DTYPE_F32) ||
         !good_optional(p->d_initial_state, LA_DTYPE_F32))
         return LA_ERR_INVALID_ARG;
+    // no gradient may lie over an input, which other warps still read, or over another gradient
+    const struct {
+        const void* p;
+        int64_t st;
+    } rows_of[] = {{p->dx, p->dx_stride_t}, {p->ddt, p->ddt_stride_t}, {p->z ? p->dz : nullptr, p->dz_stride_t}, {p->x, p->x_stride_t},
+                   {p->dt, p->dt_stride_t}, {p->dy, p->dy_stride_t}, {p->z, p->z_stride_t}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (rows_of[i].p && rows_of[j].p && rows_meet(rows_of[i].p, rows_of[i].st, rows_of[j].p, rows_of[j].st, p->T, p->D, xd))
+                return LA_ERR_INVALID_ARG;
     const size_t need = la_ssm_bwd_workspace_bytes(p->T, p->N, p->D, p->S, p->G, p->checkpoints != nullptr);
     if ((st = check_workspace(p->workspace, p->workspace_bytes, need)) != LA_OK) return st;
     Args a = {};
@@ -366,6 +376,7 @@ la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream) {
         f.shift = fwd_shift(a.T, a.D, a.S, a.G, 0);
         set_table(f, ws, f.shift);
         f.y = nullptr;
+        f.z = nullptr;
         if ((st = run_fwd(f, xd, s)) != LA_OK) return st;
     }
     a.table = table;
@@ -380,7 +391,9 @@ la_status ssm_decode(const la_ssm_decode_params* p, void* stream) {
     if (!known_dtype(p->state_dtype)) return LA_ERR_UNSUPPORTED;
     if (!p->state_pool || !good_optional(p->state_pool, p->state_dtype) || p->state_pool_size <= 0) return LA_ERR_INVALID_ARG;
     if (p->state_indices ? !aligned_to(p->state_indices, 4) : p->state_pool_size < p->N) return LA_ERR_INVALID_ARG;
-    if (!good_rows(p->y, p->y_stride_n, p->N, p->D, p->x_dtype, true)) return LA_ERR_INVALID_ARG;
+    if (!good_rows(p->y, p->y_stride_n, p->N, p->D, p->x_dtype, true) ||
+        result_clashes(p, p->N, p->y_stride_n, p->x_stride_n, p->dt_stride_n, p->z_stride_n))
+        return LA_ERR_INVALID_ARG;
     Args a = {};
     fill(a, p, p->N, p->x_stride_n, p->dt_stride_n, p->z_stride_n, p->b_stride_n, p->c_stride_n);
     a.s0 = p->state_pool; a.s0_bf16 = p->state_dtype == LA_DTYPE_BF16;

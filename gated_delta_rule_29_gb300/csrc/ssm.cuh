@@ -195,9 +195,9 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// A thread's part of stages of kTokens rows of n elements, kPitch apart and padded with zeros to kWidth in shared memory: the
-// same columns of every kRows-th row.
-template <typename X, int kWidth, int kThreads, int kTokens, int kPitch = kWidth>
+// A thread's part of stages of kTokens rows of n elements, padded with zeros to kWidth in shared memory: the same columns of
+// every kRows-th row.
+template <typename X, int kWidth, int kThreads, int kTokens>
 struct Rows {
     static constexpr int kVec = 16 / static_cast<int>(sizeof(X)), kVecs = kWidth / kVec, kRows = kThreads / kVecs;
     const X* from;  // this thread's column of its first row
@@ -213,10 +213,10 @@ struct Rows {
     // Rows from t on, of which `rows` are left.
     __device__ __forceinline__ void stage(X* to, int t, int rows) const {
         const int i = threadIdx.x % kThreads, r = i / kVecs;
-        to += r * kPitch + i % kVecs * kVec;
+        to += r * kWidth + i % kVecs * kVec;
         const X* p = from + t * stride;
 #pragma unroll
-        for (int j = 0; j < (kTokens + kRows - 1) / kRows; ++j, to += kRows * kPitch, p += kRows * stride) {
+        for (int j = 0; j < (kTokens + kRows - 1) / kRows; ++j, to += kRows * kWidth, p += kRows * stride) {
             if (r + j * kRows >= min(rows, kTokens)) continue;
             if (wide) cp_async16(to, p);
             else

@@ -910,8 +910,8 @@ typedef struct la_ssm_bwd_params {
  * ssm_bwd -- gradients of L = sum(dy * y) + sum(d_final_state * final_state).  The gradients
  * of a sequence's own inputs do not depend on the batch around it where its checkpoints do
  * not (recomputed ones are those of time_block 0); sums over channels and over the batch run
- * in an order fixed by the shape.  dx, ddt and dz must share no
- * memory with each other or an input.
+ * in an order fixed by the shape.  dx, ddt and dz must share no memory with each other, x, dt, z or dy
+ * (LA_ERR_INVALID_ARG), nor with b or c.
  */
 la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream);
 
@@ -936,7 +936,8 @@ typedef struct la_ssm_decode_params {
     int32_t* status;
 } la_ssm_decode_params;
 
-/* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode). */
+/* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode: no two sequences of one slot).  A sequence
+ * of a bad slot leaves its y as it was.  y may be x, dt or z itself, as in ssm_fwd. */
 la_status ssm_decode(const la_ssm_decode_params* p, void* stream);
 
 /* Rows of ssm_fwd's checkpoints buffer: T / 16 + N (0 for invalid arguments). */
@@ -975,7 +976,8 @@ typedef struct la_rn_fwd_params {
  * In 8 bits y is e4m3(y / scale) with, m being a block's largest |y| and at least
  * 2^-100, scale = m / 448, or for LA_QUANT_MX the least power of two with m <= 448
  * scale.  A block whose largest value is not finite has a scale of NaN.
- * residual_out may be residual or x itself; no other results share memory with an input.
+ * residual_out may be residual or x itself, and y may be x, or residual where that is not residual_out (same address,
+ * stride and type).  Results share no memory with an input or each other otherwise (LA_ERR_INVALID_ARG as for sconv_fwd).
  */
 la_status rn_fwd(const la_rn_fwd_params* p, void* stream);
 
@@ -999,8 +1001,9 @@ typedef struct la_rn_bwd_params {
 } la_rn_bwd_params;
 
 /* rn_bwd -- gradients of L = sum(dy * y) + sum(d_residual * residual_out), of 8-bit results as if they were y itself.
- * At least one of dx and ds is given; each may be dy, d_residual or s itself.  The sum over tokens runs in an order fixed
- * by the shape. */
+ * At least one of dx and ds is given; each may be dy, d_residual or s itself (same address, stride and type), and they share
+ * no memory with an input or each other otherwise (LA_ERR_INVALID_ARG).  The sum over tokens runs in an order fixed by the
+ * shape. */
 la_status rn_bwd(const la_rn_bwd_params* p, void* stream);
 
 size_t la_rn_bwd_workspace_bytes(int64_t T, int32_t V);

@@ -83,6 +83,34 @@ def test_refusals(fn, over, code):
     assert getattr(B.load(), fn)(None, None) == INV
 
 
+NEAR = FAKE + 64  # a row is 128 bytes of bf16
+SHARED = {
+    "ssm_decode": [dict(y=NEAR), dict(y=FAKE, y_stride_n=128), dict(y=FAKE + 128), dict(z=FAR + 128, z_stride_n=64)],
+    "ssm_bwd": [dict(dx=FAKE), dict(dx=NEAR), dict(ddt=FAKE + 128), dict(ddt=FAR), dict(ddt=FAR + 64),
+                dict(z=FAKE, z_stride_t=64, dz=FAKE, dz_stride_t=64), dict(z=FAKE, z_stride_t=64, dz=FAR, dz_stride_t=64),
+                dict(dy=FAR + 128)],
+    "rn_fwd": [dict(y=NEAR), dict(y=FAKE, y_stride_t=128), dict(y=FAKE, quantize=1, scales=FAR),
+               dict(residual=FAKE, residual_stride_t=64, residual_out=FAR, residual_out_stride_t=64),  # y
+               dict(residual=FAKE, residual_stride_t=64, residual_out=NEAR, residual_out_stride_t=64),
+               dict(residual=FAKE, residual_stride_t=64, residual_out=FAKE, residual_out_stride_t=128),
+               dict(residual=FAR + 128, residual_stride_t=64, residual_out=FAR + (1 << 20), residual_out_stride_t=64),  # y
+               dict(residual=FAR + (1 << 20), residual_dtype=1, residual_stride_t=64, residual_out=FAKE, residual_out_stride_t=64)],
+    "rn_bwd": [dict(dx=NEAR), dict(dx=FAKE, dx_stride_t=128), dict(dx=FAKE, s_dtype=1), dict(ds=FAR, ds_stride_t=64),
+               dict(ds=FAR + 64, ds_stride_t=64), dict(ds=NEAR, ds_stride_t=64), dict(d_residual=FAR + 128, d_residual_stride_t=64)],
+}
+
+
+@pytest.mark.parametrize("fn,over", [(f, o) for f, cases in SHARED.items() for o in cases],
+                         ids=lambda v: "-".join(f"{k}_{x}" for k, x in v.items()) if isinstance(v, dict) else None)
+def test_results_over_other_operands_are_refused(fn, over):
+    """Results that lie over an input other than element by element, or over each other."""
+    cls, fields = VALID[fn]
+    p = cls()
+    for k, v in {**fields, **over}.items():
+        setattr(p, k, v)
+    assert getattr(B.load(), fn)(ctypes.byref(p), None) == INV
+
+
 def test_sizes():
     lib = B.load()
     assert la.ssm_checkpoint_rows(0, 3) == 3 and la.ssm_checkpoint_rows(1000, 3) == 65

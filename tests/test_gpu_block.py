@@ -151,6 +151,34 @@ def test_autograd_forms():
     assert torch.equal(rv.grad, torch.ones_like(r)) and torch.equal(xv.grad, torch.ones_like(x))
 
 
+def test_results_over_operands():
+    """Single tokens over x, dt or z (both kernels: the second takes large batches), norms over x or the residual."""
+    for N, D, states in ((9, 70, 16), (70, 8192, 16), (4100, 64, 64)):
+        t = S.draw([1] * N, D, states, seed=N, xt=BF)
+        vec = [t[k] for k in "abc"]
+        opts = dict(skip=t["skip"], dt_bias=t["bias"], dt_softplus=True)
+        want = la.ssm_decode(t["x"], t["dt"], *vec, t["s0"].clone(), z=t["z"], **opts)
+        for name in ("x", "dt", "z"):
+            v = {k: t[k].clone() for k in ("x", "dt", "z")}
+            la.ssm_decode(v["x"], v["dt"], *vec, t["s0"].clone(), z=v["z"], y=v[name], **opts)
+            assert torch.equal(v[name], want), (N, name)
+    for T, V in ((1300, 4096), (700, 37), (300, 12288)):
+        x, r = (torch.randn(T, V, device=dev()).to(BF) for _ in range(2))
+        w = torch.randn(V, device=dev())
+        y, s, _ = la.rn_fwd(x, w, r)
+        xv, rv = x.clone(), r.clone()
+        la.rn_fwd(xv, w, rv, y=xv, residual_out=rv)
+        assert torch.equal(xv, y) and torch.equal(rv, s)
+        rv = r.clone()
+        s2 = la.rn_fwd(x, w, rv, y=rv)[1]
+        assert torch.equal(rv, y) and torch.equal(s2, s)
+        xv = s.clone()
+        la.rn_fwd(xv, w, y=xv)
+        assert torch.equal(xv, y)
+        with pytest.raises(la.binding.LinAttnError):
+            la.rn_fwd(x, w, r, y=rv, residual_out=rv)
+
+
 def test_steps_of_zero_keep_the_state():
     """Bit by bit, whatever the number of tokens and of states."""
     for lens, states in (([1, 2, 3, 17, 33], 16), ([5, 64], 40), ([130], 3)):
