@@ -257,7 +257,10 @@ la_status by_scan(Args& a, cudaStream_t s) {
 
 }  // namespace
 
-// Tokens of a time block: a warp takes a block of scan_width channels, and kFill of them fill an SM.
+// Tokens of a time block: a warp takes a block of scan_width channels, and kFill of them fill an SM.  Few tokens take blocks of
+// 32 where that leaves SMs less than half filled: a warp's time is then the latency of its tokens (up to two blocks of them),
+// but the blocks' states cost more, and the join walks them one by one (one sequence of 200 x 1024 x 16: 15.7 us, 22.0 with 64;
+// 600 tokens of three, 600 x 23: 25.2, 42.6; but 1024 x 512 x 64: 38.9, 34.1; 4096 x 256 x 8: 27.4, 24.8).
 int fwd_shift(int64_t T, int D, int S, int G, int time_block) {
     int shift = 6;
     if (time_block > 0) {
@@ -266,6 +269,7 @@ int fwd_shift(int64_t T, int D, int S, int G, int time_block) {
     }
     constexpr int kFill = 24;  // 49344 x 1024 in fp32, skewed: 470 us with 24, 641 with 16, 807 with 8
     const int64_t width = scan_width(S), tiles = (D / G + width - 1) / width * G;
+    if (T <= 2048 && (T * tiles >> 5) <= kSms * 10) return 5;
     while (shift < 30 && (T * tiles >> shift) > kSms * kFill) ++shift;
     return shift;
 }

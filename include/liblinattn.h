@@ -867,7 +867,7 @@ typedef struct la_ssm_fwd_params {
  * Sequences longer than two blocks of time_block tokens are split along time, blocks
  * starting at each sequence's first token; a split costs up to 3/4 of the arithmetic
  * again, so with time_block 0 blocks are as long as T and D allow while the GPU is
- * filled (powers of two from 64 on).  Results are the same bits for the same T, N, D, S, G and
+ * filled (powers of two from 32 on).  Results are the same bits for the same T, N, D, S, G and
  * time_block; with a given time_block they are batch invariant too.
  */
 la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream);
