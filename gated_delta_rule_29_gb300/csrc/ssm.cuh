@@ -232,6 +232,11 @@ __device__ __forceinline__ float4 load_states(const void* base, int64_t row, con
     if (!live || s >= a.S) return make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t at = (row * a.D + d) * a.S + s;
     if (a.svec && !is_bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    if (a.svec) {
+        Packed<bf16, 4> w;
+        w.load(static_cast<const bf16*>(base) + at);
+        return make_float4(w.get(0), w.get(1), w.get(2), w.get(3));
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (s + i < a.S) v[i] = load_any(base, at + i, is_bf16);
@@ -245,6 +250,10 @@ __device__ __forceinline__ void store_states(void* base, int64_t row, const Args
         return;
     }
     const float v[4] = {f.x, f.y, f.z, f.w};
+    if (a.svec) {
+        store_packed<bf16, 4>(static_cast<bf16*>(base) + at, v);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (s + i < a.S) store_any(base, at + i, is_bf16, v[i]);
@@ -282,6 +291,17 @@ __device__ __forceinline__ void zero(float2 (&v)[kPairs][4]) {
 // kS consecutive states of a lane's channel, as pairs.
 template <int kS>
 __device__ __forceinline__ void load_lane_states(float2 (&v)[kS / 2], const void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
+    if (is_bf16 && a.svec && a.S % 8 == 0) {  // eight at a time
+#pragma unroll
+        for (int k = 0; k < kS; k += 8) {
+            Packed<bf16, 8> w;
+            if (live && s + k < a.S) w.load(static_cast<const bf16*>(base) + (row * a.D + d) * a.S + s + k);
+            else w.zero();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k / 2 + i] = make_float2(w.get(2 * i), w.get(2 * i + 1));
+        }
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < kS; k += 4) {
         const float4 f = load_states(base, row, a, d, s + k, live, is_bf16);
@@ -291,6 +311,14 @@ __device__ __forceinline__ void load_lane_states(float2 (&v)[kS / 2], const void
 }
 template <int kS>
 __device__ __forceinline__ void store_lane_states(const float2 (&v)[kS / 2], void* base, int64_t row, const Args& a, int d, int s, bool live, int is_bf16) {
+    if (is_bf16 && a.svec && a.S % 8 == 0) {
+#pragma unroll
+        for (int k = 0; k < kS; k += 8) {
+            const float f[8] = {v[k / 2].x, v[k / 2].y, v[k / 2 + 1].x, v[k / 2 + 1].y, v[k / 2 + 2].x, v[k / 2 + 2].y, v[k / 2 + 3].x, v[k / 2 + 3].y};
+            if (live && s + k < a.S) store_packed<bf16, 8>(static_cast<bf16*>(base) + (row * a.D + d) * a.S + s + k, f);
+        }
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < kS; k += 4)
         store_states(base, row, a, d, s + k, live, is_bf16, make_float4(v[k / 2].x, v[k / 2].y, v[k / 2 + 1].x, v[k / 2 + 1].y));

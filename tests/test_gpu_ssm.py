@@ -228,6 +228,21 @@ def test_decode(xt, pool_dtype, D, S, G):
     R.within("state", before[:5], ref[1], pool_dtype, UNITS, scale[1])
 
 
+@pytest.mark.parametrize("softplus", [False, True])
+def test_a_bf16_pool_rounds_what_the_formula_gives(softplus):
+    """The states that a token leaves in a bf16 pool are the formula's in 32 bits, operation by operation, rounded once: all
+    of them, where the exponential and logarithm are the ones of elementary operations."""
+    N, D, S = 37, 520, 16
+    t = draw([1] * N, D, S, seed=11, xt=F32)
+    pool = t["s0"].to(BF)
+    raw = t["dt"] + t["bias"]
+    step = raw if not softplus else torch.clamp(raw, min=0) + torch.log1p(torch.exp(-raw.abs()))
+    b = t["b"].reshape(N, 1, S)
+    want = (torch.exp(step[:, :, None] * t["a"]) * pool.float() + (step * t["x"])[:, :, None] * b).to(BF)
+    la.ssm_decode(t["x"], t["dt"], t["a"], t["b"], t["c"], pool, dt_bias=t["bias"], dt_softplus=softplus)
+    assert torch.equal(pool, want)
+
+
 def test_prefill_then_tokens_give_the_whole():
     lens = [50, 7, 90]
     t = draw(lens, 64, 16, xt=F32, seed=8)
