@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>()))
         }
         float sum = sq.x + sq.y;
         row_reduce<true>(sum, most, a.warps, red, static_cast<int>(n));
-        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps));
+        float rs = inv_sqrt(fmaf(sum, inv_v, a.eps));
         if (!live) continue;  // a warp has one row
         if (a.quant == LA_QUANT_NONE) {
 #pragma unroll
@@ -117,7 +117,14 @@ __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>()))
             store_row<X, kVec, NV>(a.y, t * a.y_st, x, pl, a.V);
             continue;
         }
-        // y / scale as s w times (r / scale): a block's largest |y| is its largest |s w| times r
+        // y / scale as s w times (r / scale): a block's largest |y| is its largest |s w| times r.  The factor is 448 r / 2^-100 at
+        // most, within the range up to r = 2^19; beyond (rows of 2e-6 and less, padding, under a small eps) s w takes r first.
+        if (rs > 0x1p19f) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) s[j] = mul2(s[j], both(rs));
+            most *= rs;
+            rs = 1.f;
+        }
         if (a.quant == LA_QUANT_ROW) {
             const Scale sc = scale_of(most * rs, false);
 #pragma unroll
