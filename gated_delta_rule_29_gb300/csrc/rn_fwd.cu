@@ -32,6 +32,7 @@ struct Scale {
     float scale;
     uint8_t exponent;  // of the power of two, as e8m0 has it; 255 (NaN) where most is not finite
 };
+// Where most is not finite all three are NaN, and with them the block's values.
 __device__ __forceinline__ Scale scale_of(float most, bool power) {
     most = max_nan(most, 0x1p-100f);
     Scale s;
@@ -42,6 +43,7 @@ __device__ __forceinline__ Scale scale_of(float most, bool power) {
         s.inverse = __uint_as_float(b >= 0x7F800000u ? 0x7FC00000u : (254u - e) << 23);
     } else {
         s.exponent = 0;
+        most = fmaf(most, 0.f, most);  // itself, or NaN
         s.scale = __fdiv_rn(most, kTop);
         s.inverse = __fdiv_rn(kTop, most);
     }

@@ -39,3 +39,20 @@ def test_tiny_rows_are_scaled(kind):
     t["x"] *= torch.tensor([1e-37, 1e-36, 1e-33, 1e-30, 1.0], device=dev())[:, None]
     y, s, scales = la.rn_fwd(t["x"], t["w"], quantize=kind, eps=1e-30)
     expect_8bit(y, scales, s, t["w"], kind, 1e-30)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("kind,width", [("row", 512), ("block", 128), ("mx", 32)])
+def test_blocks_that_are_not_finite(kind, width, value):
+    """A weight that is not finite beside finite rows: the scales and values of its block are NaN, the others' as they are."""
+    t = draw(6, 512, F32, F32, seed=3)
+    want, _, want_scales = la.rn_fwd(t["x"], t["w"], t["r"], quantize=kind)
+    w = t["w"].clone()
+    w[200] = value
+    y, _, scales = la.rn_fwd(t["x"], w, t["r"], quantize=kind)
+    bad = torch.arange(512, device=dev()) // width == 200 // width
+    assert bool(torch.isnan(scales.float()[:, 200 // width]).all()) and bool(torch.isnan(y.float()[:, bad]).all())
+    assert torch.equal(y.float()[:, ~bad], want.float()[:, ~bad])
+    assert int(torch.isnan(scales.float()).sum()) == 6
+    other = torch.arange(want_scales.shape[1], device=dev()) != 200 // width
+    assert torch.equal(scales.float()[:, other], want_scales.float()[:, other])
