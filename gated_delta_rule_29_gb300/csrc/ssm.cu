@@ -35,13 +35,13 @@ __global__ void __launch_bounds__(kThreads) ssm_decode_kernel(const Args a) {
     float step;
     if (kBf16 && a.softplus) step = __fadd_rn(fmaxf(raw + bias, 0.f), log1pf(expf(-fabsf(raw + bias))));
     else step = steps_of(both(raw + bias), a.softplus).x;
-    const float2 u = both(__fmul_rn(step, x)), l = both(step * kLog2e);
+    const float2 u = both(__fmul_rn(step, x));
     auto next = [&](float2& h, float2 A, float2 b) {
         if (kBf16) {
             h.x = __fadd_rn(__fmul_rn(expf(__fmul_rn(step, A.x)), h.x), __fmul_rn(u.x, b.x));
             h.y = __fadd_rn(__fmul_rn(expf(__fmul_rn(step, A.y)), h.y), __fmul_rn(u.x, b.y));
         } else {
-            const float2 e = mul2(l, A);
+            const float2 e = fma2(both(step), mul2(A, both(kLog2e)), both(kEx2Low));
             h = fma2(make_float2(ex2(e.x), ex2(e.y)), h, mul2(u, b));
         }
     };
@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
     const int64_t within = static_cast<int64_t>(dl) * a.S + s, pitch = static_cast<int64_t>(a.D) * a.S;
     float* const pool = static_cast<float*>(const_cast<void*>(a.s0));
     const float bias = a.bias ? a.bias[dl] : 0.f, skip = a.skip ? a.skip[dl] : 0.f;
-    const float4 A = load_states(a.A, 0, a, d, s, live, 0);
+    float4 A = load_states(a.A, 0, a, d, s, live, 0);  // times log2(e)
+    A = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
 
     // the slots of a group's sequences as they are given; which of them are there is seen when they are used
     auto slots_of = [&](int (&slot)[kSeqs], int64_t group) {
@@ -151,12 +152,12 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
             const float t = kShare == 1 ? dt[i / kShare] : __shfl_sync(0xffffffffu, dt[i / kShare], from);
             const float v = kShare == 1 ? x[i / kShare] : __shfl_sync(0xffffffffu, x[i / kShare], from);
             const bool there = here[i] >= 0 && here[i] < a.pool;
-            const float u = t * v, l = t * kLog2e;
+            const float u = t * v;
             float4 h = ring[n % kDepth][i][threadIdx.x];
-            h.x = fmaf(ex2(l * A.x), h.x, u * now.b[i].get(0));
-            h.y = fmaf(ex2(l * A.y), h.y, u * now.b[i].get(1));
-            h.z = fmaf(ex2(l * A.z), h.z, u * now.b[i].get(2));
-            h.w = fmaf(ex2(l * A.w), h.w, u * now.b[i].get(3));
+            h.x = fmaf(ex2(fmaf(t, A.x, kEx2Low)), h.x, u * now.b[i].get(0));
+            h.y = fmaf(ex2(fmaf(t, A.y, kEx2Low)), h.y, u * now.b[i].get(1));
+            h.z = fmaf(ex2(fmaf(t, A.z, kEx2Low)), h.z, u * now.b[i].get(2));
+            h.w = fmaf(ex2(fmaf(t, A.w, kEx2Low)), h.w, u * now.b[i].get(3));
             if (live && there) *reinterpret_cast<float4*>(pool + here[i] * pitch + within) = h;
             p[i] = live ? fmaf(h.x, now.c[i].get(0), h.y * now.c[i].get(1)) + fmaf(h.z, now.c[i].get(2), h.w * now.c[i].get(3)) : 0.f;
 #pragma unroll
