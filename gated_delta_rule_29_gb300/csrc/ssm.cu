@@ -10,6 +10,9 @@ using namespace la::ssm;
 
 constexpr int kThreads = 128;
 
+// The two kernels below sum C h in one order, (h0 c0 + h2 c2) + (h1 c1 + h3 c3) of every four states and then pairs of fours, pairs
+// of those and so on, so that a sequence's bits do not depend on how many others are decoded beside it.
+
 // A lane has kS states of one channel of one sequence: as few steps are formed as there are channels, but its 16-byte
 // accesses lie kS * 4 bytes from its neighbours' (512 x 8192 x 16 in fp32: 124 us, all of it L1 wavefronts).
 // Into a bf16 pool (kBf16) the new states are formed by the formula's own operations, each rounded once, with the library's
@@ -45,17 +48,21 @@ __global__ void __launch_bounds__(kThreads) ssm_decode_kernel(const Args a) {
             h = fma2(make_float2(ex2(e.x), ex2(e.y)), h, mul2(u, b));
         }
     };
-    float2 y = both(0.f);
+    float y[kS / 4];
 #pragma unroll
     for (int k = 0; k < kPairs; k += 2) {
         const float4 b = load4<X>(a.b, b_at + 2 * k, a.S - s0 - 2 * k, a.vec), c = load4<X>(a.c, c_at + 2 * k, a.S - s0 - 2 * k, a.vec);
         next(h[k], A[k], lo(b));
         next(h[k + 1], A[k + 1], hi(b));
-        y = fma2(h[k], lo(c), y);
-        y = fma2(h[k + 1], hi(c), y);
+        const float2 t = fma2(h[k], lo(c), mul2(h[k + 1], hi(c)));
+        y[k / 2] = t.x + t.y;
     }
     store_lane_states<kS>(h, const_cast<void*>(a.s0), row, a, d, s0, live, kBf16);
-    float p = y.x + y.y;
+#pragma unroll
+    for (int n = 1; n < kS / 4; n *= 2)
+#pragma unroll
+        for (int k = 0; k < kS / 4; k += 2 * n) y[k] += y[k + n];
+    float p = y[0];
 #pragma unroll
     for (int off = kW; off < 32; off *= 2) p += __shfl_xor_sync(0xffffffffu, p, off);
     p = fmaf(skip, x, p);
@@ -159,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_decode_many_kernel(const Args
             h.z = fmaf(ex2(fmaf(t, A.z, kEx2Low)), h.z, u * now.b[i].get(2));
             h.w = fmaf(ex2(fmaf(t, A.w, kEx2Low)), h.w, u * now.b[i].get(3));
             if (live && there) *reinterpret_cast<float4*>(pool + here[i] * pitch + within) = h;
-            p[i] = live ? fmaf(h.x, now.c[i].get(0), h.y * now.c[i].get(1)) + fmaf(h.z, now.c[i].get(2), h.w * now.c[i].get(3)) : 0.f;
+            p[i] = live ? fmaf(h.x, now.c[i].get(0), h.z * now.c[i].get(2)) + fmaf(h.y, now.c[i].get(1), h.w * now.c[i].get(3)) : 0.f;
+            if (Q == 1) p[i] += 0.f;  // the other kernel's four states beyond: -0 becomes 0
 #pragma unroll
             for (int off = 1; off < Q; off *= 2) p[i] += __shfl_xor_sync(0xffffffffu, p[i], off);
             if (!there && group * kSeqs + i < a.N) raise_status(a.status, LA_ERR_BAD_STATE_INDEX);

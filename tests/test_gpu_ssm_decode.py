@@ -1,5 +1,5 @@
-"""Single tokens of the selective scan: many of them against the scan and the 64-bit decay, and the large
-batches' kernel over what it takes, against the 64-bit form."""
+"""Single tokens of the selective scan: many of them against the scan and the 64-bit decay, small batches against large
+ones (two kernels), and the large batches' kernel over what it takes, against the 64-bit form."""
 import numpy as np
 import pytest
 import torch
@@ -95,6 +95,21 @@ def test_decays_over_many_tokens(lo, hi, steps, how):
 
 
 SHAPES = [(8192, 16, 1), (8192, 4, 1), (4096, 8, 1), (2048, 32, 2), (1024, 64, 1), (2048, 12, 2), (1512, 24, 3), (1000, 48, 1), (1064, 64, 1)]
+
+
+@pytest.mark.parametrize("opts", [{}, dict(z=False, softplus=False), dict(skip=False)], ids=["all", "plain_steps", "no_skip"])
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("D,states,G", SHAPES)
+def test_a_sequence_does_not_depend_on_the_batch(D, states, G, xt, opts):
+    """The same bits in y and in an fp32 pool, alone, among a few and in a batch of the other kernel."""
+    N = LARGE // (D * states) + 5
+    t = batch(N, D, states, G, xt, seed=states, **opts)
+    pool = t["s0"].clone()
+    y = la.ssm_decode(*operands(t), pool, **options(t))
+    for at in ([0], [N - 1], [0, 1, 2, 5, N // 2, N - 3, N - 2]):
+        few = rows_of(t, at)
+        y1 = la.ssm_decode(*operands(few), few["s0"], **options(few))
+        assert torch.equal(y1, y[at]) and torch.equal(few["s0"], pool[at])
 
 
 @pytest.mark.parametrize("opts", [{}, dict(z=False), dict(softplus=False), dict(skip=False), dict(z=False, skip=False, softplus=False)],
