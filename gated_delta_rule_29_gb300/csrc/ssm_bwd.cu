@@ -175,7 +175,33 @@ struct Work {
     float b[kSub][kSP], c[kSub][kSP];
     float4 h[kWarps][kSub / 4][4][32];  // the states before every fourth token
     float dbc[kWarps][kSub][2 * kSP];   // dB, dC of a warp's channels
+    float4 ch[2][kThreads];             // d skip, d bias of the blocks so far, each thread's own
 };
+
+// Four consecutive floats of global memory that no other thread adds to.
+__device__ __forceinline__ void add_to(float* p, float4 f, int vec, int n) {
+    if (vec) {
+        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(f.x), "f"(f.y), "f"(f.z), "f"(f.w) : "memory");
+        return;
+    }
+    const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p + i), "f"(v[i]) : "memory");
+}
+// store_thread_states's counterpart.
+__device__ __forceinline__ void add_thread_states(const float2 (&v)[2][4], float* base, int64_t row, const Args& a, int d, int end, int s) {
+    if (s >= a.S) return;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        float* const at = base + (row * a.D + d + 2 * p) * a.S + s;
+        if (d + 2 * p < end) add_to(at, make_float4(v[p][0].x, v[p][1].x, v[p][2].x, v[p][3].x), a.svec, a.S - s);
+        if (d + 2 * p + 1 < end) add_to(at + a.S, make_float4(v[p][0].y, v[p][1].y, v[p][2].y, v[p][3].y), a.svec, a.S - s);
+    }
+}
+__device__ __forceinline__ void add4(float4& to, const float2 (&v)[2]) {
+    to = make_float4(to.x + v[0].x, to.y + v[0].y, to.z + v[1].x, to.w + v[1].y);
+}
 
 template <typename X, int Q, bool kGate>
 __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
@@ -191,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
     // the four channels that this thread prepares and finishes, of every kRows-th row
     constexpr int kVecs = kTile / 4, kRows = kThreads / kVecs;
     const int c4 = tid % kVecs * 4, r4 = tid / kVecs, cn = tile.n - c4;
-    float2 bias[2], skip[2], d_skip[2] = {both(0.f), both(0.f)}, d_bias[2] = {both(0.f), both(0.f)};
+    float2 bias[2], skip[2], d_skip[2], d_bias[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         bias[i].x = a.bias && 2 * i < cn ? a.bias[tile.ch + c4 + 2 * i] : 0.f;
@@ -205,7 +231,10 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int s = 0; s < 4; ++s) A2[p][s] = mul2(A2[p][s], both(kLog2e));
-    zero(dA);
+    // A running sum over all of a part's tokens would lose bits: dA, d skip and d bias are summed over a block in registers, and
+    // added up over the part's blocks in global memory (each word by one thread alone, with nothing to wait for) and in sm.ch.
+    sm.ch[0][tid] = sm.ch[1][tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool kept = false;
 
     const int64_t slots = slots_for(a.T, a.N, kShift);
     for (int64_t slot = part; slot < slots; slot += a.parts) {
@@ -231,6 +260,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
         load(0, t0);
         float2 g[2][4];
         load_thread_states(g, a.table, slot, a, d0, end, s0, 0);
+        zero(dA);
+        d_skip[0] = d_skip[1] = d_bias[0] = d_bias[1] = both(0.f);
         for (; t0 >= 0; t0 -= kSub) {
             const int n = min(kSub, blk.count - t0);
             float2 h[2][4];
@@ -452,30 +483,50 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_block_kernel(const Args a) {
                 buf ^= 1;
             }
         }
+        if (kept) add_thread_states(dA, a.pA, part, a, d0, end, s0);
+        else store_thread_states(dA, a.pA, part, a, d0, end, s0, 0);
+        kept = true;
+        add4(sm.ch[0][tid], d_skip);
+        add4(sm.ch[1][tid], d_bias);
     }
-    store_thread_states(dA, a.pA, part, a, d0, end, s0, 0);
+    if (!kept) {
+        zero(dA);
+        store_thread_states(dA, a.pA, part, a, d0, end, s0, 0);
+    }
     // d skip and d bias over the threads that share their channels, in order
     cp_async_wait<0>();
-    __syncthreads();
-    float* red = &sm.dt[0][0];  // [2][kRows][kTile]
-    *reinterpret_cast<float4*>(red + r4 * kTile + c4) = make_float4(d_skip[0].x, d_skip[0].y, d_skip[1].x, d_skip[1].y);
-    *reinterpret_cast<float4*>(red + (kRows + r4) * kTile + c4) = make_float4(d_bias[0].x, d_bias[0].y, d_bias[1].x, d_bias[1].y);
     __syncthreads();
     for (int i = tid; i < 2 * kTile; i += kThreads) {
         const int which = i / kTile, c = i % kTile;
         if (c >= tile.n) continue;
+        const float* from = reinterpret_cast<const float*>(&sm.ch[which][0]) + c;  // [kRows][kTile]
         float t = 0.f;
-        for (int r = 0; r < kRows; ++r) t += red[(which * kRows + r) * kTile + c];
+        for (int r = 0; r < kRows; ++r) t += from[r * kTile];
         a.pch[(static_cast<int64_t>(part) * 2 + which) * a.D + tile.ch + c] = t;
     }
 }
 
 // ---------------------------------------------------------------- sums over tiles and parts
+// p[0] + p[pitch] + ... over `rows` rows as eight sums, of every eighth row, and pairs of those: up to 304 parts would cost a
+// single running sum its last bits.
+__device__ __forceinline__ float sum_in_eight(const float* p, int64_t pitch, int rows) {
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = i < rows ? p[i * pitch] : 0.f;
+    for (int r = 8; r < rows; r += 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += r + i < rows ? p[(r + i) * pitch] : 0.f;
+#pragma unroll
+    for (int n = 1; n < 8; n *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2 * n) s[i] += s[i + n];
+    return s[0];
+}
 template <typename X>
 __global__ void __launch_bounds__(256) ssm_sum_bc_kernel(const Args a) {
     const int64_t e = blockIdx.x * 256ll + threadIdx.x, n = a.T * a.G * 2 * a.S;
     if (e >= n) return;
-    const float t = strided_sum<8>(a.dbc + e, n, 0, a.tiles_pg, 1);
+    const float t = sum_in_eight(a.dbc + e, n, a.tiles_pg);
     const int64_t row = e / (2 * a.S), j = e - row * 2 * a.S;
     X* to = static_cast<X*>(j < a.S ? a.db : a.dc);
     to[row * a.S + (j < a.S ? j : j - a.S)] = from_f<X>(t);
@@ -483,11 +534,11 @@ __global__ void __launch_bounds__(256) ssm_sum_bc_kernel(const Args a) {
 __global__ void __launch_bounds__(256) ssm_sum_parts_kernel(const Args a) {
     const int64_t e = blockIdx.x * 256ll + threadIdx.x, DS = static_cast<int64_t>(a.D) * a.S;
     if (e < DS) {
-        a.dA[e] = strided_sum<8>(a.pA + e, DS, 0, a.parts, 1);
+        a.dA[e] = sum_in_eight(a.pA + e, DS, a.parts);
     } else if (e < DS + 2 * a.D) {
         const int64_t c = e - DS;
         float* to = c < a.D ? a.dskip : a.dbias;
-        if (to) to[c < a.D ? c : c - a.D] = strided_sum<8>(a.pch + c, 2 * a.D, 0, a.parts, 1);
+        if (to) to[c < a.D ? c : c - a.D] = sum_in_eight(a.pch + c, 2 * a.D, a.parts);
     }
 }
 
