@@ -129,6 +129,29 @@ __device__ __forceinline__ int64_t state_row(const Args& a, int32_t seq) {
     return k;
 }
 
+// Walks kAhead blocks: each takes the state (or gradient) v that enters it by take(k, v) and leaves e^(its steps' sum a) v + left.
+// Rates above 0 may lift the factor beyond the 32-bit range: it then comes in two halves, and a state of 0 stays 0 beside it
+// (asked once for all blocks: a branch at each would hold back the next loads, 150 instead of 85 us for 65536 x 2048 x 16 back).
+template <int kAhead, typename Take>
+__device__ __forceinline__ float walk_blocks(float v, float A2, const float (&sum)[kAhead], const float (&left)[kAhead], Take take) {
+    bool grows = false;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) grows |= A2 * sum[k] > 127.f;
+    if (grows) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (take(k, v)) {
+                const float half = ex2(0.5f * (A2 * sum[k]));
+                v = v == 0.f ? left[k] : fmaf(half, half * v, left[k]);
+            }
+        return v;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (take(k, v)) v = fmaf(ex2(A2 * sum[k]), v, left[k]);
+    return v;
+}
+
 // ---------------------------------------------------------------- steps
 // softplus(v) = max(v, 0) + log1p(t), t = e^-|v| in (0, 1]; log1p(t) = 2 atanh(s), s = t / (2 + t) up to 1/3, where a
 // polynomial of degree 4 in s^2 (fitted at Chebyshev nodes) is off by 4e-9: no difference of near values anywhere, and two

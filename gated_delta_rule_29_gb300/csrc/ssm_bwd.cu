@@ -149,12 +149,10 @@ __global__ void __launch_bounds__(128) ssm_join_back_kernel(const Args a) {
             loc[k] = c >= k ? a.table[(slot + c - k) * DS + e] : 0.f;
             sum[k] = c >= k ? a.sums[(slot + c - k) * a.D + d] : 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (c >= k) {
-                a.table[(slot + c - k) * DS + e] = g;
-                g = fmaf(ex2(A2 * sum[k]), g, loc[k]);
-            }
+        g = walk_blocks(g, A2, sum, loc, [&](int k, float entering) {
+            if (c >= k) a.table[(slot + c - k) * DS + e] = entering;
+            return c >= k;
+        });
     }
     if (a.ds0) a.ds0[i * DS + e] = g;
 }

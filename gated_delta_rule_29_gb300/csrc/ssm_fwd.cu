@@ -222,12 +222,10 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(const Args a) {
             loc[k] = live ? a.table[row * DS + e] : 0.f;
             sum[k] = live ? a.sums[row * a.D + d] : 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (c + k < blocks) {
-                a.table[launched_row(a, a.shift, i, t0, c + k) * DS + e] = st;
-                st = fmaf(ex2(A2 * sum[k]), st, loc[k]);
-            }
+        st = walk_blocks(st, A2, sum, loc, [&](int k, float entering) {
+            if (c + k < blocks) a.table[launched_row(a, a.shift, i, t0, c + k) * DS + e] = entering;
+            return c + k < blocks;
+        });
     }
 }
 

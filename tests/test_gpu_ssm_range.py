@@ -1,10 +1,12 @@
-"""The selective scan at the ends of its range: sums over many tokens."""
+"""The selective scan at the ends of its range: sums over many tokens, states that grow."""
 import numpy as np
 import pytest
 import torch
 
+import block_reference as R
 import gated_delta_rule_29_gb300 as la
-from test_gpu_ssm import cu_of, dev
+from test_gpu_ssm import F32, UNITS, compare, cu_of, dev, draw
+import test_gpu_ssm as S
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +40,36 @@ def test_sums_over_many_tokens():
                                  ("d_dt_bias", d_bias, e * x.double() + w * A, 2 * 64 * (w * A).abs() / (e * x.double() + w * A).abs() + 64)):
         off = (got.double() / (T * term) - 1).abs() * 2.0 ** 24
         assert bool((off <= 128 + own).all()), (name, float(off.max()))
+
+
+@pytest.mark.parametrize("time_block", [64, 256])
+def test_growing_states(time_block):
+    """Rates above 0: a block's factor leaves the range, but the states it stands beside are 0 until the last tokens."""
+    T, D, N = 600, 5, 4
+    t = draw([T], D, N, xt=F32, seed=1, softplus=False, z=False)
+    del t["s0"], t["dfin"]
+    t["a"] = torch.full((D, N), 0.5, device=dev())
+    t["a"][:, 1] = 2.0
+    t["a"][:, 2] = -1.0
+    t["dt"] = torch.ones_like(t["dt"])
+    t["x"][:-10] = 0  # states are 0 up to here
+    t["dy"][10:] = 0  # gradients are 0 from here on
+    compare(S.call(t, cu_of([T]), time_block=time_block), t, [T])
+
+
+def test_tiny_states_that_grow():
+    """States of 1e-30 that grow by e^73 and e^90 in one block, the second being beyond the 32-bit range as a factor."""
+    T, D, N = 3 * 256, 3, 2
+    t = draw([T], D, N, xt=F32, seed=1, softplus=False, z=False)
+    t["a"] = torch.full((D, N), 0.30, device=dev())
+    t["a"][:, 1] = 0.37
+    t["dt"] = torch.zeros_like(t["dt"])
+    t["dt"][100:500] = 1.0
+    t["x"].zero_()
+    t["s0"] *= 1e-30
+    t["dy"].zero_()
+    t["dfin"] *= 1e-30
+    got = S.call(t, cu_of([T]), backward=False, time_block=256)
+    ref, scale = S.reference(t, [T], False), S.reference(t, [T], False, scales=True)
+    assert np.isfinite(ref[1]).all()
+    R.within("final_state", got[1], ref[1], F32, UNITS, scale[1])
