@@ -316,8 +316,10 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.
                    initial_state: Optional[torch.Tensor] = None, save_checkpoints: bool = True, time_block: int = 0
                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable ssm_fwd: returns (y, final_state); gradients flow to x, dt, a, b, c, skip, z, dt_bias and
-    initial_state.  save_checkpoints keeps the state entering every 16 tokens (D * S * 4 bytes each) for the backward;
-    without them it recomputes them (in the blocks of time_block 0)."""
+    initial_state.  save_checkpoints keeps the state entering every 16 tokens (D * S * 4 bytes each) for the backward, where
+    there will be one; without them it recomputes them (in the blocks of time_block 0)."""
+    save_checkpoints = save_checkpoints and torch.is_grad_enabled() and any(
+        getattr(v, "requires_grad", False) for v in (x, dt, a, b, c, skip, z, dt_bias, initial_state))
     return _SelectiveScan.apply(x, dt, a, b, c, cu_seqlens, skip, z, dt_bias, initial_state, dt_softplus, save_checkpoints,
                                 time_block)
 
