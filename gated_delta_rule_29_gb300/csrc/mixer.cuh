@@ -5,8 +5,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "../../include/liblinattn.h"
 #include "ptx.cuh"
@@ -263,18 +265,34 @@ inline bool good_rows(const void* p, int64_t stride, int64_t rows, int64_t D, in
     if (stride < 0) return false;
     return !out || rows == 1 || stride >= D;
 }
-// Whether `rows` rows of a_row bytes, a_st bytes apart, share memory with rows of b_row bytes: for sure where the strides are
-// the same, and where they differ as far as the first rows tell.
+// Whether `rows` rows of a_row bytes, a_st bytes apart, share memory with rows of b_row bytes.  Operands that lie apart take a
+// few comparisons, the same stride two divisions; only rows of one buffer with two strides are gone through.
 inline bool bytes_meet(const void* a, int64_t a_st, int64_t a_row, const void* b, int64_t b_st, int64_t b_row, int64_t rows) {
     if (rows == 0) return false;
-    const int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
-    if (rows == 1 || a_st != b_st || a_st == 0) return off > -b_row && off < a_row;
-    int64_t q = off / a_st, r = off % a_st;  // b's first row is r bytes after a's row q
-    if (r < 0) {
-        r += a_st;
-        --q;
+    int64_t off = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+    const int64_t last = rows - 1;
+    if (off >= last * a_st + a_row || off + last * b_st + b_row <= 0) return false;
+    if (rows == 1) return true;
+    // whether some i from lo to hi has -b_row < x - i st < a_row
+    auto one = [](int64_t x, int64_t st, int64_t a_row, int64_t b_row, int64_t lo, int64_t hi) {
+        auto floor_div = [](int64_t n, int64_t d) { return n / d - (n % d < 0); };
+        if (st == 0) return -b_row < x && x < a_row;
+        return std::max(lo, floor_div(x - a_row, st) + 1) <= std::min(hi, -floor_div(-(x + b_row), st) - 1);
+    };
+    if (a_st == b_st) return one(off, a_st, a_row, b_row, -last, last);
+    if (a_st > b_st) {  // the rows further apart are fewer beside the others
+        std::swap(a_st, b_st);
+        std::swap(a_row, b_row);
+        off = -off;
     }
-    return (r < a_row && q < rows && q > -rows) || (a_st - r < b_row && q + 1 < rows && q + 1 > -rows);
+    // rows of b that lie within a's
+    const int64_t first = off < -b_row ? (-b_row - off) / b_st : 0;
+    for (int64_t j = first; j <= last; ++j) {
+        const int64_t x = off + j * b_st;
+        if (x >= last * a_st + a_row) break;
+        if (one(x, a_st, a_row, b_row, 0, last)) return true;
+    }
+    return false;
 }
 // The same of two operands of D channels.
 inline bool rows_meet(const void* a, int64_t a_st, const void* b, int64_t b_st, int64_t rows, int64_t D, int32_t dtype) {

@@ -765,7 +765,7 @@ typedef struct la_sconv_fwd_params {
  * tokens before the start being the initial state's rows (zeros without one).  final_state
  * is the last W - 1 inputs (the initial state's rows shifted along for shorter sequences),
  * which with state_indices goes back into the sequence's slot.  y must not share memory with x, nor sconv_bwd's dx with
- * x or dy (LA_ERR_INVALID_ARG where their strides are the same or their first rows meet): a token's neighbours read them.
+ * x or dy (LA_ERR_INVALID_ARG): a token's neighbours read them.
  */
 la_status sconv_fwd(const la_sconv_fwd_params* p, void* stream);
 
@@ -862,7 +862,7 @@ typedef struct la_ssm_fwd_params {
  * receives the fp32 state entering every 16 tokens of every sequence, for ssm_bwd:
  * part c of sequence i is row cu_seqlens[i] / 16 + i + c (rows in between are left
  * alone).  y may be x, dt or z itself (same address and stride), and must share no
- * memory with them otherwise (LA_ERR_INVALID_ARG as for sconv_fwd), nor with b or c.
+ * memory with them otherwise (LA_ERR_INVALID_ARG), nor with b or c.
  *
  * Sequences longer than two blocks of time_block tokens are split along time, blocks
  * starting at each sequence's first token; a split costs up to 3/4 of the arithmetic
@@ -977,7 +977,7 @@ typedef struct la_rn_fwd_params {
  * 2^-100, scale = m / 448, or for LA_QUANT_MX the least power of two with m <= 448
  * scale.  A block whose largest value is not finite has a scale of NaN.
  * residual_out may be residual or x itself, and y may be x, or residual where that is not residual_out (same address,
- * stride and type).  Results share no memory with an input or each other otherwise (LA_ERR_INVALID_ARG as for sconv_fwd).
+ * stride and type).  Results share no memory with an input or each other otherwise (LA_ERR_INVALID_ARG).
  */
 la_status rn_fwd(const la_rn_fwd_params* p, void* stream);
 
