@@ -232,12 +232,25 @@ bool good_states(const void* p, int64_t st, int64_t sg, int64_t rows, int32_t dt
     return rows == 0 || (p && aligned_to(p, dtype_size(dtype)) && st >= 0 && sg >= 0);
 }
 
-// Whether y shares memory with x, dt or z other than by lying exactly over one of them.
+// Whether rows of D elements share memory with b's or c's vectors, which every channel of a group reads.
 template <typename P>
-bool result_clashes(const P* p, int64_t rows, int64_t y_st, int64_t x_st, int64_t dt_st, int64_t z_st) {
+bool over_vectors(const P* p, const void* rows_at, int64_t st, int64_t rows, int64_t b_st, int64_t c_st) {
+    const int64_t es = dtype_size(p->x_dtype);
+    auto over = [&](const void* v, int64_t v_st, int64_t v_sg) {
+        if (!bytes_meet(rows_at, st * es, p->D * es, v, v_st * es, ((p->G - 1) * v_sg + p->S) * es, rows)) return false;
+        for (int64_t j = 0; j < (v_sg ? p->G : 1); ++j)
+            if (bytes_meet(rows_at, st * es, p->D * es, static_cast<const uint8_t*>(v) + j * v_sg * es, v_st * es, p->S * es, rows)) return true;
+        return false;
+    };
+    return rows_at && (over(p->b, b_st, p->b_stride_g) || over(p->c, c_st, p->c_stride_g));
+}
+
+// Whether y shares memory with x, dt or z other than by lying exactly over one of them, or with b or c.
+template <typename P>
+bool result_clashes(const P* p, int64_t rows, int64_t y_st, int64_t x_st, int64_t dt_st, int64_t z_st, int64_t b_st, int64_t c_st) {
     const int64_t es = dtype_size(p->x_dtype);
     auto over = [&](const void* in, int64_t st) { return clashes(p->y, y_st, es, in, st, es, rows, p->D); };
-    return over(p->x, x_st) || over(p->dt, dt_st) || over(p->z, z_st);
+    return over(p->x, x_st) || over(p->dt, dt_st) || over(p->z, z_st) || over_vectors(p, p->y, y_st, rows, b_st, c_st);
 }
 
 template <typename P>
@@ -324,7 +337,7 @@ la_status ssm_fwd(const la_ssm_fwd_params* p, void* stream) {
     if (!good_rows(p->y, p->y_stride_t, p->T, p->D, p->x_dtype, true) || !good_optional(p->initial_state, p->initial_state_dtype) ||
         !good_optional(p->final_state, LA_DTYPE_F32) || !good_optional(p->checkpoints, LA_DTYPE_F32) || !good_time_block(p->time_block))
         return LA_ERR_INVALID_ARG;
-    if (result_clashes(p, p->T, p->y_stride_t, p->x_stride_t, p->dt_stride_t, p->z_stride_t)) return LA_ERR_INVALID_ARG;
+    if (result_clashes(p, p->T, p->y_stride_t, p->x_stride_t, p->dt_stride_t, p->z_stride_t, p->b_stride_t, p->c_stride_t)) return LA_ERR_INVALID_ARG;
     if (p->state_indices && (!aligned_to(p->state_indices, 4) || !p->initial_state || p->final_state || p->state_pool_size <= 0))
         return LA_ERR_INVALID_ARG;
     Args a = {};
@@ -362,10 +375,12 @@ la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream) {
         int64_t st;
     } rows_of[] = {{p->dx, p->dx_stride_t}, {p->ddt, p->ddt_stride_t}, {p->z ? p->dz : nullptr, p->dz_stride_t}, {p->x, p->x_stride_t},
                    {p->dt, p->dt_stride_t}, {p->dy, p->dy_stride_t}, {p->z, p->z_stride_t}};
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 3; ++i) {
+        if (over_vectors(p, rows_of[i].p, rows_of[i].st, p->T, p->b_stride_t, p->c_stride_t)) return LA_ERR_INVALID_ARG;
         for (int j = i + 1; j < 7; ++j)
             if (rows_of[i].p && rows_of[j].p && rows_meet(rows_of[i].p, rows_of[i].st, rows_of[j].p, rows_of[j].st, p->T, p->D, xd))
                 return LA_ERR_INVALID_ARG;
+    }
     const size_t need = la_ssm_bwd_workspace_bytes(p->T, p->N, p->D, p->S, p->G, p->checkpoints != nullptr);
     if ((st = check_workspace(p->workspace, p->workspace_bytes, need)) != LA_OK) return st;
     Args a = {};
@@ -416,7 +431,7 @@ la_status ssm_decode(const la_ssm_decode_params* p, void* stream) {
     if (!p->state_pool || !good_optional(p->state_pool, p->state_dtype) || p->state_pool_size <= 0) return LA_ERR_INVALID_ARG;
     if (p->state_indices ? !aligned_to(p->state_indices, 4) : p->state_pool_size < p->N) return LA_ERR_INVALID_ARG;
     if (!good_rows(p->y, p->y_stride_n, p->N, p->D, p->x_dtype, true) ||
-        result_clashes(p, p->N, p->y_stride_n, p->x_stride_n, p->dt_stride_n, p->z_stride_n))
+        result_clashes(p, p->N, p->y_stride_n, p->x_stride_n, p->dt_stride_n, p->z_stride_n, p->b_stride_n, p->c_stride_n))
         return LA_ERR_INVALID_ARG;
     Args a = {};
     fill(a, p, p->N, p->x_stride_n, p->dt_stride_n, p->z_stride_n, p->b_stride_n, p->c_stride_n);

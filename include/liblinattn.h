@@ -862,7 +862,7 @@ typedef struct la_ssm_fwd_params {
  * receives the fp32 state entering every 16 tokens of every sequence, for ssm_bwd:
  * part c of sequence i is row cu_seqlens[i] / 16 + i + c (rows in between are left
  * alone).  y may be x, dt or z itself (same address and stride), and must share no
- * memory with them otherwise (LA_ERR_INVALID_ARG), nor with b or c.
+ * memory with them otherwise, nor with b or c (LA_ERR_INVALID_ARG).
  *
  * Sequences longer than two blocks of time_block tokens are split along time, blocks
  * starting at each sequence's first token; a split costs up to 3/4 of the arithmetic
@@ -910,8 +910,8 @@ typedef struct la_ssm_bwd_params {
  * ssm_bwd -- gradients of L = sum(dy * y) + sum(d_final_state * final_state).  The gradients
  * of a sequence's own inputs do not depend on the batch around it where its checkpoints do
  * not (recomputed ones are those of time_block 0); sums over channels and over the batch run
- * in an order fixed by the shape.  dx, ddt and dz must share no memory with each other, x, dt, z or dy
- * (LA_ERR_INVALID_ARG), nor with b or c.
+ * in an order fixed by the shape.  dx, ddt and dz must share no memory with each other, x, dt, z, dy, b
+ * or c (LA_ERR_INVALID_ARG).
  */
 la_status ssm_bwd(const la_ssm_bwd_params* p, void* stream);
 

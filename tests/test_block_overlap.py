@@ -1,5 +1,5 @@
-"""Results of the scan and the norm that share memory with an operand of another row stride, anywhere,
-on the host with fake pointers (the library returns before any CUDA call), and on a GPU that what only looks like it is
+"""Results of the scan and the norm that share memory with an operand of another row stride, anywhere, or with the scan's
+vectors, on the host with fake pointers (the library returns before any CUDA call), and on a GPU that what only looks like it is
 taken."""
 import ctypes
 
@@ -28,6 +28,12 @@ OVER = [("ssm_fwd", dict(x=FAR + 128 * 5, x_stride_t=0)),                       
         ("rn_fwd", dict(quantize=1, scales=FAKE, x=FAR + 64 * 5, x_stride_t=100)),
         ("rn_bwd", dict(s=FAR + 128 * 7, s_stride_t=0)), ("rn_bwd", dict(dy=FAR + 128 * 7 + 126, dy_stride_t=900)),
         ("rn_bwd", dict(ds=FAR + 128 * 7, ds_stride_t=65))]
+# two vectors of 32 bytes a row
+OVER_VECTORS = [("ssm_fwd", dict(b=FAR)), ("ssm_fwd", dict(c=FAR + 128 * 255)), ("ssm_fwd", dict(b=FAR + 128 * 5, b_stride_t=0)),
+                ("ssm_fwd", dict(y_stride_t=128, c=FAR + 96, b_stride_t=128, c_stride_t=128)),
+                ("ssm_fwd", dict(b=FAR - (1 << 20) + 64, b_stride_t=128, b_stride_g=1 << 19)), ("ssm_decode", dict(c=FAR + 128)),
+                ("ssm_bwd", dict(b=FAR)), ("ssm_bwd", dict(c=FAR + (1 << 20))), ("ssm_bwd", dict(z=FAKE, z_stride_t=64, dz=FAKE + (1 << 21),
+                 dz_stride_t=64, b=FAKE + (1 << 21) + 128 * 30))]
 
 
 def code(fn, over):
@@ -38,7 +44,7 @@ def code(fn, over):
     return getattr(B.load(), fn)(ctypes.byref(p), None)
 
 
-@pytest.mark.parametrize("fn,over", OVER, ids=lambda v: "-".join(f"{k}_{x:x}" for k, x in v.items()) if isinstance(v, dict) else v)
+@pytest.mark.parametrize("fn,over", OVER + OVER_VECTORS, ids=lambda v: "-".join(f"{k}_{x:x}" for k, x in v.items()) if isinstance(v, dict) else v)
 def test_rows_of_another_stride(fn, over):
     assert code(fn, over) == INV
 
@@ -75,6 +81,7 @@ def test_rows_beside_each_other():
     assert torch.equal(la.rn_fwd(x, w, dt, y=y)[0], want)
     assert torch.equal(la.rn_bwd(x, w, z, dx=y)[0], la.rn_bwd(x, w, z)[0])
     for call in (lambda: la.ssm_fwd(*ops, cu, y=buf[::2, :D], **opts), lambda: la.ssm_decode(*ops, pool, y=buf[::2, 2 * D:3 * D], **opts),
+                 lambda: la.ssm_decode(*ops, pool, y=buf[::2, 3 * D:4 * D], **opts), lambda: la.ssm_bwd(*ops, cu, x, ddt=buf[::2, 3 * D:4 * D], **opts),
                  lambda: la.rn_fwd(x, w, dt, y=buf[::2, D:2 * D])):
         with pytest.raises(B.LinAttnError):
             call()
