@@ -168,6 +168,12 @@ la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
         (p->dx && p->ds && bytes_meet(p->dx, p->dx_stride_t * xs, int64_t(p->V) * xs, p->ds, p->ds_stride_t * rs, int64_t(p->V) * rs, p->T)))
         return LA_ERR_INVALID_ARG;
     if ((st = check_workspace(p->workspace, p->workspace_bytes, la_rn_bwd_workspace_bytes(p->T, p->V))) != LA_OK) return st;
+    // the weight, which every row reads, and its gradient, which is written last
+    const int64_t ws = dtype_size(p->weight_dtype) * int64_t(p->V);
+    for (const void* w : {p->weight, static_cast<const void*>(p->d_weight)})
+        if ((p->dx && bytes_meet(p->dx, p->dx_stride_t * xs, int64_t(p->V) * xs, w, 0, ws, p->T)) ||
+            (p->ds && bytes_meet(p->ds, p->ds_stride_t * rs, int64_t(p->V) * rs, w, 0, ws, p->T)))
+            return LA_ERR_INVALID_ARG;
     Args a = {};
     a.x = p->s; a.x_st = p->s_stride_t; a.dy = p->dy; a.dy_st = p->dy_stride_t; a.dres = p->d_residual; a.dres_st = p->d_residual_stride_t;
     a.w = p->weight; a.w_bf16 = p->weight_dtype == LA_DTYPE_BF16;

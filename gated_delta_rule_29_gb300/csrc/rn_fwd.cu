@@ -218,6 +218,17 @@ la_status rn_fwd(const la_rn_fwd_params* p, void* stream) {
                         clashes(p->residual_out, p->residual_out_stride_t, ss, p->residual, p->residual_stride_t, ss, p->T, p->V) ||
                         bytes_meet(p->y, p->y_stride_t * ys, p->V * ys, p->residual_out, p->residual_out_stride_t * ss, p->V * ss, p->T)))
         return LA_ERR_INVALID_ARG;
+    // the weight, which every row reads, and the scales: one row, and rows of their own
+    const int64_t ws = dtype_size(p->weight_dtype), cs = int64_t(la_rn_scale_blocks(p->V, p->quantize)) * (p->quantize == LA_QUANT_MX ? 1 : 4);
+    auto on = [&](const void* q, int64_t st, int64_t size, const void* r, int64_t r_st, int64_t r_row) {
+        return q && r && bytes_meet(q, st * size, p->V * size, r, r_st, r_row, p->T);
+    };
+    const void *out = p->residual ? p->residual_out : nullptr, *scales = eight ? p->scales : nullptr;
+    if (on(p->y, p->y_stride_t, ys, p->weight, 0, p->V * ws) || on(out, p->residual_out_stride_t, ss, p->weight, 0, p->V * ws) ||
+        on(p->y, p->y_stride_t, ys, scales, cs, cs) || on(out, p->residual_out_stride_t, ss, scales, cs, cs) ||
+        on(p->x, p->x_stride_t, xs, scales, cs, cs) || on(p->residual, p->residual_stride_t, ss, scales, cs, cs) ||
+        (scales && bytes_meet(p->weight, 0, p->V * ws, scales, cs, cs, p->T)))
+        return LA_ERR_INVALID_ARG;
     if (p->T == 0) return LA_OK;
     Args a = {};
     a.x = p->x; a.x_st = p->x_stride_t; a.res = p->residual; a.res_st = p->residual_stride_t;

@@ -1002,7 +1002,7 @@ typedef struct la_rn_bwd_params {
 
 /* rn_bwd -- gradients of L = sum(dy * y) + sum(d_residual * residual_out), of 8-bit results as if they were y itself.
  * At least one of dx and ds is given; each may be dy, d_residual or s itself (same address, stride and type), and they share
- * no memory with an input or each other otherwise (LA_ERR_INVALID_ARG).  The sum over tokens runs in an order fixed by the
+ * no memory with an input, d_weight or each other otherwise (LA_ERR_INVALID_ARG).  The sum over tokens runs in an order fixed by the
  * shape. */
 la_status rn_bwd(const la_rn_bwd_params* p, void* stream);
 

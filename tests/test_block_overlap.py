@@ -1,5 +1,5 @@
-"""Results of the scan and the norm that share memory with an operand of another row stride, anywhere, or with the scan's
-vectors, on the host with fake pointers (the library returns before any CUDA call), and on a GPU that what only looks like it is
+"""Results of the scan and the norm that share memory with an operand of another row stride, anywhere, with the scan's
+vectors or the norm's parameters, on the host with fake pointers (the library returns before any CUDA call), and on a GPU that what only looks like it is
 taken."""
 import ctypes
 
@@ -34,6 +34,17 @@ OVER_VECTORS = [("ssm_fwd", dict(b=FAR)), ("ssm_fwd", dict(c=FAR + 128 * 255)), 
                 ("ssm_fwd", dict(b=FAR - (1 << 20) + 64, b_stride_t=128, b_stride_g=1 << 19)), ("ssm_decode", dict(c=FAR + 128)),
                 ("ssm_bwd", dict(b=FAR)), ("ssm_bwd", dict(c=FAR + (1 << 20))), ("ssm_bwd", dict(z=FAKE, z_stride_t=64, dz=FAKE + (1 << 21),
                  dz_stride_t=64, b=FAKE + (1 << 21) + 128 * 30))]
+# the norm's weight (128 bytes), its gradient and the scales
+EIGHT = dict(quantize=2, scales=FAR + (1 << 20))
+OVER_PARAMETERS = [("rn_fwd", dict(weight=FAR + 128 * 7)), ("rn_fwd", dict(weight=FAR - 126, weight_dtype=0)),
+                   ("rn_fwd", dict(residual=FAKE + (1 << 20), residual_stride_t=64, residual_out=FAKE + (1 << 21), residual_out_stride_t=64,
+                                   weight=FAKE + (1 << 21) + 1000)),
+                   ("rn_fwd", dict(EIGHT, scales=FAR)), ("rn_fwd", dict(EIGHT, scales=FAR + 64 * 8 - 4)), ("rn_fwd", dict(EIGHT, scales=FAKE + 128 * 8 - 4)),
+                   ("rn_fwd", dict(EIGHT, weight=FAR + (1 << 20) + 28)),
+                   ("rn_fwd", dict(EIGHT, residual=FAR + (1 << 20) - 1020, residual_stride_t=64, residual_out=FAKE + (1 << 21), residual_out_stride_t=64)),
+                   ("rn_fwd", dict(EIGHT, residual=FAKE + (1 << 20), residual_stride_t=64, residual_out=FAR + (1 << 20) - 1020, residual_out_stride_t=64)),
+                   ("rn_bwd", dict(d_weight=FAR + 128 * 7)), ("rn_bwd", dict(weight=FAR + 64, d_weight=FAKE + (1 << 22))),
+                   ("rn_bwd", dict(ds=FAKE + (1 << 21), ds_stride_t=64, d_weight=FAKE + (1 << 21) + 512))]
 
 
 def code(fn, over):
@@ -44,7 +55,7 @@ def code(fn, over):
     return getattr(B.load(), fn)(ctypes.byref(p), None)
 
 
-@pytest.mark.parametrize("fn,over", OVER + OVER_VECTORS, ids=lambda v: "-".join(f"{k}_{x:x}" for k, x in v.items()) if isinstance(v, dict) else v)
+@pytest.mark.parametrize("fn,over", OVER + OVER_VECTORS + OVER_PARAMETERS, ids=lambda v: "-".join(f"{k}_{x:x}" for k, x in v.items()) if isinstance(v, dict) else v)
 def test_rows_of_another_stride(fn, over):
     assert code(fn, over) == INV
 
