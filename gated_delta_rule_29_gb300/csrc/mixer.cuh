@@ -1,5 +1,5 @@
-// mixer.cuh -- what the token-mixer operators (glr.cu, gn.cu, sconv.cu) share: element access in
-// bf16 or fp32, activations, the numbering of sequence blocks, and host-side argument checks.
+// mixer.cuh -- what the token-mixer operators (glr, gn, sconv) and those of a state-space block (ssm, rn) share: element
+// access in bf16 or fp32, activations, the numbering of sequence blocks, and host-side argument checks.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -10,9 +10,10 @@
 //   e_t = C_t dp_t + g_{t+1},  g_t = a_t e_t,  dC_t = sum_d dp h_t,  dB_t = sum_d e_t dt x,  du = sum_s e_t B_t,
 //   w_t = g_t h_{t-1},  dA += w_t dt,  dx = du dt + dp skip,  d dt = du x + sum_s w_t A.
 //
-// A thread holds four states of a few channels in registers and walks the tokens; Q = 1, 2, 4, 8 or 16 lanes share a
-// channel (up to 64 states, the ones beyond S with A = B = C = 0), so one warp has 32 / Q groups of channels beside
-// each other.  B and C are read from shared memory once for all of a thread's channels, the steps once for all its states.
+// States stay in registers while a lane walks the tokens; the ones beyond S (up to 64) have A = B = C = 0.  In the scan, the
+// gradient behind each block and the small batches' single tokens a lane has 8 or 16 states of one channel, which Q = 1, 2 or 4
+// lanes share.  In the kernel of all gradients it has four states of four channels (Q = 4, 8 or 16 lanes share them), for the large
+// batches' single tokens four states of one channel (Q = 1 to 16).
 #pragma once
 #include <algorithm>
 

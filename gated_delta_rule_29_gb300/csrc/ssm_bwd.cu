@@ -9,7 +9,9 @@
 // goes forward once, leaving the states before every fourth token in shared memory (and p, for dz), then takes four tokens
 // at a time from the end: forward again with states and decays kept in registers, then back.  dB and dC are summed over a
 // thread's channels, the warp's, the CTA's, and by a later launch over the CTAs that share a group; dA, d skip and d bias over
-// a CTA's blocks and then over the CTAs, all in an order that the shape fixes.
+// a block's tokens, a CTA's blocks and then the CTAs, all in an order that the shape fixes.  What the CTAs leave of dB and dC is
+// 8 S bytes a token for each tile of 128, 64 or 32 channels (S up to 16, 32 and 64), written and read once: 1 byte a channel and
+// token for 16 states, 4 for 32, 16 for 64, where x has 2 in bf16 and the checkpoints S / 4.
 #include "ssm.cuh"
 
 namespace la {
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(128) ssm_join_back_kernel(const Args a) {
 
 // ---------------------------------------------------------------- all gradients of a block
 // A lane has four channels with four states each, Q lanes share the channels: what is summed over channels and what is
-// summed over states then both have few lanes to cross.  65536 x 2048 x 16, gated, in 2.45 ms: 375 instructions a token of a warp
+// summed over states then both have few lanes to cross.  65536 x 2048 x 16, gated, in 2.46 ms: 375 instructions a token of a warp
 // (32 channels), 157 of them pairs of operations, with two warps a scheduler.
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kSub = kSave;
 

@@ -6,8 +6,10 @@
 // take four), pairs of states come as they lie, and up to 16 states no sum goes over lanes.  What two tokens' scans need
 // beside B and C is formed while the two before are scanned.
 //
-// Bound by issue: 99 instructions a token of a warp, 43 of them pairs of fp32 operations, which take two slots; 196 cycles at best,
-// of which the states alone take 105.  8 x 8192 x 4096 x 16 in 1.42 ms (3.0e12 state steps a second; its bytes would take 0.32 ms).
+// Bound by a warp's latency where it walks its tokens almost alone: about 350 cycles a token.  8 x 8192 x 4096 x 16 are 1024 such
+// warps on 608 schedulers, and their 8192 tokens at 350 cycles are its 1.46 ms (2.9e12 state steps a second; its bytes would take
+// 0.32 ms).  With schedulers full a token takes 196 cycles: 99 instructions, 43 of them pairs of fp32 operations, which take two
+// slots, fill 142; the states alone, in a loop of their own, take 105.
 //
 // Time is split where the channels of all sequences are too few to fill the GPU: blocks of 2^shift tokens from each sequence's start.
 // A first launch leaves what each block but the last makes of a zero state, and its steps' sum; a second one goes along

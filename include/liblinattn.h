@@ -936,14 +936,17 @@ typedef struct la_ssm_decode_params {
     int32_t* status;
 } la_ssm_decode_params;
 
-/* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode: no two sequences of one slot).  A sequence
+/* ssm_decode -- one ssm_fwd step per sequence against a state pool (as gdn_decode: no two sequences of one slot), batch
+ * invariant; an fp32 pool takes the very states that ssm_fwd gives a sequence that it does not split.  A sequence
  * of a bad slot leaves its y as it was.  y may be x, dt or z itself, as in ssm_fwd. */
 la_status ssm_decode(const la_ssm_decode_params* p, void* stream);
 
 /* Rows of ssm_fwd's checkpoints buffer: T / 16 + N (0 for invalid arguments). */
 size_t la_ssm_checkpoint_rows(int64_t T, int32_t N);
 
-/* Bytes of device workspace that ssm_fwd and ssm_bwd need (0 for invalid arguments, and where none is needed). */
+/* Bytes of device workspace that ssm_fwd and ssm_bwd need (0 for invalid arguments, and where none is needed).  Beside the
+ * checkpoints (D S / 4 bytes a token, also in the workspace where they are not given) the backward's holds what is left of dB and
+ * dC to sum: about D bytes a token for S up to 16, 4 D up to 32, 16 D up to 64 (4.3 GB for 65536 tokens of 4096 x 64). */
 size_t la_ssm_fwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int32_t G, int32_t time_block);
 size_t la_ssm_bwd_workspace_bytes(int64_t T, int32_t N, int32_t D, int32_t S, int32_t G, int32_t checkpoints_given);
 
