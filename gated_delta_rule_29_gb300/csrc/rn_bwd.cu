@@ -11,8 +11,11 @@ template <typename R, int kVec, int kElements>
 constexpr int resident() { return kElements > 16 ? 1 : kVec == 1 ? (kElements > 8 ? 2 : 3) : kElements > 8 ? (sizeof(R) == 4 ? 1 : 2) : sizeof(R) == 4 ? 2 : 3; }
 constexpr int kMostResident = 3;
 
-// The weight gradient is summed in registers over a warp's rows, then over the CTA's groups, then by a second launch over
-// the CTAs, in an order fixed by the shape.
+// The weight gradient is summed in registers over kRows of a warp's rows at a time, those sums in shared memory (each word by one
+// thread alone), then over the CTA's groups, then by a second launch over the CTAs, in an order fixed by the shape.  One running sum
+// over a warp's rows was 435 units of 2^-24 off over 262144 equal rows (16-bit stream, 65536 x 4096: 325 us, now 328).
+constexpr int kRows = 64;
+
 template <typename X, typename R, int kVec, int NV, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>())) rn_bwd_kernel(const Args a) {
     constexpr int P = NV * kVec / 2;
@@ -36,55 +39,57 @@ __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>()))
     constexpr bool kKeep = NV * kVec <= 16;
     float2 w[kKeep ? P : 1], dw[P];  // the weights are kept where a lane holds few elements
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        if (kKeep) w[j] = weight_pair<kVec, NV>(a, pl, j);
-        dw[j] = both(0.f);
-    }
+    for (int j = 0; j < (kKeep ? P : 0); ++j) w[j] = weight_pair<kVec, NV>(a, pl, j);
     auto weight = [&](int j) { return kKeep ? w[j] : weight_pair<kVec, NV>(a, pl, j); };
-    for (int64_t n = 0; n < rounds; ++n, t += step) {
-        const bool live = t < a.T;
-        if (kAhead) {
+    auto each = [&](auto f) {  // f(word of this thread's column in sums, its place in dw)
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                s[k] = next_s[k];
-                dy[k] = next_dy[k];
-                dr[k] = next_dr[k];
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (pl.column(k) + i < a.V) f(sums[g * a.V + pl.column(k) + i], k * kVec + i);
+    };
+    each([](float& word, int) { word = 0.f; });
+    for (int64_t n = 0; n < rounds;) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) dw[j] = both(0.f);
+        for (const int64_t end = min(rounds, n + kRows); n < end; ++n, t += step) {
+            const bool live = t < a.T;
+            if (kAhead) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    s[k] = next_s[k];
+                    dy[k] = next_dy[k];
+                    dr[k] = next_dr[k];
+                }
+                load(next_s, next_dy, next_dr, t + step);
+            } else {
+                load(s, dy, dr, t);
             }
-            load(next_s, next_dy, next_dr, t + step);
-        } else {
-            load(s, dy, dr, t);
-        }
-        float2 sq = both(0.f), sd = both(0.f);
+            float2 sq = both(0.f), sd = both(0.f);
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const float2 v = pair_of<R, kVec, NV>(s, j);
-            sq = fma2(v, v, sq);
-            sd = fma2(mul2(pair_of<X, kVec, NV>(dy, j), weight(j)), v, sd);
-        }
-        float sum = sq.x + sq.y, dot = sd.x + sd.y;
-        row_reduce<false>(sum, dot, a.warps, red, static_cast<int>(n));
-        const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps)), m = -(dot * inv_v * rs * rs);  // mean(dn n) r, what s is taken off with
-        if (!live) continue;  // a warp has one row
+            for (int j = 0; j < P; ++j) {
+                const float2 v = pair_of<R, kVec, NV>(s, j);
+                sq = fma2(v, v, sq);
+                sd = fma2(mul2(pair_of<X, kVec, NV>(dy, j), weight(j)), v, sd);
+            }
+            float sum = sq.x + sq.y, dot = sd.x + sd.y;
+            row_reduce<false>(sum, dot, a.warps, red, static_cast<int>(n));
+            const float rs = inv_sqrt(fmaf(sum, inv_v, a.eps)), m = -(dot * inv_v * rs * rs);  // mean(dn n) r, what s is taken off with
+            if (!live) continue;  // a warp has one row
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const float2 v = pair_of<R, kVec, NV>(s, j), d = pair_of<X, kVec, NV>(dy, j);
-            dw[j] = fma2(d, mul2(v, both(rs)), dw[j]);
-            float2 o = mul2(both(rs), fma2(v, both(m), mul2(d, weight(j))));
-            if (a.dres) o = add2(o, pair_of<R, kVec, NV>(dr, j));
-            set_pair<X, kVec, NV>(dy, j, o);
-            set_pair<R, kVec, NV>(s, j, o);
+            for (int j = 0; j < P; ++j) {
+                const float2 v = pair_of<R, kVec, NV>(s, j), d = pair_of<X, kVec, NV>(dy, j);
+                dw[j] = fma2(d, mul2(v, both(rs)), dw[j]);
+                float2 o = mul2(both(rs), fma2(v, both(m), mul2(d, weight(j))));
+                if (a.dres) o = add2(o, pair_of<R, kVec, NV>(dr, j));
+                set_pair<X, kVec, NV>(dy, j, o);
+                set_pair<R, kVec, NV>(s, j, o);
+            }
+            if (a.y) store_row<X, kVec, NV>(a.y, t * a.y_st, dy, pl, a.V);
+            if (a.ds) store_row<R, kVec, NV>(a.ds, t * a.ds_st, s, pl, a.V);
         }
-        if (a.y) store_row<X, kVec, NV>(a.y, t * a.y_st, dy, pl, a.V);
-        if (a.ds) store_row<R, kVec, NV>(a.ds, t * a.ds_st, s, pl, a.V);
+        each([&](float& word, int e) { word += e % 2 ? dw[e / 2].y : dw[e / 2].x; });
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = pl.column(k) + i;
-            const int e = k * kVec + i;
-            if (c < a.V) sums[g * a.V + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
-        }
     __syncthreads();
     for (int c = threadIdx.x; c < a.V; c += blockDim.x) {
         float s = 0.f;
