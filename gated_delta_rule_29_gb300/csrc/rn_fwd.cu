@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>()))
         load_row<X, kVec, NV>(to_x, a.x, t * a.x_st, t < a.T, pl, a.V);
         if (a.res) load_row<R, kVec, NV>(to_r, a.res, t * a.res_st, t < a.T, pl, a.V);
     };
-    // the next row is on its way while this one is worked on, where a lane holds few elements (65536 x 4096 to 8 bits: 342 us,
-    // 446 without; a floor of 281)
+    // the next row is on its way while this one is worked on, where a lane holds few elements (65536 x 4096 to 8 bits: 349 us,
+    // 30 % more without; a floor of 281)
     constexpr bool kAhead = kVec > 1 && NV * kVec <= 16;
     int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
     if (kAhead) load(next_x, next_r, t);
@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(kMaxThreads, (resident<R, kVec, NV * kVec>()))
             continue;
         }
         // y / scale as s w times (r / scale): a block's largest |y| is its largest |s w| times r.  The factor is 448 r / 2^-100 at
-        // most, within the range up to r = 2^19; beyond (rows of 2e-6 and less, padding, under a small eps) s w takes r first.
+        // most, within the range up to r = 2^19; beyond (rows of 2e-6 and less, padding, under a small eps) s w takes r first
+        // (65536 x 4096 in blocks of 32: 343 us without that question, 349 with it, by block 361 and 366, by row 337 and 340; as a
+        // second copy of the code below the same, but odd rows 201 -> 210).
         if (rs > 0x1p19f) {
 #pragma unroll
             for (int j = 0; j < P; ++j) s[j] = mul2(s[j], both(rs));
