@@ -193,10 +193,11 @@ la_status dispatch(Args& a, int32_t xd, int32_t rd, bool wide, cudaStream_t s) {
     return rd == LA_DTYPE_F32 ? by_row<Launch, bf16, float>(a, wide, s) : by_row<Launch, bf16, bf16>(a, wide, s);
 }
 
-// Whether rows of V elements of `size` bytes take accesses of kVec elements, of at most 16 bytes each.
-inline bool wide_rows(const void* p, int64_t st, int64_t T, int64_t size, int vec) {
+// Whether rows of V elements of `size` bytes take accesses of kVec elements, of at most 16 bytes each.  A single row asks for its
+// stride too: wide rows sum in another order, and a row alone has the bits that it has among others.
+inline bool wide_rows(const void* p, int64_t st, int64_t size, int vec) {
     const int64_t bytes = std::min<int64_t>(16, vec * size);
-    return !p || (aligned_to(p, bytes) && (T <= 1 || st * size % bytes == 0));
+    return !p || (aligned_to(p, bytes) && st * size % bytes == 0);
 }
 
 inline la_status check(int64_t T, int32_t V, int32_t xd, int32_t rd, int32_t wd, float eps, const void* w) {

@@ -186,8 +186,8 @@ la_status rn_bwd(const la_rn_bwd_params* p, void* stream) {
     a.y = p->dx; a.y_st = p->dx_stride_t; a.ds = p->ds; a.ds_st = p->ds_stride_t;
     a.pw = static_cast<float*>(p->workspace);
     const int vec = 16 / xs;
-    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, rs, vec) && wide_rows(a.dy, a.dy_st, a.T, xs, vec) && wide_rows(a.dres, a.dres_st, a.T, rs, vec) &&
-                      wide_rows(a.y, a.y_st, a.T, xs, vec) && wide_rows(a.ds, a.ds_st, a.T, rs, vec);
+    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, rs, vec) && wide_rows(a.dy, a.dy_st, xs, vec) && wide_rows(a.dres, a.dres_st, rs, vec) &&
+                      wide_rows(a.y, a.y_st, xs, vec) && wide_rows(a.ds, a.ds_st, rs, vec);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p->T > 0 && (st = dispatch<Launch>(a, p->x_dtype, p->s_dtype, wide, s)) != LA_OK) return st;
     rn_sum_kernel<<<static_cast<unsigned>((a.V + 31) / 32), 1024, 0, s>>>(a.pw, a.ctas, a.V, p->d_weight, a.w_bf16);

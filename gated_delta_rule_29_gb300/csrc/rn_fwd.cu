@@ -239,8 +239,8 @@ la_status rn_fwd(const la_rn_fwd_params* p, void* stream) {
     a.y = p->y; a.y_st = p->y_stride_t; a.out = p->residual ? p->residual_out : nullptr; a.out_st = p->residual_out_stride_t;
     a.scales = p->scales;
     const int vec = 16 / static_cast<int>(xs);
-    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, a.T, xs, vec) && wide_rows(a.res, a.res_st, a.T, ss, vec) &&
-                      wide_rows(a.out, a.out_st, a.T, ss, vec) && wide_rows(a.y, a.y_st, a.T, ys, vec);
+    const bool wide = a.V % vec == 0 && wide_rows(a.x, a.x_st, xs, vec) && wide_rows(a.res, a.res_st, ss, vec) &&
+                      wide_rows(a.out, a.out_st, ss, vec) && wide_rows(a.y, a.y_st, ys, vec);
     return dispatch<Launch>(a, p->x_dtype, rd, wide, static_cast<cudaStream_t>(stream));
 }
 

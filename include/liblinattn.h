@@ -978,7 +978,8 @@ typedef struct la_rn_fwd_params {
  *
  * In 8 bits y is e4m3(y / scale) with, m being a block's largest |y| and at least
  * 2^-100, scale = m / 448, or for LA_QUANT_MX the least power of two with m <= 448
- * scale.  A block whose largest value is not finite has a scale of NaN.
+ * scale.  A block whose largest value is not finite has a scale of NaN.  A row's bits do not depend on the rows beside it
+ * (rows whose V, addresses and strides allow accesses of 16 bytes sum in another order than others).
  * residual_out may be residual or x itself, and y may be x, or residual where that is not residual_out (same address,
  * stride and type).  Results share no memory with an input or each other otherwise (LA_ERR_INVALID_ARG).
  */
